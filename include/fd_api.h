@@ -163,7 +163,7 @@ typedef struct {
     int scratch_in_stage; /* 1: the item epilogue's scratch lives in the item's
                              last pipeline stage (16-bit K/V, where that makes
                              room for another stage); 0: a region of its own */
-    int reserved[2];
+    int reserved[2];      /* 0; fd_plan_diff: marks the plan and its output type  */
 } fd_plan_t;
 
 /* Plan a decode call [P1 §2.1 step 1; P2 进阶突破; P3 §6.3, §8.2].
@@ -401,6 +401,152 @@ fd_status fd_decode_paged_staged(const fd_plan_t *plan, const void *dev_in, cons
                                  void *dev_out, void *host_out, void *workspace, size_t workspace_bytes,
                                  int32_t *status_dev, void *stream);
 fd_status fd_host_copy_out(const fd_plan_t *plan, const void *dev_out, void *host_out, void *stream);
+
+/* New tokens on their way into the cache in one pass: RMS norm of every query
+ * and key head, rotary embedding, and the write of K and V into the pools.
+ * tokens (T) per sequence, 1 or many: token i of sequence b goes to cache slot
+ * seq_lens[b] + i.
+ *   y = x * rsqrt(mean(x^2) + eps) * weight over the D elements of a head, in
+ *   fp32; then pairs (x1, x2) of the first rotary_dim elements become
+ *   ((x1*cos) - (x2*sin), (x2*cos) + (x1*sin)); then one rounding (RNE) to
+ *   q_dtype, the cache's type, or E4M3 codes of y / scale[page, kvh].  V is
+ *   not normed or rotated. */
+typedef struct {
+    int tokens;              /* T >= 1                                            */
+    const void *q;           /* device [B, T, Hq, D] q_dtype, or NULL (K/V only)  */
+    const void *k_new;       /* device [B, T, Hkv, D] q_dtype                     */
+    const void *v_new;
+    void *q_out;             /* device [B, T, Hq, D] q_dtype: q itself (same
+                                stride) or memory no other argument covers; NULL
+                                exactly when q is                                 */
+    long long q_stride;      /* elements from one token's first head to the next
+                                token's (b, i) -> (b*T + i): heads are contiguous,
+                                tokens may be a slice of wider rows (a fused QKV
+                                projection); multiples of 8, at least heads * D   */
+    long long k_stride, v_stride, q_out_stride;
+    const void *q_weight;    /* device [D], or NULL: q is not normed              */
+    const void *k_weight;    /* device [D], or NULL: k is not normed              */
+    fd_dtype weight_dtype;   /* of both weights: q_dtype or FD_F32                */
+    float eps;               /* > 0, finite                                       */
+    const float *rotary_cos; /* device fp32 [max_pos, rotary_dim / 2], or NULL
+                                (both): no rotation                               */
+    const float *rotary_sin;
+    int rotary_dim;          /* even, <= D                                        */
+    int max_pos;
+    int interleaved;         /* 0: pairs (i, i + rotary_dim/2); 1: (2i, 2i+1)     */
+    const int32_t *positions;/* device [B]: rotary position of token 0 of each
+                                sequence (token i: + i), or NULL: seq_lens.  They
+                                differ once tokens were evicted from the cache    */
+    const int32_t *new_lens; /* device [B]: the sequence's tokens in this call,
+                                0..T (a padded batch), or NULL: T each.  Tokens
+                                beyond are not read and their q_out is not written */
+} fd_norm_append;
+
+/*   problem        B, Hq, Hkv, D, page_size, max_blocks_per_seq, num_pages and
+ *                  the types; k/v pools, scales, block_table, seq_lens as in
+ *                  fd_append_kv (pools 16-byte aligned)
+ * Every pointer of a row of D elements is 16-byte aligned.  Device errors: a
+ * target page out of range sets FD_DEV_BAD_PAGE and the token's K and V are
+ * not written (its q_out is); a rotary position outside [0, max_pos), with
+ * rotary_cos given, sets FD_DEV_CAPACITY and the token is skipped; so does a
+ * new_lens[b] outside [0, T], and the sequence is skipped.  No two sequences'
+ * target slots may coincide.  seq_lens is not advanced. */
+fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *args, void *k_pages,
+                            void *v_pages, const float *k_scale, const float *v_scale,
+                            const int32_t *block_table, const int32_t *seq_lens,
+                            int32_t *status_dev, void *stream);
+
+/* fd_decode_paged that also keeps count of the attention every cached token
+ * received, per KV head:
+ *   weights_out[b][kvh][t] = weights[b][kvh][t] + sum exp(s_r(t) - lse_r)
+ * for t in [0, seq_lens[b]), summed over the query rows r that read the KV
+ * head (the Hq / Hkv heads of its group, and the q_len tokens of a plan with
+ * several query tokens, each within its causal limit).
+ *   lse               as fd_decode_paged; may be NULL
+ *   weights           device fp32 [kv rows, Hkv, weights_stride], or NULL
+ *                     (zeros: weights_out is then this step's weights alone)
+ *   weights_out       the same shape: weights itself (in place) or disjoint
+ *                     from it; entries t >= seq_lens[b] are not written
+ *   weights_stride    entries per (row, KV head), >= every length (a longer
+ *                     row sets FD_DEV_CAPACITY; its first weights_stride
+ *                     tokens are counted)
+ *   weights_workspace device, 256-byte aligned, at least the bytes that
+ *                     fd_decode_weights_workspace gives for the plan (the
+ *                     scores of every live token up to the plan's capacity,
+ *                     and lse); need not be zeroed; one per call in flight
+ *   other arguments as fd_decode_paged.
+ * After a call that set an FD_DEV_* bit, weights_out of the rows concerned is
+ * unspecified.  Not for shared_kv plans (FD_ERR_UNSUPPORTED). */
+fd_status fd_decode_weights_workspace(const fd_plan_t *plan, size_t *bytes);
+fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const void *k_pages,
+                                  const void *v_pages, const float *k_scale, const float *v_scale,
+                                  const int32_t *block_table, const int32_t *seq_lens, void *out,
+                                  float *lse, const float *weights, float *weights_out,
+                                  int weights_stride, void *workspace, size_t workspace_bytes,
+                                  void *weights_workspace, size_t weights_workspace_bytes,
+                                  int32_t *status_dev, void *stream);
+
+/* Cut every sequence back to its budget of cached tokens by accumulated
+ * attention weight.  With L = seq_lens[b]: L <= budget keeps all; otherwise
+ * every KV head keeps the first `sinks` tokens, the last `recent` tokens and,
+ * of those between, the budget - sinks - recent with the largest weights
+ * (equal weights: the lowest index; -0 equals +0; NaN is smallest).  What is
+ * kept moves to slots [0, min(L, budget)) in its order, K, V and weights.
+ * Rotated keys keep their rotation, so later tokens must be rotated at their
+ * true positions (fd_norm_append.positions).
+ *   problem           Hkv, D, page_size, ..., kv_dtype (Hq is not used)
+ *   weights           device fp32 [B, Hkv, weights_stride]
+ *   weights_out       the kept weights, then zeros up to L (entries beyond L
+ *                     are not written): weights itself, disjoint, or NULL
+ *   dst_table         device int32 [B, max_blocks_per_seq]: the pages that
+ *                     receive the rows, or NULL: the sequence's own, in place.
+ *                     Given, it must name no page that block_table's live
+ *                     entries name (e.g. fresh pages where others still hold
+ *                     the old ones, which are left as they were)
+ *   new_lens          out: device int32 [B], min(L, budget); not seq_lens
+ *   kept              out: device int32 [B, Hkv, budget], the index in the old
+ *                     order of every kept token, -1 past the new length
+ * In place, no page that changes may belong to another sequence.  E4M3 codes
+ * that move to a page with another scale become
+ * e4m3_rne_satfinite(code * scale_from / scale_to), multiplied and divided in
+ * fp32; the scales are not changed.
+ * A length outside [0, min(weights_stride, max_blocks_per_seq * page_size)]
+ * sets FD_DEV_CAPACITY: the sequence is left as it was, new_lens[b] =
+ * seq_lens[b], kept = -1.  A page out of range sets FD_DEV_BAD_PAGE and the
+ * row is not copied.  0 <= sinks, recent; sinks + recent <= budget; budget
+ * <= max_blocks_per_seq * page_size. */
+fd_status fd_evict_kv(const fd_problem *problem, void *k_pages, void *v_pages, const float *k_scale,
+                      const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                      const float *weights, float *weights_out, int weights_stride, int budget,
+                      int sinks, int recent, const int32_t *dst_table, int32_t *new_lens,
+                      int32_t *kept, int32_t *status_dev, void *stream);
+
+/* Differential attention over the paged cache: head h has two queries of
+ * width d = D / 2, the cache two keys of width d and a value of width D:
+ *   out_h = softmax(q1 k1^T / sqrt(d)) V - lambda_h softmax(q2 k2^T / sqrt(d)) V
+ * then, with norm_weight, out * rsqrt(mean(out^2) + eps) * norm_weight over
+ * the D elements, and in any case times out_scale.
+ * fd_plan_diff plans it (arguments as fd_plan): problem->Hq counts
+ * differential heads and problem->D = 2 d; q is [B, Hq, D] with q1 in the
+ * first half of a head and q2 in the second, K pages hold [k1 | k2], the head
+ * groups are as for fd_decode_paged, and so is q_len.  No shared_kv.  The
+ * plan is only for fd_decode_paged_diff (its problem field holds the doubled
+ * heads the kernel works on), and no other plan is for it.
+ *   lambda        device fp32 [Hq]
+ *   norm_weight   device [D] in norm_weight_dtype (q_dtype or FD_F32), or NULL
+ *   eps           > 0, finite, where norm_weight is given
+ *   out           device [B, (q_len,) Hq, D] in problem->out_dtype
+ *   lse           device fp32 [B, (q_len,) Hq, 2], or NULL: of both maps
+ *   other arguments as fd_decode_paged.  An empty sequence gives out = 0. */
+fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host,
+                       const fd_plan_options *options, fd_plan_t *plan);
+fd_status fd_decode_paged_diff(const fd_plan_t *plan, const void *q, const void *k_pages,
+                               const void *v_pages, const float *k_scale, const float *v_scale,
+                               const int32_t *block_table, const int32_t *seq_lens,
+                               const float *lambda, const void *norm_weight,
+                               fd_dtype norm_weight_dtype, float eps, float out_scale, void *out,
+                               float *lse, void *workspace, size_t workspace_bytes,
+                               int32_t *status_dev, void *stream);
 
 /* Map a device status word to a status code (FD_OK when zero). */
 fd_status fd_status_from_device(int32_t status_word);

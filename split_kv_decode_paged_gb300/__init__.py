@@ -14,9 +14,12 @@ import torch
 from . import _lib
 from ._lib import (FD_BF16, FD_E4M3, FD_F16, FD_F32, FdError, fd_append_kv, fd_decode_paged, fd_merge_states,
                    fd_plan, fd_status_from_device, fd_status_string, make_problem)
+from .cache_ops import append_kv_norm, evict_kv
+from .diff import DiffDecoder
 
 __all__ = ["PagedDecoder", "HostStep", "HostPipeline", "fd_plan", "fd_decode_paged", "fd_merge_states", "fd_append_kv", "fd_status_string",
-           "fd_status_from_device", "make_problem", "FdError", "append_kv", "merge_states"]
+           "fd_status_from_device", "make_problem", "FdError", "append_kv", "merge_states", "append_kv_norm", "evict_kv",
+           "DiffDecoder"]
 
 
 class PagedDecoder:
@@ -24,15 +27,21 @@ class PagedDecoder:
 
     The plan is made once from host lengths and reused while every device
     length stays within plan.capacity_tokens (pass max_seq_len to reserve
-    room for growth).  Calls on one decoder must not overlap on the GPU."""
+    room for growth).  Calls on one decoder must not overlap on the GPU.
+    track_weights=True adds the workspace of decode_weights (four bytes per
+    token of capacity and query head)."""
 
-    def __init__(self, problem, seq_lens_host, device="cuda", **plan_opts):
+    def __init__(self, problem, seq_lens_host, device="cuda", track_weights=False, **plan_opts):
         self.problem = problem
         self.plan = fd_plan(problem, seq_lens_host, **plan_opts)
         self.device = torch.device(device)
         nbytes = max(256, int(self.plan.workspace_bytes))
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.weights_workspace = None
+        if track_weights:
+            self.weights_workspace = torch.empty(_lib.fd_decode_weights_workspace(self.plan), dtype=torch.uint8,
+                                                 device=self.device)
 
     @classmethod
     def for_pools(cls, q, k_pages, v_pages, block_table, seq_lens_host, out_dtype=None, **plan_opts):
@@ -61,6 +70,28 @@ class PagedDecoder:
         fd_decode_paged(self.plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
                         self.workspace, self.status, stream)
         return out, lse
+
+    def decode_weights(self, q, k_pages, v_pages, block_table, seq_lens, weights, weights_out=None, k_scale=None,
+                       v_scale=None, out=None, lse=None, want_lse=True, stream=None):
+        """The decode call that also adds to weights (fp32 [B, Hkv, N], N >=
+        every length) the attention weight that each cached token received,
+        summed over the query heads (and query tokens) of its KV head; what
+        evict_kv goes by.  weights_out None: in place; weights None with
+        weights_out given: this step's weights alone.  Needs
+        track_weights=True.  Returns (out, lse, weights_out)."""
+        if self.weights_workspace is None:
+            raise ValueError("decode_weights: make the decoder with track_weights=True")
+        p, plan = self.problem, self.plan
+        lead = (p.B,) if plan.q_len <= 1 else (p.B, plan.q_len)
+        if weights_out is None:
+            weights_out = weights
+        if out is None:
+            out = _lib.empty_on(lead + (p.Hq, p.D), _lib.FD_TO_TORCH[p.out_dtype], self.device, stream)
+        if lse is None and want_lse:
+            lse = _lib.empty_on(lead + (p.Hq,), torch.float32, self.device, stream)
+        _lib.fd_decode_paged_weights(plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
+                                     weights, weights_out, self.workspace, self.weights_workspace, self.status, stream)
+        return out, lse, weights_out
 
     def host_step(self):
         """Pinned host and device blocks for step_host (see HostStep)."""

@@ -3,7 +3,8 @@
 Each function keeps the name of the C entry point it calls (fd_plan,
 fd_decode_paged, fd_decode_paged_ex, fd_decode_paged_host, fd_host_copy_in,
 fd_decode_paged_staged, fd_host_copy_out, fd_merge_states,
-fd_merge_two, fd_append_kv, fd_append_kv_rotary, ...).  Tensors are passed by
+fd_merge_two, fd_append_kv, fd_append_kv_rotary, fd_append_kv_norm,
+fd_decode_paged_weights, fd_evict_kv, fd_plan_diff, fd_decode_paged_diff, ...).  Tensors are passed by
 data_ptr(); the stream is torch's current CUDA stream unless given.  No
 computation happens here and there is no fallback: if libfd.so is missing or
 fails to load, every call raises.
@@ -74,6 +75,16 @@ class FdPlan(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_ if n not in ("problem", "reserved")}
 
 
+class FdNormAppend(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p),
+                ("v_new", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_longlong),
+                ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong), ("q_out_stride", ctypes.c_longlong),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("rotary_cos", ctypes.c_void_p), ("rotary_sin", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int), ("max_pos", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)]
+
+
 class FdHostIoLayout(ctypes.Structure):
     _fields_ = [("q_offset", ctypes.c_size_t), ("block_table_offset", ctypes.c_size_t),
                 ("seq_lens_offset", ctypes.c_size_t), ("in_bytes", ctypes.c_size_t),
@@ -117,6 +128,19 @@ def load(path: str = LIB_PATH):
     L.fd_decode_paged_staged.argtypes = [ctypes.POINTER(FdPlan), P, P, P, P, P, P, P, P, S, P, P]
     L.fd_host_copy_out.restype = I
     L.fd_host_copy_out.argtypes = [ctypes.POINTER(FdPlan), P, P, P]
+    L.fd_append_kv_norm.restype = I
+    L.fd_append_kv_norm.argtypes = [ctypes.POINTER(FdProblem), ctypes.POINTER(FdNormAppend), P, P, P, P, P, P, P, P]
+    L.fd_decode_weights_workspace.restype = I
+    L.fd_decode_weights_workspace.argtypes = [ctypes.POINTER(FdPlan), ctypes.POINTER(S)]
+    L.fd_decode_paged_weights.restype = I
+    L.fd_decode_paged_weights.argtypes = [ctypes.POINTER(FdPlan), P, P, P, P, P, P, P, P, P, P, P, I, P, S, P, S, P, P]
+    L.fd_evict_kv.restype = I
+    L.fd_evict_kv.argtypes = [ctypes.POINTER(FdProblem), P, P, P, P, P, P, P, P, I, I, I, I, P, P, P, P, P]
+    L.fd_plan_diff.restype = I
+    L.fd_plan_diff.argtypes = [ctypes.POINTER(FdProblem), P, ctypes.POINTER(FdPlanOptions), ctypes.POINTER(FdPlan)]
+    L.fd_decode_paged_diff.restype = I
+    L.fd_decode_paged_diff.argtypes = [ctypes.POINTER(FdPlan), P, P, P, P, P, P, P, P, P, I, ctypes.c_float,
+                                       ctypes.c_float, P, P, P, S, P, P]
     L.fd_status_string.restype = ctypes.c_char_p
     L.fd_status_string.argtypes = [I]
     L.fd_status_from_device.restype = I
@@ -171,6 +195,37 @@ class _Args:
             self._fail(name, f"must hold at least {min_bytes} bytes, got {t.nbytes}")
         self.placed.append((name, t, host))
 
+    def rows(self, name, t, dtype, lead, heads, D):
+        """[*lead, heads, D] whose heads are contiguous and whose tokens (lead
+        flattened) lie at one stride, e.g. a slice of a fused projection;
+        returns that stride in elements."""
+        if not isinstance(t, torch.Tensor):
+            self._fail(name, "is required" if t is None else f"must be a torch.Tensor, got {type(t).__name__}")
+        if t.dtype != dtype:
+            self._fail(name, f"must have dtype {dtype}, got {t.dtype}")
+        if t.shape != lead + (heads, D):
+            self._fail(name, f"must have shape {lead + (heads, D)}, got {tuple(t.shape)}")
+        self.placed.append((name, t, False))
+        if t.is_contiguous():
+            return heads * D
+        st = t.stride()
+        if st[-1] != 1 or (heads > 1 and st[-2] != D):
+            self._fail(name, "must have contiguous heads")
+        token = None  # (size, stride) of the flattened leading dimensions
+        for n, s in zip(reversed(lead), reversed(st[:-2])):
+            if n == 1:
+                continue
+            if token is None:
+                token = (n, s)
+            elif s == token[0] * token[1]:
+                token = (token[0] * n, token[1])
+            else:
+                self._fail(name, "must have its tokens at one stride")
+        stride = heads * D if token is None else token[1]
+        if stride < heads * D or stride % 8:
+            self._fail(name, f"must have a token stride that is a multiple of 8 and at least {heads * D} elements")
+        return stride
+
     def absent(self, name, t, why):
         if t is not None:
             self._fail(name, f"must be None ({why})")
@@ -188,6 +243,32 @@ class _Args:
                 index, first = t.get_device(), t
             elif t.get_device() != index:
                 self._fail(name, f"is on {t.device}, other arguments on {first.device}")
+        return index
+
+
+def _launch(entry, index, stream, fn, *args):
+    """Call fn(*args, stream) with the tensors' device (its index) current;
+    stream None: that device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(index)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc != FD_OK:
+        raise FdError(rc, entry)
+
+
+def empty_on(shape, dtype, device, stream=None):
+    """torch.empty from the allocator's pool of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _rows_shape(plan, t, tail):
@@ -244,13 +325,9 @@ def make_problem(B, Hq, Hkv, D, page_size, max_blocks_per_seq, num_pages, q_dtyp
                      q if out_dtype is None else fd_dtype(out_dtype))
 
 
-def fd_plan(problem: FdProblem, seq_lens_host, num_splits=0, num_sms=0, fuse_merge=1, max_seq_len=0,
-            ctas_per_sm=0, split_margin_pct=0, tile_tokens=0, shared_kv=0, timeout_us=0, debug_stall_us=0,
-            debug_stall_role=0, q_len=0) -> FdPlan:
-    """Plan a decode call; seq_lens_host is a host int32 tensor/sequence.
-    timeout_us bounds every device-side wait (0 = 2 s); debug_stall_us and
-    debug_stall_role are the test hook of the timeout path (0 = off); q_len
-    > 1 plans q_len causal query tokens per sequence (q [B, q_len, Hq, D])."""
+def _plan(entry, fn, problem, seq_lens_host, num_splits=0, num_sms=0, fuse_merge=1, max_seq_len=0,
+          ctas_per_sm=0, split_margin_pct=0, tile_tokens=0, shared_kv=0, timeout_us=0, debug_stall_us=0,
+          debug_stall_role=0, q_len=0) -> FdPlan:
     lens = torch.as_tensor(seq_lens_host, dtype=torch.int32).cpu().contiguous()
     if lens.numel() != problem.B and not (shared_kv and lens.numel() >= 1):
         raise ValueError("seq_lens_host must have B entries")
@@ -258,11 +335,28 @@ def fd_plan(problem: FdProblem, seq_lens_host, num_splits=0, num_sms=0, fuse_mer
                          int(split_margin_pct), int(tile_tokens), int(shared_kv), int(timeout_us),
                          int(debug_stall_us), int(debug_stall_role), int(q_len))
     plan = FdPlan()
-    rc = load().fd_plan(ctypes.byref(problem), ctypes.c_void_p(lens.data_ptr()), ctypes.byref(opts),
-                        ctypes.byref(plan))
+    rc = fn(ctypes.byref(problem), ctypes.c_void_p(lens.data_ptr()), ctypes.byref(opts), ctypes.byref(plan))
     if rc != FD_OK:
-        raise FdError(rc, "fd_plan")
+        raise FdError(rc, entry)
     return plan
+
+
+def fd_plan(problem: FdProblem, seq_lens_host, num_splits=0, num_sms=0, fuse_merge=1, max_seq_len=0,
+            ctas_per_sm=0, split_margin_pct=0, tile_tokens=0, shared_kv=0, timeout_us=0, debug_stall_us=0,
+            debug_stall_role=0, q_len=0) -> FdPlan:
+    """Plan a decode call; seq_lens_host is a host int32 tensor/sequence.
+    timeout_us bounds every device-side wait (0 = 2 s); debug_stall_us and
+    debug_stall_role are the test hook of the timeout path (0 = off); q_len
+    > 1 plans q_len causal query tokens per sequence (q [B, q_len, Hq, D])."""
+    return _plan("fd_plan", load().fd_plan, problem, seq_lens_host, num_splits, num_sms, fuse_merge, max_seq_len,
+                 ctas_per_sm, split_margin_pct, tile_tokens, shared_kv, timeout_us, debug_stall_us, debug_stall_role,
+                 q_len)
+
+
+def fd_plan_diff(problem: FdProblem, seq_lens_host, **opts) -> FdPlan:
+    """Plan differential attention (options as fd_plan, no shared_kv):
+    problem.Hq counts differential heads, problem.D is both maps' width."""
+    return _plan("fd_plan_diff", load().fd_plan_diff, problem, seq_lens_host, **opts)
 
 
 def fd_decode_paged(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
@@ -454,3 +548,149 @@ def fd_host_copy_out(plan: FdPlan, dev_out, host_out, stream=None):
     rc = load().fd_host_copy_out(ctypes.byref(plan), _ptr(dev_out), _ptr(host_out), _stream(stream))
     if rc != FD_OK:
         raise FdError(rc, "fd_host_copy_out")
+
+
+def fd_append_kv_norm(problem: FdProblem, q, k_new, v_new, q_out, k_pages, v_pages, k_scale, v_scale, block_table,
+                      seq_lens, q_weight=None, k_weight=None, eps=1e-6, rotary_cos=None, rotary_sin=None,
+                      interleaved=False, positions=None, new_lens=None, status=None, stream=None):
+    """k_new/v_new [B, T, Hkv, D] or [B, Hkv, D] (T = 1), q and q_out the same
+    with Hq heads (or None); tokens may lie at a stride (see _Args.rows)."""
+    p = problem
+    a = _Args("fd_append_kv_norm")
+    act, kv = FD_TO_TORCH[p.q_dtype], FD_TO_TORCH[p.kv_dtype]
+    if not isinstance(k_new, torch.Tensor):
+        a._fail("k_new", "is required" if k_new is None else f"must be a torch.Tensor, got {type(k_new).__name__}")
+    if k_new.dim() == 4:
+        T = k_new.shape[1]
+        lead = (p.B, T)
+        if T < 1:
+            a._fail("k_new", "must hold at least one token per sequence")
+    else:
+        T, lead = 1, (p.B,)
+    n = FdNormAppend()
+    n.tokens = T
+    n.k_stride = a.rows("k_new", k_new, act, lead, p.Hkv, p.D)
+    n.v_stride = a.rows("v_new", v_new, act, lead, p.Hkv, p.D)
+    n.k_new, n.v_new = k_new.data_ptr(), v_new.data_ptr()
+    if q is None:
+        a.absent("q_out", q_out, "there is no q")
+    else:
+        n.q_stride = a.rows("q", q, act, lead, p.Hq, p.D)
+        n.q_out_stride = a.rows("q_out", q_out, act, lead, p.Hq, p.D)
+        n.q, n.q_out = q.data_ptr(), q_out.data_ptr()
+    weight = q_weight if q_weight is not None else k_weight
+    if weight is not None:
+        wt = weight.dtype if isinstance(weight, torch.Tensor) and weight.dtype == torch.float32 else act
+        a.tensor("q_weight", q_weight, wt, (p.D,), optional=True)
+        a.tensor("k_weight", k_weight, wt, (p.D,), optional=True)
+        n.q_weight, n.k_weight, n.weight_dtype = _ptr(q_weight), _ptr(k_weight), _TORCH_TO_FD[wt]
+    n.eps = eps
+    if rotary_cos is not None or rotary_sin is not None:
+        a.tensor("rotary_cos", rotary_cos, torch.float32)
+        if rotary_cos.dim() != 2:
+            a._fail("rotary_cos", f"must be 2-D [max_pos, rotary_dim / 2], got shape {tuple(rotary_cos.shape)}")
+        a.tensor("rotary_sin", rotary_sin, torch.float32, tuple(rotary_cos.shape))
+        n.max_pos, half = rotary_cos.shape
+        n.rotary_dim = 2 * half
+        n.rotary_cos, n.rotary_sin = rotary_cos.data_ptr(), rotary_sin.data_ptr()
+        n.interleaved = 1 if interleaved else 0
+    a.tensor("positions", positions, torch.int32, (p.B,), optional=True)
+    a.tensor("new_lens", new_lens, torch.int32, (p.B,), optional=True)
+    n.positions, n.new_lens = _ptr(positions), _ptr(new_lens)
+    _check_pools(a, p, kv, k_pages, v_pages, k_scale, v_scale)
+    a.tensor("block_table", block_table, torch.int32, (p.B, p.max_blocks_per_seq))
+    a.tensor("seq_lens", seq_lens, torch.int32, (p.B,))
+    a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)
+    _launch("fd_append_kv_norm", a.done(), stream, load().fd_append_kv_norm, ctypes.byref(p), ctypes.byref(n),
+            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+            _ptr(status))
+
+
+def _check_pools(a, p, kv, k_pages, v_pages, k_scale, v_scale):
+    pool = (p.num_pages, p.page_size, p.Hkv, p.D)
+    a.tensor("k_pages", k_pages, kv, pool)
+    a.tensor("v_pages", v_pages, kv, pool)
+    if p.kv_dtype == FD_E4M3:
+        a.tensor("k_scale", k_scale, torch.float32, (p.num_pages, p.Hkv))
+        a.tensor("v_scale", v_scale, torch.float32, (p.num_pages, p.Hkv))
+    else:
+        a.absent("k_scale", k_scale, "the cache is not E4M3")
+        a.absent("v_scale", v_scale, "the cache is not E4M3")
+
+
+def fd_decode_weights_workspace(plan: FdPlan) -> int:
+    """Bytes of the weights workspace of fd_decode_paged_weights for the plan."""
+    n = ctypes.c_size_t()
+    rc = load().fd_decode_weights_workspace(ctypes.byref(plan), ctypes.byref(n))
+    if rc != FD_OK:
+        raise FdError(rc, "fd_decode_weights_workspace")
+    return n.value
+
+
+def fd_decode_paged_weights(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
+                            weights, weights_out, workspace, weights_workspace, status=None, stream=None):
+    """weights (or None: zeros) and weights_out fp32 [kv rows, Hkv, N]."""
+    a = _check_decode("fd_decode_paged_weights", plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                      out, lse, workspace, status)
+    a.tensor("weights_out", weights_out, torch.float32)
+    lead = (plan.kv_rows, plan.problem.Hkv)
+    if weights_out.dim() != 3 or weights_out.shape[:2] != lead or weights_out.shape[2] < 1:
+        a._fail("weights_out", f"must have shape {lead + ('N',)}, got {tuple(weights_out.shape)}")
+    a.tensor("weights", weights, torch.float32, tuple(weights_out.shape), optional=True)
+    a.tensor("weights_workspace", weights_workspace, None, None)
+    _launch("fd_decode_paged_weights", a.done(), stream, load().fd_decode_paged_weights, ctypes.byref(plan), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(out),
+            _ptr(lse), _ptr(weights), _ptr(weights_out), weights_out.shape[2], _ptr(workspace), workspace.nbytes,
+            _ptr(weights_workspace), weights_workspace.nbytes, _ptr(status))
+
+
+def fd_evict_kv(problem: FdProblem, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, weights_out,
+                budget, sinks, recent, new_lens, kept, dst_table=None, status=None, stream=None):
+    """weights fp32 [B, Hkv, N]; weights_out the same or None; new_lens int32
+    [B]; kept int32 [B, Hkv, budget]."""
+    p = problem
+    a = _Args("fd_evict_kv")
+    _check_pools(a, p, FD_TO_TORCH[p.kv_dtype], k_pages, v_pages, k_scale, v_scale)
+    a.tensor("block_table", block_table, torch.int32, (p.B, p.max_blocks_per_seq))
+    a.tensor("dst_table", dst_table, torch.int32, (p.B, p.max_blocks_per_seq), optional=True)
+    a.tensor("seq_lens", seq_lens, torch.int32, (p.B,))
+    a.tensor("weights", weights, torch.float32)
+    if weights.dim() != 3 or weights.shape[:2] != (p.B, p.Hkv) or weights.shape[2] < 1:
+        a._fail("weights", f"must have shape {(p.B, p.Hkv, 'N')}, got {tuple(weights.shape)}")
+    a.tensor("weights_out", weights_out, torch.float32, tuple(weights.shape), optional=True)
+    a.tensor("new_lens", new_lens, torch.int32, (p.B,))
+    a.tensor("kept", kept, torch.int32, (p.B, p.Hkv, int(budget)))
+    a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)
+    _launch("fd_evict_kv", a.done(), stream, load().fd_evict_kv, ctypes.byref(p), _ptr(k_pages), _ptr(v_pages),
+            _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(weights), _ptr(weights_out),
+            weights.shape[2], int(budget), int(sinks), int(recent), _ptr(dst_table), _ptr(new_lens), _ptr(kept),
+            _ptr(status))
+
+
+def fd_decode_paged_diff(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, lam, out, lse,
+                         workspace, norm_weight=None, eps=1e-5, out_scale=1.0, status=None, stream=None):
+    """plan from fd_plan_diff; q [B, (q_len,) Hq, D], lam fp32 [Hq], out like q
+    in the planned output type, lse fp32 [B, (q_len,) Hq, 2] or None."""
+    p = plan.problem  # its heads are the doubled ones, its rows B * q_len
+    a = _Args("fd_decode_paged_diff")
+    if plan.reserved[0] != 1:
+        raise ValueError("fd_decode_paged_diff: the plan must come from fd_plan_diff")
+    Hq, act = p.Hq // 2, FD_TO_TORCH[p.q_dtype]
+    a.tensor("q", q, act, _rows_shape(plan, q, (Hq, p.D)))
+    _check_pools(a, p, FD_TO_TORCH[p.kv_dtype], k_pages, v_pages, k_scale, v_scale)
+    a.tensor("block_table", block_table, torch.int32, (plan.kv_rows, p.max_blocks_per_seq))
+    a.tensor("seq_lens", seq_lens, torch.int32, (plan.kv_rows,))
+    a.tensor("lam", lam, torch.float32, (Hq,))
+    a.tensor("out", out, FD_TO_TORCH[plan.reserved[1]], _rows_shape(plan, out, (Hq, p.D)))
+    a.tensor("lse", lse, torch.float32, _rows_shape(plan, lse, (Hq, 2)), optional=True)
+    a.tensor("workspace", workspace, None, None, min_bytes=int(plan.workspace_bytes))
+    a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)
+    wt = FD_F32
+    if norm_weight is not None:
+        dt = norm_weight.dtype if isinstance(norm_weight, torch.Tensor) and norm_weight.dtype == torch.float32 else act
+        a.tensor("norm_weight", norm_weight, dt, (p.D,))
+        wt = _TORCH_TO_FD[dt]
+    _launch("fd_decode_paged_diff", a.done(), stream, load().fd_decode_paged_diff, ctypes.byref(plan), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(lam),
+            _ptr(norm_weight), wt, eps, out_scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.nbytes,
+            _ptr(status))

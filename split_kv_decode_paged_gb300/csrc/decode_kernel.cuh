@@ -53,6 +53,7 @@ constexpr int kCoopBlocks = 4;     // 32-row blocks from which every warp builds
 constexpr int kFlagFirst = 1;
 constexpr int kFlagLast = 2;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kPlain = 0, kScores = 1, kDiff = 2;  // MODE of a decode instance
 constexpr float kMaxSlack = 8.f;  // log2 headroom of the softmax reference maximum
 
 struct StageMeta {
@@ -424,7 +425,15 @@ __device__ __noinline__ void build_dispatch_tables_coop(const DecodeParams &p, i
 // its own causal limit; a separate instance so the one-token decode carries
 // none of it.
 // SCR: the E4M3 instance that may keep its epilogue scratch in the held stage.
-template <int KV, int D, int NT, int NC, int SUBT, bool QBF16, bool CAUSAL, bool SCR = false>
+// MODE kScores: every score (log2 units, -inf where hidden) also goes to
+// DecodeParams::scores, for the attention-weight totals (weights.cu).  MODE
+// kDiff: the decode of differential attention (diff.cu).  In both the
+// denominator sums the weights before they are rounded for P.V: their
+// results go by the lse itself (a total of weights, a difference of two
+// outputs), where a plain decode's output is a ratio in which the rounding of
+// numerator and denominator partly cancels (12 f16 bits of a weight would be
+// up to 1e-4 of a short row's lse).
+template <int KV, int D, int NT, int NC, int SUBT, bool QBF16, bool CAUSAL, bool SCR = false, int MODE = kPlain>
 __global__ void __launch_bounds__((NC + 1) * 32, 1)
     fd_split_kv_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                               const __grid_constant__ CUtensorMap tmv) {
@@ -1110,6 +1119,22 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                     sv[sub][n][1] = v01 ? (sv[sub][n][1] + s2[n][1]) * sc1 : -INFINITY;
                     sv[sub][n][2] = v10 ? (sv[sub][n][2] + s2[n][2]) * sc0 : -INFINITY;
                     sv[sub][n][3] = v11 ? (sv[sub][n][3] + s2[n][3]) * sc1 : -INFINITY;
+                    if constexpr (MODE == kScores) {
+                        // rows of the item's tokens: R = G * fold scores each
+                        const int R = p.G * p.fold;
+                        const int col = mt.hg * QROWS + n * 8 + 2 * c;
+                        const int tok = mt.t0 + r0 + g;
+                        float *to = p.scores + ((size_t)((size_t)mt.b * p.Hkv + mt.kvh) * p.cap + tok) * R + col;
+                        if (col < R) {
+                            const size_t o8 = (size_t)8 * R;
+                            if (v0) to[0] = sv[sub][n][0];
+                            if (v1) to[o8] = sv[sub][n][2];
+                            if (col + 1 < R) {
+                                if (v0) to[1] = sv[sub][n][1];
+                                if (v1) to[o8 + 1] = sv[sub][n][3];
+                            }
+                        }
+                    }
                 }
             }
 
@@ -1185,8 +1210,13 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                         const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&x1));
                         wr0 = f0.x; wr1 = f0.y; wr2 = f1.x; wr3 = f1.y;
                     }
-                    add0 += wr0 + wr2;
-                    add1 += wr1 + wr3;
+                    if constexpr (MODE == kPlain) {
+                        add0 += wr0 + wr2;
+                        add1 += wr1 + wr3;
+                    } else {
+                        add0 += p0 + p2;
+                        add1 += p1 + p3;
+                    }
                     pb[sub][n][0] = movmatrix_t(x0);
                     pb[sub][n][1] = movmatrix_t(x1);
                 }
@@ -1489,10 +1519,11 @@ cudaError_t occupancy_t(size_t smem, int *blocks) {
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, kern, DecodeShape<KV, D, NT, NC, SUBT>::THREADS, smem);
 }
 
-template <int KV, int D, int NT, int NC, int SUBT, bool QBF16, bool CAUSAL = false, bool SCR = false>
+template <int KV, int D, int NT, int NC, int SUBT, bool QBF16, bool CAUSAL = false, bool SCR = false,
+          int MODE = kPlain>
 cudaError_t launch_decode_t(const DecodeParams &dp, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid,
                             size_t smem, cudaStream_t stream) {
-    auto kern = fd_split_kv_decode_kernel<KV, D, NT, NC, SUBT, QBF16, CAUSAL, SCR>;
+    auto kern = fd_split_kv_decode_kernel<KV, D, NT, NC, SUBT, QBF16, CAUSAL, SCR, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // Programmatic dependent launch: the kernel may begin its prologue while

@@ -13,12 +13,11 @@
 
 namespace fd {
 
-cudaError_t launch_decode_f16(const fd_problem &, const KernelShape &, const DecodeParams &, const CUtensorMap &,
-                              const CUtensorMap &, int, size_t, cudaStream_t);
-cudaError_t launch_decode_bf16(const fd_problem &, const KernelShape &, const DecodeParams &, const CUtensorMap &,
-                               const CUtensorMap &, int, size_t, cudaStream_t);
-cudaError_t launch_decode_e4m3(const fd_problem &, const KernelShape &, const DecodeParams &, const CUtensorMap &,
-                               const CUtensorMap &, int, size_t, cudaStream_t);
+using LaunchDecode = cudaError_t(const fd_problem &, const KernelShape &, const DecodeParams &, const CUtensorMap &,
+                                 const CUtensorMap &, int, size_t, cudaStream_t);
+LaunchDecode launch_decode_f16, launch_decode_bf16, launch_decode_e4m3;
+LaunchDecode launch_decode_scores_f16, launch_decode_scores_bf16, launch_decode_scores_e4m3;  // scores out (weights.cu)
+LaunchDecode launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3;        // diff.cu
 cudaError_t decode_occupancy_f16(const fd_problem &, const KernelShape &, size_t, int *);
 cudaError_t decode_occupancy_bf16(const fd_problem &, const KernelShape &, size_t, int *);
 cudaError_t decode_occupancy_e4m3(const fd_problem &, const KernelShape &, size_t, int *);
@@ -68,14 +67,19 @@ cudaError_t decode_occupancy(const fd_problem &p, const KernelShape &ks, size_t 
     }
 }
 
-cudaError_t launch_decode(const fd_problem &p, const KernelShape &ks, const DecodeParams &dp, const CUtensorMap &tmk,
-                          const CUtensorMap &tmv, int grid, size_t smem, cudaStream_t stream) {
-    switch (p.kv_dtype) {
-    case FD_F16: return launch_decode_f16(p, ks, dp, tmk, tmv, grid, smem, stream);
-    case FD_BF16: return launch_decode_bf16(p, ks, dp, tmk, tmv, grid, smem, stream);
-    default: return launch_decode_e4m3(p, ks, dp, tmk, tmv, grid, smem, stream);
-    }
-}
+namespace {
+
+// Launchers of one kind of decode call, by K/V type (f16, bf16, E4M3).
+struct DecodeLaunchers {
+    LaunchDecode *f16, *bf16, *e4m3;
+    LaunchDecode *of(fd_dtype kv) const { return kv == FD_F16 ? f16 : (kv == FD_BF16 ? bf16 : e4m3); }
+};
+constexpr DecodeLaunchers kPlainDecode = {launch_decode_f16, launch_decode_bf16, launch_decode_e4m3};
+constexpr DecodeLaunchers kScoresDecode = {launch_decode_scores_f16, launch_decode_scores_bf16,
+                                           launch_decode_scores_e4m3};
+constexpr DecodeLaunchers kDiffDecode = {launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3};
+
+}  // namespace
 
 }  // namespace fd
 
@@ -84,6 +88,9 @@ using namespace fd;
 namespace {
 
 constexpr int kMaxStages = 8;
+// fd_plan_t::reserved[0]: what the plan was made for.
+constexpr int kPlanPlain = 0;
+constexpr int kPlanDiff = 1;  // fd_plan_diff; reserved[1] = fd_dtype of the output
 constexpr int kMaxQLen = 64;  // query tokens per sequence (multi-token mode)
 constexpr int kMinStages = 2;
 constexpr int kSmallGridItemTokens = 1024;  // small grids: two CTAs per SM for items up to this long
@@ -614,11 +621,21 @@ fd_status fd_plan(const fd_problem *problem, const int32_t *seq_lens_host, const
 
 namespace {
 
+// What sets a decode call apart from the plain one.
+struct DecodeMode {
+    const DecodeLaunchers *launch = &kPlainDecode;
+    int kind = kPlanPlain;     // the plan's kind the call takes
+    float *scores = nullptr;   // kScoresDecode: where the scores go
+    int score_width = 0;       // elements of q and k a score is formed over; 0 = D
+    const void *pair_q = nullptr;  // kDiffDecode: the query pairs, to be padded into the call's q
+};
+
 fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
                       const float *k_scale, const float *v_scale, const int32_t *block_table,
                       const int32_t *seq_lens, const fd_decode_extras *ex, void *out, float *lse, void *workspace,
-                      size_t workspace_bytes, int32_t *status_dev, void *stream) {
-    if (!plan) return FD_ERR_INVALID_ARG;
+                      size_t workspace_bytes, int32_t *status_dev, void *stream,
+                      const DecodeMode &mode = DecodeMode()) {
+    if (!plan || plan->reserved[0] != mode.kind) return FD_ERR_INVALID_ARG;
     const fd_problem &p = plan->problem;
     fd_status st = validate_problem(&p);
     if (st != FD_OK) return st;
@@ -697,14 +714,18 @@ fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages,
     dp.fuse_merge = plan->fuse_merge;
     dp.stages = plan->stages;
     dp.scr_in_stage = plan->scratch_in_stage;
-    dp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.D));
+    dp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)(mode.score_width > 0 ? mode.score_width : p.D)));
+    dp.scores = mode.scores;
     dp.timeout_ns = plan->timeout_us > 0 ? (uint64_t)plan->timeout_us * 1000ull : kTimeoutNs;
     dp.stall_ns = (uint64_t)plan->debug_stall_us * 1000ull;
     dp.stall_role = plan->debug_stall_role;
     dp.qn = q_len;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_decode(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
+    cudaError_t e = cudaSuccess;
+    if (mode.pair_q) e = launch_diff_expand(mode.pair_q, const_cast<void *>(q), (long long)p.B * (p.Hq / 2), p.D, s);
+    if (e != cudaSuccess) return FD_ERR_CUDA;
+    e = mode.launch->of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
     if (e != cudaSuccess) return FD_ERR_CUDA;
     if (!plan->fuse_merge && plan->num_splits > 1) {
         MergeParams mp;
@@ -951,6 +972,301 @@ fd_status fd_append_kv_rotary(const fd_problem *problem, const void *k_new, cons
         return FD_ERR_INVALID_ARG;
     return append_impl(problem, k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, rotary_cos,
                        rotary_sin, rotary_dim, max_pos, interleaved, q_inout, status_dev, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Byte layout of the weights workspace: lse, then the scores.
+struct WeightsLayout {
+    size_t scores, bytes;
+};
+
+bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
+    const fd_problem &p = plan->problem;
+    if (validate_problem(&p) != FD_OK || plan->reserved[0] != kPlanPlain || plan->kv_rows < 1 || plan->row_fold < 1 ||
+        plan->kv_rows * plan->row_fold != p.B || plan->num_splits < 1 || plan->chunk_tokens < 1)
+        return false;
+    l->scores = align256((size_t)p.B * p.Hq * sizeof(float));
+    l->bytes = l->scores + align256((size_t)p.B * p.Hq * (size_t)plan->num_splits * (size_t)plan->chunk_tokens * sizeof(float));
+    return true;
+}
+
+// Two arrays of n floats that share some but not all of their places.
+bool half_overlaps(const float *a, const float *b, size_t n) {
+    if (!a || !b || a == b) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + n * sizeof(float) && y < x + n * sizeof(float);
+}
+
+bool norm_weight_ok(const void *w, fd_dtype t, fd_dtype act) {
+    if (!w) return true;
+    return (t == FD_F32 || t == act) && aligned(w, elem_bytes(t));
+}
+
+}  // namespace
+
+extern "C" {
+
+fd_status fd_decode_weights_workspace(const fd_plan_t *plan, size_t *bytes) {
+    if (!plan || !bytes) return FD_ERR_INVALID_ARG;
+    WeightsLayout l;
+    if (!weights_layout(plan, &l)) return FD_ERR_INVALID_ARG;
+    if (plan->row_fold != std::max(1, plan->q_len)) return FD_ERR_UNSUPPORTED;  // shared_kv
+    *bytes = l.bytes;
+    return FD_OK;
+}
+
+fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
+                                  const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                  const int32_t *seq_lens, void *out, float *lse, const float *weights,
+                                  float *weights_out, int weights_stride, void *workspace, size_t workspace_bytes,
+                                  void *weights_workspace, size_t weights_workspace_bytes, int32_t *status_dev,
+                                  void *stream) {
+    size_t need = 0;
+    const fd_status st = fd_decode_weights_workspace(plan, &need);
+    if (st != FD_OK) return st;
+    if (!weights_out || !weights_workspace || weights_stride < 1) return FD_ERR_INVALID_ARG;
+    if (!aligned(weights_out, 4) || !aligned(weights, 4) || !aligned(weights_workspace, 256)) return FD_ERR_INVALID_ARG;
+    if (weights_workspace_bytes < need) return FD_ERR_WORKSPACE_TOO_SMALL;
+    WeightsLayout l;
+    weights_layout(plan, &l);
+    const fd_problem &p = plan->problem;
+    if (half_overlaps(weights, weights_out, (size_t)plan->kv_rows * p.Hkv * weights_stride)) return FD_ERR_INVALID_ARG;
+    uint8_t *ww = static_cast<uint8_t *>(weights_workspace);
+    DecodeMode mode;
+    mode.launch = &kScoresDecode;
+    mode.scores = reinterpret_cast<float *>(ww + l.scores);
+    float *use_lse = lse ? lse : reinterpret_cast<float *>(ww);
+    const fd_status r = decode_impl(plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, nullptr, out,
+                                    use_lse, workspace, workspace_bytes, status_dev, stream, mode);
+    if (r != FD_OK) return r;
+    WeightParams wp;
+    std::memset(&wp, 0, sizeof(wp));
+    wp.scores = mode.scores;
+    wp.lse = use_lse;
+    wp.in = weights;
+    wp.out = weights_out;
+    wp.seq_lens = seq_lens;
+    wp.status = status_dev;
+    wp.Bkv = plan->kv_rows;
+    wp.Hq = p.Hq;
+    wp.Hkv = p.Hkv;
+    wp.G = p.Hq / p.Hkv;
+    wp.fold = plan->row_fold;
+    wp.R = wp.G * wp.fold;
+    wp.cap = plan->num_splits * plan->chunk_tokens;
+    wp.weights_stride = weights_stride;
+    return launch_weights(wp, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *args, void *k_pages, void *v_pages,
+                            const float *k_scale, const float *v_scale, const int32_t *block_table,
+                            const int32_t *seq_lens, int32_t *status_dev, void *stream) {
+    const fd_status st = validate_problem(problem);
+    if (st != FD_OK) return st;
+    if (!args || !args->k_new || !args->v_new || !k_pages || !v_pages || !block_table || !seq_lens)
+        return FD_ERR_INVALID_ARG;
+    const fd_problem &p = *problem;
+    const fd_norm_append &a = *args;
+    const bool fp8 = p.kv_dtype == FD_E4M3;
+    if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr)) return FD_ERR_INVALID_ARG;
+    if ((a.q == nullptr) != (a.q_out == nullptr)) return FD_ERR_INVALID_ARG;
+    if (a.tokens < 1 || !(a.eps > 0.f) || !std::isfinite(a.eps)) return FD_ERR_INVALID_ARG;
+    if (!aligned(a.q, 16) || !aligned(a.q_out, 16) || !aligned(a.k_new, 16) || !aligned(a.v_new, 16) ||
+        !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(a.positions, 4) || !aligned(a.new_lens, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return FD_ERR_INVALID_ARG;
+    // token strides: 16-byte rows, no overlap of a token's heads with the next token's
+    auto stride_ok = [&](long long s, int heads) { return s % 8 == 0 && s >= (long long)heads * p.D; };
+    if ((a.q && (!stride_ok(a.q_stride, p.Hq) || !stride_ok(a.q_out_stride, p.Hq))) ||
+        !stride_ok(a.k_stride, p.Hkv) || !stride_ok(a.v_stride, p.Hkv))
+        return FD_ERR_INVALID_ARG;
+    if (!norm_weight_ok(a.q_weight, a.weight_dtype, p.q_dtype) || !norm_weight_ok(a.k_weight, a.weight_dtype, p.q_dtype))
+        return FD_ERR_INVALID_ARG;
+    if ((a.rotary_cos == nullptr) != (a.rotary_sin == nullptr)) return FD_ERR_INVALID_ARG;
+    if (a.rotary_cos && (a.max_pos < 1 || a.rotary_dim < 2 || (a.rotary_dim & 1) || a.rotary_dim > p.D ||
+                         !aligned(a.rotary_cos, 4) || !aligned(a.rotary_sin, 4)))
+        return FD_ERR_INVALID_ARG;
+    NormAppendParams np;
+    std::memset(&np, 0, sizeof(np));
+    np.q = a.q;
+    np.k = a.k_new;
+    np.v = a.v_new;
+    np.q_out = a.q_out;
+    np.q_stride = a.q_stride;
+    np.k_stride = a.k_stride;
+    np.v_stride = a.v_stride;
+    np.q_out_stride = a.q_out_stride;
+    np.qw = a.q_weight;
+    np.kw = a.k_weight;
+    np.w_f32 = a.weight_dtype == FD_F32;
+    np.eps = a.eps;
+    np.cos = a.rotary_cos;
+    np.sin = a.rotary_sin;
+    np.rotary_dim = a.rotary_cos ? a.rotary_dim : 0;
+    np.max_pos = a.max_pos;
+    np.k_pages = k_pages;
+    np.v_pages = v_pages;
+    np.k_scale = k_scale;
+    np.v_scale = v_scale;
+    np.block_table = block_table;
+    np.seq_lens = seq_lens;
+    np.positions = a.positions;
+    np.new_lens = a.new_lens;
+    np.status = status_dev;
+    np.B = p.B;
+    np.T = a.tokens;
+    np.Hq = a.q ? p.Hq : 0;
+    np.Hkv = p.Hkv;
+    np.page_size = p.page_size;
+    np.max_blocks = p.max_blocks_per_seq;
+    np.num_pages = p.num_pages;
+    np.kv_kind = p.kv_dtype == FD_F16 ? KV_F16 : (p.kv_dtype == FD_BF16 ? KV_BF16 : KV_E4M3);
+    np.is_bf16 = p.q_dtype == FD_BF16 ? 1 : 0;
+    const cudaError_t e = launch_append_norm(np, p.D, a.interleaved ? 1 : 0, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FD_OK : (e == cudaErrorInvalidConfiguration ? FD_ERR_UNSUPPORTED : FD_ERR_CUDA);
+}
+
+fd_status fd_evict_kv(const fd_problem *problem, void *k_pages, void *v_pages, const float *k_scale,
+                      const float *v_scale, const int32_t *block_table, const int32_t *seq_lens, const float *weights,
+                      float *weights_out, int weights_stride, int budget, int sinks, int recent,
+                      const int32_t *dst_table, int32_t *new_lens, int32_t *kept, int32_t *status_dev, void *stream) {
+    const fd_status st = validate_problem(problem);
+    if (st != FD_OK) return st;
+    const fd_problem &p = *problem;
+    if (!k_pages || !v_pages || !block_table || !seq_lens || !weights || !new_lens || !kept) return FD_ERR_INVALID_ARG;
+    const bool fp8 = p.kv_dtype == FD_E4M3;
+    if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr)) return FD_ERR_INVALID_ARG;
+    if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(weights, 4) || !aligned(weights_out, 4) ||
+        !aligned(dst_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
+        return FD_ERR_INVALID_ARG;
+    if (weights_stride < 1 || budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+        return FD_ERR_INVALID_ARG;
+    if ((long long)budget > (long long)p.page_size * p.max_blocks_per_seq) return FD_ERR_INVALID_ARG;
+    if (half_overlaps(weights, weights_out, (size_t)p.B * p.Hkv * weights_stride)) return FD_ERR_INVALID_ARG;
+    // other CTAs still read a length while the first one of its sequence writes the new one
+    if (new_lens == seq_lens) return FD_ERR_INVALID_ARG;
+    DeviceInfo di;
+    const fd_status ds = device_info(di);
+    if (ds != FD_OK) return ds;
+    EvictParams ep;
+    std::memset(&ep, 0, sizeof(ep));
+    ep.k_pages = k_pages;
+    ep.v_pages = v_pages;
+    ep.k_scale = k_scale;
+    ep.v_scale = v_scale;
+    ep.block_table = block_table;
+    ep.dst_table = dst_table ? dst_table : block_table;
+    ep.seq_lens = seq_lens;
+    ep.weights = weights;
+    ep.weights_out = weights_out;
+    ep.new_lens = new_lens;
+    ep.kept = kept;
+    ep.status = status_dev;
+    ep.B = p.B;
+    ep.Hkv = p.Hkv;
+    ep.D = p.D;
+    ep.page_size = p.page_size;
+    ep.max_blocks = p.max_blocks_per_seq;
+    ep.num_pages = p.num_pages;
+    ep.row_bytes = p.D * elem_bytes(p.kv_dtype);
+    ep.weights_stride = weights_stride;
+    ep.budget = budget;
+    ep.sinks = sinks;
+    ep.recent = recent;
+    const cudaError_t e = launch_evict(ep, di.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FD_OK : (e == cudaErrorInvalidConfiguration ? FD_ERR_UNSUPPORTED : FD_ERR_CUDA);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Byte layout behind a differential plan's decode workspace: the padded
+// queries, both maps' outputs, and their lse.
+struct DiffLayout {
+    size_t q, o, lse, bytes;
+};
+
+DiffLayout diff_layout(const fd_problem &p) {  // p: the doubled problem
+    const size_t rows = (size_t)p.B * p.Hq;
+    DiffLayout l;
+    l.q = 0;
+    l.o = align256(rows * p.D * 2);
+    l.lse = l.o + align256(rows * p.D * sizeof(float));
+    l.bytes = l.lse + align256(rows * sizeof(float));
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
+                       fd_plan_t *plan) {
+    if (!plan || !seq_lens_host) return FD_ERR_INVALID_ARG;
+    const fd_status st = validate_problem(problem);
+    if (st != FD_OK) return st;
+    if (problem->Hq > (1 << 20)) return FD_ERR_UNSUPPORTED;
+    if (options && options->shared_kv) return FD_ERR_UNSUPPORTED;
+    fd_problem p = *problem;
+    p.Hq *= 2;
+    p.out_dtype = FD_F32;
+    const fd_status r = fd_plan(&p, seq_lens_host, options, plan);
+    if (r != FD_OK) return r;
+    plan->reserved[0] = kPlanDiff;
+    plan->reserved[1] = problem->out_dtype;
+    plan->workspace_bytes += diff_layout(plan->problem).bytes;
+    return FD_OK;
+}
+
+fd_status fd_decode_paged_diff(const fd_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
+                               const float *k_scale, const float *v_scale, const int32_t *block_table,
+                               const int32_t *seq_lens, const float *lambda, const void *norm_weight,
+                               fd_dtype norm_weight_dtype, float eps, float out_scale, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, int32_t *status_dev, void *stream) {
+    if (!plan || plan->reserved[0] != kPlanDiff) return FD_ERR_INVALID_ARG;
+    const fd_problem &p = plan->problem;
+    const fd_status st = validate_problem(&p);
+    if (st != FD_OK) return st;
+    const fd_dtype out_dtype = (fd_dtype)plan->reserved[1];
+    if (out_dtype != p.q_dtype && out_dtype != FD_F32) return FD_ERR_INVALID_ARG;
+    if (!q || !lambda || !out || !workspace) return FD_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lambda, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+        return FD_ERR_INVALID_ARG;
+    if (!norm_weight_ok(norm_weight, norm_weight_dtype, p.q_dtype)) return FD_ERR_INVALID_ARG;
+    if (norm_weight && (!(eps > 0.f) || !std::isfinite(eps))) return FD_ERR_INVALID_ARG;
+    const DiffLayout l = diff_layout(p);
+    if (workspace_bytes < plan->workspace_bytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+    if (plan->workspace_bytes < l.bytes) return FD_ERR_INVALID_ARG;
+    uint8_t *ws = static_cast<uint8_t *>(workspace) + (plan->workspace_bytes - l.bytes);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const long long rows = (long long)p.B * (p.Hq / 2);
+    DecodeMode mode;
+    mode.launch = &kDiffDecode;
+    mode.kind = kPlanDiff;
+    mode.score_width = p.D / 2;
+    mode.pair_q = q;
+    const fd_status r = decode_impl(plan, ws + l.q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, nullptr,
+                                    ws + l.o, lse ? lse : reinterpret_cast<float *>(ws + l.lse), workspace,
+                                    workspace_bytes, status_dev, stream, mode);
+    if (r != FD_OK) return r;
+    DiffCombineParams dp;
+    std::memset(&dp, 0, sizeof(dp));
+    dp.o = reinterpret_cast<const float *>(ws + l.o);
+    dp.lambda = lambda;
+    dp.w = norm_weight;
+    dp.out = out;
+    dp.rows = rows;
+    dp.Hq = p.Hq / 2;
+    dp.w_dtype = norm_weight_dtype;
+    dp.out_dtype = out_dtype;
+    dp.eps = eps;
+    dp.out_scale = out_scale;
+    return launch_diff_combine(dp, p.D, s) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 }  // extern "C"

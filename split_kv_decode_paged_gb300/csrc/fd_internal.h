@@ -59,6 +59,60 @@ struct DecodeParams {
     uint64_t stall_ns;         // test hook (0 = off): idle time of stall_role
     int stall_role;            // 1: producer before its first load; 2: consumers before the first release
     int qn;                    // query tokens per KV row, causal among them (1: one-token decode)
+    float *scores;             // [Bkv, Hkv, cap, G * fold] log2-unit scores, or null (the score-writing instances only)
+};
+
+// Attention-weight totals from the scores and lse of a decode call.
+struct WeightParams {
+    const float *scores;       // [Bkv, Hkv, cap, R]
+    const float *lse;          // [Bkv * fold, Hq]
+    const float *in;           // [Bkv, Hkv, weights_stride] or null (zeros)
+    float *out;                // [Bkv, Hkv, weights_stride]
+    const int32_t *seq_lens;
+    int *status;
+    int Bkv, Hq, Hkv, G, fold, R, cap, weights_stride;
+    int chunk_tokens;          // tokens per CTA (set at launch)
+};
+
+struct NormAppendParams {
+    const void *q, *k, *v;     // [B, T, heads, D] 16-bit, token strides in elements
+    void *q_out;
+    long long q_stride, k_stride, v_stride, q_out_stride;
+    const void *qw, *kw;       // [D] or null: no norm
+    int w_f32;                 // norm weights in fp32 (else in q's type)
+    float eps;
+    const float *cos, *sin;    // null: no rotation
+    int rotary_dim, max_pos;
+    void *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *seq_lens, *positions, *new_lens;
+    int *status;
+    int B, T, Hq, Hkv;         // Hq = 0: no queries
+    int page_size, max_blocks, num_pages;
+    int kv_kind, is_bf16;
+    int parts;                 // warps per token (set at launch)
+};
+
+struct EvictParams {
+    void *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const int32_t *block_table, *dst_table, *seq_lens;
+    const float *weights;
+    float *weights_out;        // null: not kept
+    int32_t *new_lens, *kept;  // [B], [B, Hkv, budget]
+    int *status;
+    int B, Hkv, D, page_size, max_blocks, num_pages, row_bytes;
+    int weights_stride, budget, sinks, recent;
+};
+
+struct DiffCombineParams {
+    const float *o;            // [2 rows, D]
+    const float *lambda;       // [Hq]
+    const void *w;             // [D] or null: no norm
+    void *out;                 // [rows, D]
+    long long rows;
+    int Hq, w_dtype, out_dtype;
+    float eps, out_scale;
 };
 
 struct MergeParams {
@@ -112,11 +166,13 @@ size_t decode_smem_bytes(const fd_problem &p, const KernelShape &ks, int stages,
 // dynamic shared memory (needs a device).
 cudaError_t decode_occupancy(const fd_problem &p, const KernelShape &ks, size_t smem, int *blocks);
 
-cudaError_t launch_decode(const fd_problem &p, const KernelShape &ks, const DecodeParams &dp,
-                          const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, size_t smem,
-                          cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams &mp, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &ap, cudaStream_t stream);
+cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream);
+cudaError_t launch_append_norm(NormAppendParams p, int D, int interleaved, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_diff_expand(const void *q, void *out, long long rows, int D, cudaStream_t stream);
+cudaError_t launch_diff_combine(const DiffCombineParams &p, int D, cudaStream_t stream);
 cudaError_t launch_merge_two(const float *oa, const float *la, const float *ob, const float *lb, int rows, int D,
                              int out_dtype, void *out, float *lse, cudaStream_t stream);
 
