@@ -163,7 +163,7 @@ typedef struct {
     int scratch_in_stage; /* 1: the item epilogue's scratch lives in the item's
                              last pipeline stage (16-bit K/V, where that makes
                              room for another stage); 0: a region of its own */
-    int reserved[2];      /* 0; fd_plan_diff: marks the plan and its output type  */
+    int reserved[2];      /* 0; fd_plan_diff marks its plans here               */
 } fd_plan_t;
 
 /* Plan a decode call [P1 §2.1 step 1; P2 进阶突破; P3 §6.3, §8.2].
@@ -529,8 +529,8 @@ fd_status fd_evict_kv(const fd_problem *problem, void *k_pages, void *v_pages, c
  * fd_plan_diff plans it (arguments as fd_plan): problem->Hq counts
  * differential heads and problem->D = 2 d; q is [B, Hq, D] with q1 in the
  * first half of a head and q2 in the second, K pages hold [k1 | k2], the head
- * groups are as for fd_decode_paged, and so is q_len.  No shared_kv.  The
- * plan is only for fd_decode_paged_diff (its problem field holds the doubled
+ * groups are as for fd_decode_paged, and so is q_len.  No shared_kv, and
+ * fuse_merge is taken as 1.  The plan is only for fd_decode_paged_diff (its problem field holds the doubled
  * heads the kernel works on), and no other plan is for it.
  *   lambda        device fp32 [Hq]
  *   norm_weight   device [D] in norm_weight_dtype (q_dtype or FD_F32), or NULL

@@ -681,7 +681,7 @@ def fd_decode_paged_diff(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale, bl
     a.tensor("block_table", block_table, torch.int32, (plan.kv_rows, p.max_blocks_per_seq))
     a.tensor("seq_lens", seq_lens, torch.int32, (plan.kv_rows,))
     a.tensor("lam", lam, torch.float32, (Hq,))
-    a.tensor("out", out, FD_TO_TORCH[plan.reserved[1]], _rows_shape(plan, out, (Hq, p.D)))
+    a.tensor("out", out, FD_TO_TORCH[p.out_dtype], _rows_shape(plan, out, (Hq, p.D)))
     a.tensor("lse", lse, torch.float32, _rows_shape(plan, lse, (Hq, 2)), optional=True)
     a.tensor("workspace", workspace, None, None, min_bytes=int(plan.workspace_bytes))
     a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)

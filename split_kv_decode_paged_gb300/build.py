@@ -18,7 +18,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["fd_api.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e4m3.cu", "decode_scores_f16.cu",
            "decode_scores_bf16.cu", "decode_scores_e4m3.cu", "decode_diff_f16.cu", "decode_diff_bf16.cu",
            "decode_diff_e4m3.cu", "merge.cu", "append.cu",
-           "append_norm.cu", "weights.cu", "evict.cu", "diff.cu", "noalloc.cu"]
+           "append_norm.cu", "weights.cu", "evict.cu", "noalloc.cu"]
 
 
 def nvcc() -> str:

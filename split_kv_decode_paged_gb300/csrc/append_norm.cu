@@ -9,15 +9,27 @@
 // D / 8 lanes of 16 bytes, so a warp takes 2 rows (D = 128) or 4 (D = 64) a
 // step; a lane keeps its place in the row, so the token's cosines and sines
 // and the norm weights stay in its registers over all the token's heads.
+// Where the whole row turns in halves a lane holds four elements of each half
+// instead of eight neighbours: its pairs are its own, no lane exchange, and it
+// needs four cosines and sines, not eight.
+#include <algorithm>
+
 #include "fd_internal.h"
 #include "ptx.cuh"
 
 namespace fd {
 
 constexpr int kNormWarps = 4;
-constexpr int kNormUnroll = 2;  // steps of a warp whose rows are requested together
+constexpr int kNormUnroll = 4;  // steps of a warp whose rows are requested together
 
-enum RotKind { ROT_NONE = 0, ROT_PAIRS = 1, ROT_HALVES = 2, ROT_HALVES_ANY = 3 };
+// How the pairs of a row lie in the lanes.
+enum RotKind {
+    ROT_NONE = 0,
+    ROT_PAIRS = 1,   // (2i, 2i + 1), rotary_dim a multiple of 8: in the lane
+    ROT_FULL = 2,    // halves, rotary_dim = D: four elements of each half a lane
+    ROT_HALVES = 3,  // halves of a multiple of 8: the same element of another lane
+    ROT_ANY = 4      // through shared memory; also for tables that are not 16-byte aligned
+};
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4 &r, float *x) {
@@ -45,57 +57,76 @@ __device__ __forceinline__ uint4 pack8(const float *y) {
     return r;
 }
 
+// Four norm weights from element d on (w16: 8-byte aligned 16-bit weights).
 template <bool BF16>
-__device__ __forceinline__ void load_weight8(const void *w, int f32, int d0, float *out) {
+__device__ __forceinline__ void load_weight4(const void *w, int f32, bool w16, int d, float *out) {
+    if (!f32 && w16) {
+        const uint2 r = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(w) + d));
+        float x[8];
+        unpack8<BF16>(make_uint4(r.x, r.y, 0u, 0u), x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) out[e] = x[e];
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
         if (f32) {
-            out[e] = __ldg(reinterpret_cast<const float *>(w) + d0 + e);
+            out[e] = __ldg(reinterpret_cast<const float *>(w) + d + e);
         } else {
-            const uint16_t b = __ldg(reinterpret_cast<const uint16_t *>(w) + d0 + e);
+            const uint16_t b = __ldg(reinterpret_cast<const uint16_t *>(w) + d + e);
             out[e] = BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
         }
     }
 }
 
-template <int D, bool BF16, bool FP8, int ROT>
+// ONE: a warp has one step (few tokens: the latency of a call); its rows are
+// requested before the lengths, positions and page id that say where they go.
+// Otherwise a warp goes through every p.parts-th step of its token.
+template <int D, bool BF16, bool FP8, int ROT, bool ONE>
 __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(const __grid_constant__ NormAppendParams p) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int NCS = ROT == ROT_NONE ? 1 : (ROT == ROT_PAIRS || ROT == ROT_FULL ? 4 : 8);  // cosines a lane holds
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = lane / LPR, d0 = (lane % LPR) * 8;
+    const int sub = lane / LPR, l = lane % LPR;
+    // elements 0-3 of the lane are da .. da + 3 of the row, 4-7 db .. db + 3
+    const int da = ROT == ROT_FULL ? 4 * l : 8 * l, db = ROT == ROT_FULL ? D / 2 + 4 * l : 8 * l + 4;
     const long long job = (long long)blockIdx.x * kNormWarps + warp;  // (token, part of its rows)
     const long long tok = job / p.parts;
     const int part = (int)(job - tok * p.parts);
     if (tok >= (long long)p.B * p.T) return;
     const int b = (int)(tok / p.T), i = (int)(tok - (long long)b * p.T);
-    const int nrows = p.Hq + 2 * p.Hkv;
-    const int step = p.parts * RPW;
+    // Steps of this token: those of q, then k, then v (a step has one kind).
+    const int sq = (p.Hq + RPW - 1) / RPW, sk = (p.Hkv + RPW - 1) / RPW;
 
-    auto load_row = [&](int row) -> uint4 {
-        if (row >= nrows) return make_uint4(0u, 0u, 0u, 0u);
-        const uint16_t *src;
-        if (row < p.Hq)
-            src = reinterpret_cast<const uint16_t *>(p.q) + tok * p.q_stride + (size_t)row * D;
-        else if (row < p.Hq + p.Hkv)
-            src = reinterpret_cast<const uint16_t *>(p.k) + tok * p.k_stride + (size_t)(row - p.Hq) * D;
-        else
-            src = reinterpret_cast<const uint16_t *>(p.v) + tok * p.v_stride + (size_t)(row - p.Hq - p.Hkv) * D;
-        return *reinterpret_cast<const uint4 *>(src + d0);
+    auto load8 = [&](const uint16_t *src) -> uint4 {
+        if constexpr (ROT == ROT_FULL) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(src + da), y = *reinterpret_cast<const uint2 *>(src + db);
+            return make_uint4(x.x, x.y, y.x, y.y);
+        } else {
+            return *reinterpret_cast<const uint4 *>(src + da);
+        }
     };
-    // The first rows do not depend on where they go: requested before the
-    // lengths, positions and page id.
-    uint4 raw[kNormUnroll];
-#pragma unroll
-    for (int u = 0; u < kNormUnroll; ++u) raw[u] = load_row(part * RPW + sub + u * step);
-
-    const int fresh = p.new_lens ? __ldg(p.new_lens + b) : p.T;
+    const uint16_t *qrow = reinterpret_cast<const uint16_t *>(p.q) + tok * p.q_stride;
+    const uint16_t *krow = reinterpret_cast<const uint16_t *>(p.k) + tok * p.k_stride;
+    const uint16_t *vrow = reinterpret_cast<const uint16_t *>(p.v) + tok * p.v_stride;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    int fresh = p.T;
+    uint4 first = none;
+    if constexpr (ONE) {
+        const int kind = part < sq ? 0 : (part < sq + sk ? 1 : 2);
+        const int row = (part - (kind == 0 ? 0 : (kind == 1 ? sq : sq + sk))) * RPW + sub;
+        if (row < (kind == 0 ? p.Hq : p.Hkv)) first = load8((kind == 0 ? qrow : (kind == 1 ? krow : vrow)) + row * D);
+    }
+    if (p.new_lens) {
+        fresh = __ldg(p.new_lens + b);
+        if (i >= fresh && fresh >= 0) return;
+    }
     const int len = __ldg(p.seq_lens + b);
     const long long pos = (long long)(p.positions ? __ldg(p.positions + b) : len) + i;
     if (fresh < 0 || fresh > p.T) {
         if (lane == 0 && part == 0 && i == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
         return;
     }
-    if (i >= fresh) return;
     if (ROT != ROT_NONE && (pos < 0 || pos >= p.max_pos)) {
         if (lane == 0 && part == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
         return;
@@ -108,153 +139,255 @@ __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(cons
     if (!stored && lane == 0 && part == 0 && p.status) atomicOr(p.status, FD_DEV_BAD_PAGE);
     const size_t dst_tok = stored ? ((size_t)page * p.page_size + (size_t)(at - col * p.page_size)) * p.Hkv : 0;
 
-    // This lane's cosines and sines: element e of the row turns with angle
-    // index ai(e); elements from rotary_dim on pass through.
-    const int half = p.rotary_dim >> 1;
-    float c[8], s[8];
+    // This lane's cosines and sines; elements from rotary_dim on pass through.
+    const int rd = p.rotary_dim, half = rd >> 1;
+    float c[NCS], s[NCS];
     if constexpr (ROT != ROT_NONE) {
         const float *cr = p.cos + (size_t)pos * half, *sr = p.sin + (size_t)pos * half;
+        if constexpr (ROT == ROT_ANY) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int d = d0 + e;
-            const int ai = ROT == ROT_PAIRS ? d >> 1 : (d < half ? d : d - half);
-            const bool in = d < p.rotary_dim;
-            c[e] = in ? __ldg(cr + ai) : 1.f;
-            s[e] = in ? __ldg(sr + ai) : 0.f;
+            for (int e = 0; e < 8; ++e) {
+                const int d = da + e;
+                const int ai = p.interleaved ? d >> 1 : (d < half ? d : d - half);
+                c[e] = d < rd ? __ldg(cr + ai) : 1.f;
+                s[e] = d < rd ? __ldg(sr + ai) : 0.f;
+            }
+        } else {
+            const int a0 = ROT == ROT_PAIRS ? da >> 1 : (ROT == ROT_FULL || da < half ? da : da - half);
+            if (da < rd) {
+#pragma unroll
+                for (int e = 0; e < NCS; e += 4) {
+                    const float4 x = __ldg(reinterpret_cast<const float4 *>(cr + a0 + e));
+                    const float4 y = __ldg(reinterpret_cast<const float4 *>(sr + a0 + e));
+                    c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
+                    s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
+                }
+            }
         }
     }
-    float wq[8], wk[8];
-    if (p.qw) load_weight8<BF16>(p.qw, p.w_f32, d0, wq);
-    if (p.kw) load_weight8<BF16>(p.kw, p.w_f32, d0, wk);
-    __shared__ float xch[ROT == ROT_HALVES_ANY ? kNormWarps * RPW * D : 1];
-
-    for (int r0 = part * RPW; r0 < nrows; r0 += kNormUnroll * step) {
-        if (r0 != part * RPW) {
-#pragma unroll
-            for (int u = 0; u < kNormUnroll; ++u) raw[u] = load_row(r0 + sub + u * step);
+    float w[8];  // norm weights of the kind at hand
+    auto load_weights = [&](const void *src) {
+        if (src) {
+            load_weight4<BF16>(src, p.w_f32, p.w_vec, da, w);
+            load_weight4<BF16>(src, p.w_f32, p.w_vec, db, w + 4);
         }
-#pragma unroll
-        for (int u = 0; u < kNormUnroll; ++u) {
-            if (r0 + u * step >= nrows) break;  // the same for the whole warp
-            const int row = r0 + sub + u * step;
-            const int kind = row < p.Hq ? 0 : (row < p.Hq + p.Hkv ? 1 : 2);  // q, k, v
-            float x[8];
-            unpack8<BF16>(raw[u], x);
-            // every lane takes part in the row sums; v rows drop them
+    };
+    __shared__ float xch[ROT == ROT_ANY ? kNormWarps * RPW * D : 1];
+
+    // each product and the sum rounded by itself, as in fd_append_kv_rotary
+    auto turn_first = [](float x, float y, float cc, float ss) { return __fsub_rn(__fmul_rn(x, cc), __fmul_rn(y, ss)); };
+    auto turn_second = [](float x, float y, float cc, float ss) { return __fadd_rn(__fmul_rn(x, cc), __fmul_rn(y, ss)); };
+    // Norm and rotation of a q or k row; every lane of the warp takes part.
+    auto norm_turn = [&](bool normed, float *x) {
+        if (normed) {
             float ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += shfl_xor(ss, o);
-            const bool normed = kind == 0 ? p.qw != nullptr : (kind == 1 && p.kw != nullptr);
-            if (normed) {
-                const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+            const float inv = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * (kind == 0 ? wq[e] : wk[e]);
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * w[e];
+        }
+        if constexpr (ROT == ROT_FULL) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = x[e], bb = x[e + 4];
+                x[e] = turn_first(a, bb, c[e], s[e]);
+                x[e + 4] = turn_second(bb, a, c[e], s[e]);
             }
-            if constexpr (ROT != ROT_NONE) {
-                float y[8];
-                if constexpr (ROT == ROT_PAIRS) {
+        } else if constexpr (ROT == ROT_PAIRS) {
+            if (da < rd) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-                } else if constexpr (ROT == ROT_HALVES) {
-                    // half a multiple of 8: element e's partner is element e
-                    // of the lane half / 8 places on (or back)
-                    const int hl = half >> 3, l = lane % LPR;
-                    const int from = lane - l + (l < hl ? l + hl : (l < 2 * hl ? l - hl : l));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], from);
-                } else {
-                    float *buf = xch + (warp * RPW + sub) * D;
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) buf[d0 + e] = x[e];
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int d = d0 + e;
-                        y[e] = d < p.rotary_dim ? buf[d < half ? d + half : d - half] : 0.f;
-                    }
-                }
-                if (kind < 2) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int d = d0 + e;
-                        const bool first = ROT == ROT_PAIRS ? (e & 1) == 0 : d < half;
-                        // each product and the sum rounded by itself, as in fd_append_kv_rotary
-                        const float r = first ? __fsub_rn(__fmul_rn(x[e], c[e]), __fmul_rn(y[e], s[e]))
-                                              : __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(y[e], s[e]));
-                        if (d < p.rotary_dim) x[e] = r;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float a = x[2 * e], bb = x[2 * e + 1];
+                    x[2 * e] = turn_first(a, bb, c[e], s[e]);
+                    x[2 * e + 1] = turn_second(bb, a, c[e], s[e]);
                 }
             }
-            if (row >= nrows) continue;
-            if (kind == 0) {
-                uint16_t *out = reinterpret_cast<uint16_t *>(p.q_out) + tok * p.q_out_stride + (size_t)row * D + d0;
-                *reinterpret_cast<uint4 *>(out) = pack8<BF16>(x);
-                continue;
-            }
-            if (!stored) continue;
-            const int h = row - p.Hq - (kind == 2 ? p.Hkv : 0);
-            const size_t dst = (dst_tok + h) * D + d0;
-            void *pool = kind == 1 ? p.k_pages : p.v_pages;
-            if constexpr (FP8) {
-                const float sc = __ldg((kind == 1 ? p.k_scale : p.v_scale) + (size_t)page * p.Hkv + h);
-                uint2 codes;
-                uint32_t *cw = reinterpret_cast<uint32_t *>(&codes);
+        } else if constexpr (ROT == ROT_HALVES || ROT == ROT_ANY) {
+            float y[8];
+            if constexpr (ROT == ROT_HALVES) {
+                const int hl = half >> 3;  // lanes of a half
+                const int from = lane - l + (l < hl ? l + hl : (l < 2 * hl ? l - hl : l));
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t lo = f32x2_to_e4m3x2(__fdiv_rn(x[4 * k + 1], sc), __fdiv_rn(x[4 * k], sc));
-                    const uint32_t hi = f32x2_to_e4m3x2(__fdiv_rn(x[4 * k + 3], sc), __fdiv_rn(x[4 * k + 2], sc));
-                    cw[k] = lo | (hi << 16);
-                }
-                *reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(pool) + dst) = codes;
+                for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], from);
             } else {
-                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(pool) + dst) = pack8<BF16>(x);
+                float *buf = xch + (warp * RPW + sub) * D;
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) buf[da + e] = x[e];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = da + e;
+                    const int other = p.interleaved ? d ^ 1 : (d < half ? d + half : d - half);
+                    y[e] = d < rd ? buf[other] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = da + e;
+                const bool lower = ROT == ROT_ANY && p.interleaved ? (e & 1) == 0 : d < half;
+                const float r = lower ? turn_first(x[e], y[e], c[e], s[e]) : turn_second(x[e], y[e], c[e], s[e]);
+                if (d < rd) x[e] = r;
             }
         }
+    };
+
+    // 16 bytes of a q row, or of a cache row in its 16-bit type.
+    auto store8 = [&](uint16_t *out, const uint4 &v) {
+        if constexpr (ROT == ROT_FULL) {
+            *reinterpret_cast<uint2 *>(out + da) = make_uint2(v.x, v.y);
+            *reinterpret_cast<uint2 *>(out + db) = make_uint2(v.z, v.w);
+        } else {
+            *reinterpret_cast<uint4 *>(out + da) = v;
+        }
+    };
+    auto store_codes = [&](uint8_t *out, const float *x, float sc) {
+        uint32_t cw[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t lo = f32x2_to_e4m3x2(__fdiv_rn(x[4 * k + 1], sc), __fdiv_rn(x[4 * k], sc));
+            const uint32_t hi = f32x2_to_e4m3x2(__fdiv_rn(x[4 * k + 3], sc), __fdiv_rn(x[4 * k + 2], sc));
+            cw[k] = lo | (hi << 16);
+        }
+        if constexpr (ROT == ROT_FULL) {
+            *reinterpret_cast<uint32_t *>(out + da) = cw[0];
+            *reinterpret_cast<uint32_t *>(out + db) = cw[1];
+        } else {
+            *reinterpret_cast<uint2 *>(out + da) = make_uint2(cw[0], cw[1]);
+        }
+    };
+    // One row (live: there is one here): v rows keep their bits in a 16-bit cache.
+    uint16_t *qo = reinterpret_cast<uint16_t *>(p.q_out) + tok * p.q_out_stride;
+    auto do_q = [&](uint4 bits, int row, bool live) {
+        float x[8];
+        unpack8<BF16>(bits, x);
+        norm_turn(p.qw != nullptr, x);
+        if (live) store8(qo + row * D, pack8<BF16>(x));
+    };
+    auto do_k = [&](uint4 bits, int row, bool live) {
+        float x[8];
+        unpack8<BF16>(bits, x);
+        norm_turn(p.kw != nullptr, x);
+        if (!live || !stored) return;
+        if constexpr (FP8)
+            store_codes(reinterpret_cast<uint8_t *>(p.k_pages) + (dst_tok + row) * D, x,
+                        __ldg(p.k_scale + (size_t)page * p.Hkv + row));
+        else
+            store8(reinterpret_cast<uint16_t *>(p.k_pages) + (dst_tok + row) * D, pack8<BF16>(x));
+    };
+    auto do_v = [&](uint4 bits, int row, bool live) {
+        if (!live || !stored) return;
+        if constexpr (FP8) {
+            float x[8];
+            unpack8<BF16>(bits, x);
+            store_codes(reinterpret_cast<uint8_t *>(p.v_pages) + (dst_tok + row) * D, x,
+                        __ldg(p.v_scale + (size_t)page * p.Hkv + row));
+        } else {
+            store8(reinterpret_cast<uint16_t *>(p.v_pages) + (dst_tok + row) * D, bits);
+        }
+    };
+    if constexpr (ONE) {
+        if (part < sq) {
+            load_weights(p.qw);
+            do_q(first, part * RPW + sub, part * RPW + sub < p.Hq);
+        } else if (part < sq + sk) {
+            load_weights(p.kw);
+            do_k(first, (part - sq) * RPW + sub, (part - sq) * RPW + sub < p.Hkv);
+        } else {
+            do_v(first, (part - sq - sk) * RPW + sub, (part - sq - sk) * RPW + sub < p.Hkv);
+        }
+    } else {
+        // This warp's steps of one kind with n rows, steps base and on.
+        auto each = [&](int base, int n, const uint16_t *rows, auto &&work) {
+            int j = part - base % p.parts;
+            if (j < 0) j += p.parts;  // the first step of the kind that is this warp's
+            for (int r0 = j * RPW; r0 < n; r0 += kNormUnroll * p.parts * RPW) {
+                uint4 raw[kNormUnroll];
+#pragma unroll
+                for (int u = 0; u < kNormUnroll; ++u) {
+                    const int row = r0 + u * p.parts * RPW + sub;
+                    raw[u] = row < n ? load8(rows + row * D) : none;
+                }
+#pragma unroll
+                for (int u = 0; u < kNormUnroll; ++u) {
+                    const int row = r0 + u * p.parts * RPW + sub;
+                    if (row - sub < n) work(raw[u], row, row < n);  // the same for the whole warp
+                }
+            }
+        };
+        load_weights(p.qw);
+        each(0, p.Hq, qrow, do_q);
+        load_weights(p.kw);
+        each(sq, p.Hkv, krow, do_k);
+        each(sq + sk, p.Hkv, vrow, do_v);
     }
 }
 
 namespace {
 
-template <int D, bool BF16, bool FP8>
-cudaError_t launch_rot(const NormAppendParams &p, int rot, unsigned blocks, cudaStream_t stream) {
-    const int threads = kNormWarps * 32;
-    switch (rot) {
-    case ROT_NONE: fd_append_kv_norm_kernel<D, BF16, FP8, ROT_NONE><<<blocks, threads, 0, stream>>>(p); break;
-    case ROT_PAIRS: fd_append_kv_norm_kernel<D, BF16, FP8, ROT_PAIRS><<<blocks, threads, 0, stream>>>(p); break;
-    case ROT_HALVES: fd_append_kv_norm_kernel<D, BF16, FP8, ROT_HALVES><<<blocks, threads, 0, stream>>>(p); break;
-    default: fd_append_kv_norm_kernel<D, BF16, FP8, ROT_HALVES_ANY><<<blocks, threads, 0, stream>>>(p); break;
-    }
+template <int D, bool BF16, bool FP8, int ROT>
+cudaError_t launch_rot(const NormAppendParams &p, bool one, unsigned blocks, cudaStream_t stream) {
+    if (one)
+        fd_append_kv_norm_kernel<D, BF16, FP8, ROT, true><<<blocks, kNormWarps * 32, 0, stream>>>(p);
+    else
+        fd_append_kv_norm_kernel<D, BF16, FP8, ROT, false><<<blocks, kNormWarps * 32, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
+template <int D, bool BF16, bool FP8>
+cudaError_t launch_types(const NormAppendParams &p, int rot, bool one, unsigned blocks, cudaStream_t stream) {
+    switch (rot) {
+    case ROT_NONE: return launch_rot<D, BF16, FP8, ROT_NONE>(p, one, blocks, stream);
+    case ROT_PAIRS: return launch_rot<D, BF16, FP8, ROT_PAIRS>(p, one, blocks, stream);
+    case ROT_FULL: return launch_rot<D, BF16, FP8, ROT_FULL>(p, one, blocks, stream);
+    case ROT_HALVES: return launch_rot<D, BF16, FP8, ROT_HALVES>(p, one, blocks, stream);
+    default: return launch_rot<D, BF16, FP8, ROT_ANY>(p, one, blocks, stream);
+    }
+}
+
 template <int D>
-cudaError_t launch_kind(const NormAppendParams &p, int rot, unsigned blocks, cudaStream_t stream) {
+cudaError_t launch_width(const NormAppendParams &p, int rot, bool one, unsigned blocks, cudaStream_t stream) {
     if (p.kv_kind == KV_E4M3)
-        return p.is_bf16 ? launch_rot<D, true, true>(p, rot, blocks, stream)
-                         : launch_rot<D, false, true>(p, rot, blocks, stream);
-    return p.is_bf16 ? launch_rot<D, true, false>(p, rot, blocks, stream)
-                     : launch_rot<D, false, false>(p, rot, blocks, stream);
+        return p.is_bf16 ? launch_types<D, true, true>(p, rot, one, blocks, stream)
+                         : launch_types<D, false, true>(p, rot, one, blocks, stream);
+    return p.is_bf16 ? launch_types<D, true, false>(p, rot, one, blocks, stream)
+                     : launch_types<D, false, false>(p, rot, one, blocks, stream);
 }
 
 }  // namespace
 
-// D: 64 or 128 (validated); p.parts is set here.  A grid that CUDA cannot
-// launch is cudaErrorInvalidConfiguration.
-cudaError_t launch_append_norm(NormAppendParams p, int D, int interleaved, cudaStream_t stream) {
+// D: 64 or 128 (validated); p.parts and p.w_vec are set here.  A grid that
+// CUDA cannot launch is cudaErrorInvalidConfiguration.
+cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream) {
     const long long tokens = (long long)p.B * p.T;
     const int rpw = 256 / D;
-    const int steps = (p.Hq + 2 * p.Hkv + rpw - 1) / rpw;
-    p.parts = steps;  // one step a warp
-    if (tokens * steps > 16384) p.parts = (steps + 7) / 8;
+    const int steps = (p.Hq + rpw - 1) / rpw + 2 * ((p.Hkv + rpw - 1) / rpw);
+    // Few tokens: a step a warp.  Many: a warp per token (measured on 16.6K
+    // tokens of 24 steps: 71.6 us; 2 warps a token 75.4, 4 warps 96.7), or as
+    // many as give every SM its 64 warps.
+    const bool one = tokens * steps <= 16384;
+    p.parts = one ? steps : (int)std::min<long long>(steps, (9728 + tokens - 1) / tokens);
     const long long blocks = (tokens * p.parts + kNormWarps - 1) / kNormWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    auto al = [](const void *x, size_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };
+    p.w_vec = al(p.qw, 8) && al(p.kw, 8);
     int rot = ROT_NONE;
-    if (p.cos) rot = interleaved ? ROT_PAIRS : (p.rotary_dim % 16 == 0 ? ROT_HALVES : ROT_HALVES_ANY);
-    return D == 128 ? launch_kind<128>(p, rot, (unsigned)blocks, stream)
-                    : launch_kind<64>(p, rot, (unsigned)blocks, stream);
+    if (p.cos) {
+        const bool vec = al(p.cos, 16) && al(p.sin, 16);
+        if (vec && p.interleaved && p.rotary_dim % 8 == 0)
+            rot = ROT_PAIRS;
+        else if (vec && !p.interleaved && p.rotary_dim == D)
+            rot = ROT_FULL;
+        else if (vec && !p.interleaved && p.rotary_dim % 16 == 0)
+            rot = ROT_HALVES;
+        else
+            rot = ROT_ANY;
+    }
+    return D == 128 ? launch_width<128>(p, rot, one, (unsigned)blocks, stream)
+                    : launch_width<64>(p, rot, one, (unsigned)blocks, stream);
 }
 
 }  // namespace fd

@@ -45,6 +45,7 @@
 
 #include "fd_internal.h"
 #include "ptx.cuh"
+#include "weights.cuh"
 
 namespace fd {
 
@@ -271,6 +272,121 @@ __device__ void merge_group(const DecodeParams &p, int b, int kvh, int hg, int n
     }
 }
 
+// One output head of differential attention, by D / 4 neighbouring lanes of a
+// warp with elements d .. d + 3 each: a1 * inv1 - lambda * a2 * inv2, its RMS
+// norm where there is a weight, and the scale.  vrow: the head's first padded
+// query row.  Every lane of the warp calls it; in: whether it has elements.
+template <int D>
+__device__ __forceinline__ void finish_pair(const DecodeParams &p, size_t vrow, int d, const float4 &a1, float inv1,
+                                            const float4 &a2, float inv2, bool in) {
+    const size_t row = vrow >> 1;
+    const float lam = __ldg(p.lambda + row % (unsigned)(p.Hq >> 1)) * inv2;
+    float v[4] = {a1.x * inv1 - lam * a2.x, a1.y * inv1 - lam * a2.y, a1.z * inv1 - lam * a2.z, a1.w * inv1 - lam * a2.w};
+    float mul = p.out_scale;
+    if (p.norm_w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ss = fmaf(v[e], v[e], ss);
+#pragma unroll
+        for (int o = D / 8; o > 0; o >>= 1) ss += shfl_xor(ss, o);
+        mul *= rsqrtf(ss * (1.f / D) + p.norm_eps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float w;
+            if (p.norm_w_dtype == FD_F32)
+                w = __ldg(reinterpret_cast<const float *>(p.norm_w) + d + e);
+            else {
+                const uint16_t b = __ldg(reinterpret_cast<const uint16_t *>(p.norm_w) + d + e);
+                w = p.norm_w_dtype == FD_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+            }
+            v[e] *= w;
+        }
+    }
+    if (in) store_out4(p.out, row * D + d, v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul, p.out_dtype);
+}
+
+// merge_group of differential attention: both rows of a pair merged and
+// finished by the same lanes.  The weights of all splits first (a warp per
+// row), then the outputs.
+template <int NC, int D>
+__device__ void merge_pairs(const DecodeParams &p, int b, int kvh, int hg, int nrows, int qrows, int nsplit,
+                            float *alpha, int warp, int lane) {
+    const int S = p.S;
+    for (int h = warp; h < nrows; h += NC) {
+        const size_t row = q_row(p, b, kvh, hg, h, qrows);
+        const float *pm = p.part_m + row * S;
+        const float *pd = p.part_d + row * S;
+        float mx = -INFINITY, d_lane = 0.f;
+        for (int s = lane; s < nsplit; s += 32) {
+            const float ms = ldcg(pm + s);
+            if (s < 32) d_lane = ldcg(pd + s);
+            alpha[h * nsplit + s] = ms;
+            mx = fmaxf(mx, ms);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, shfl_xor(mx, o));
+        float sum = 0.f;
+        for (int s = lane; s < nsplit; s += 32) {
+            const float ms = alpha[h * nsplit + s];
+            const float a = (ms == -INFINITY) ? 0.f : __expf(ms - mx);
+            alpha[h * nsplit + s] = a;
+            sum += a * (s < 32 ? d_lane : ldcg(pd + s));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += shfl_xor(sum, o);
+        const bool empty = (mx == -INFINITY) || !(sum > 0.f);
+        const float inv = empty ? 0.f : 1.f / sum;
+        for (int s = lane; s < nsplit; s += 32) alpha[h * nsplit + s] *= inv;
+        if (lane == 0 && p.lse) p.lse[row] = empty ? -INFINITY : mx + logf(sum);
+    }
+    named_bar_sync(1, NC * 32);
+    const int total = nrows / 2 * (D / 4);
+    for (int i0 = warp * 32; i0 < total; i0 += NC * 32) {
+        const int idx = i0 + lane;
+        const bool in = idx < total;
+        const int h = in ? idx / (D / 4) * 2 : 0, d = (idx % (D / 4)) * 4;
+        const size_t row = q_row(p, b, kvh, hg, h, qrows);
+        float4 acc[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const float *po = p.part_o + (row + m) * S * D + d;
+            const float *al = alpha + (h + m) * nsplit;
+            acc[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s0 = 0; s0 < nsplit; s0 += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = (s0 + k < nsplit) ? __ldcg(reinterpret_cast<const float4 *>(po + (size_t)(s0 + k) * D))
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float a = (s0 + k < nsplit) ? al[s0 + k] : 0.f;
+                    acc[m].x = fmaf(a, v[k].x, acc[m].x);
+                    acc[m].y = fmaf(a, v[k].y, acc[m].y);
+                    acc[m].z = fmaf(a, v[k].z, acc[m].z);
+                    acc[m].w = fmaf(a, v[k].w, acc[m].w);
+                }
+            }
+        }
+        finish_pair<D>(p, row, d, acc[0], 1.f, acc[1], 1.f, in);
+    }
+}
+
+// Attention-weight totals of a whole sequence's tokens [0, L) for one KV head
+// from this CTA's scores and the rows' max and 1 / denominator.
+template <int NC>
+__device__ __forceinline__ void add_weights(const DecodeParams &p, int b, int kvh, int L, const float *row_max,
+                                            const float *row_inv, int tid) {
+    const int R = p.G * p.fold;
+    const size_t at = ((size_t)b * p.Hkv + kvh) * p.w_stride;
+    if (L > p.w_stride) {
+        if (tid == 0) flag_status(p.status, FD_DEV_CAPACITY);
+        L = p.w_stride;
+    }
+    sum_weights<NC * 32, 8>(p.cta_scores + (size_t)blockIdx.x * p.chunk * R, R, row_max, row_inv,
+                            p.w_in ? p.w_in + at : nullptr, p.w_out + at, 0, L, tid);
+}
+
 // Dispatch tables of a large batch (at least kCoopBlocks 32-row blocks),
 // built by all NC + 1 warps of the CTA: the consumers have nothing to do
 // before the first stage lands.  The result is the one the producer builds
@@ -427,7 +543,8 @@ __device__ __noinline__ void build_dispatch_tables_coop(const DecodeParams &p, i
 // SCR: the E4M3 instance that may keep its epilogue scratch in the held stage.
 // MODE kScores: every score (log2 units, -inf where hidden) also goes to
 // DecodeParams::scores, for the attention-weight totals (weights.cu).  MODE
-// kDiff: the decode of differential attention (diff.cu).  In both the
+// kDiff: differential attention (two padded query rows a head, see
+// kQRowsPerHead; the pair's difference and norm in the epilogue).  In both the
 // denominator sums the weights before they are rounded for P.V: their
 // results go by the lse itself (a total of weights, a difference of two
 // outputs), where a plain decode's output is a ratio in which the rounding of
@@ -441,6 +558,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     constexpr int TILE = Sh::TILE, SUBROW = Sh::SUBROW, NHALF = Sh::NHALF;
     constexpr int QROWS = Sh::QROWS, SS = Sh::SS;
     constexpr bool FP8 = (KV == KV_E4M3);
+    // Differential attention: the query rows 2i and 2i + 1 of an item are
+    // [q1 | 0] and [0 | q2] of one head; memory holds [q1 | q2].  All the
+    // counts of rows here are of the padded ones (even in number).
+    constexpr int kQRowsPerHead = MODE == kDiff ? 2 : 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -778,7 +899,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 const int t0 = t_begin + j * TILE;
                 const bool load_q = (j == 0) && (ntok > 0);
                 const uint32_t bytes = (uint32_t)__popc(good_mask) * 2u * (uint32_t)(boxr * Sh::RB) +
-                                       (load_q ? (uint32_t)(cur.nrows * D * 2) : 0u);
+                                       (load_q ? (uint32_t)(cur.nrows * D * 2 / kQRowsPerHead) : 0u);
                 StageMeta *m = &meta[st];
                 if (lane == 0) {
                     m->b = b; m->kvh = kvh; m->s = s; m->t0 = t0;
@@ -828,9 +949,9 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                         if (ia < ib) {
                             const int bq = b * p.fold + ia / Gh;
                             const uint8_t *qsrc = reinterpret_cast<const uint8_t *>(p.q) +
-                                                  ((size_t)bq * p.Hq + (size_t)kvh * Gh + (ia % Gh)) * D * 2;
-                            bulk_load(smem_u32(sb + 2 * Sh::KV_REGION + (ia - i0) * D * 2), qsrc,
-                                      (uint32_t)((ib - ia) * D * 2), fb);
+                                                  ((size_t)bq * p.Hq + (size_t)kvh * Gh + (ia % Gh)) / kQRowsPerHead * D * 2;
+                            bulk_load(smem_u32(sb + 2 * Sh::KV_REGION + (ia - i0) / kQRowsPerHead * D * 2), qsrc,
+                                      (uint32_t)((ib - ia) / kQRowsPerHead * D * 2), fb);
                         }
                     }
                 };
@@ -918,26 +1039,29 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
         const uint32_t kbase = smem_u32(sb), vbase = kbase + Sh::KV_REGION, qbase = kbase + 2 * Sh::KV_REGION;
 
         if (flags & kFlagFirst) {
-            // Query fragments (B operand of QK), zero for padded heads.
+            // Query fragments (B operand of QK), zero for padded heads and, in
+            // a differential item, for the half that is not this row's.
+            auto q_live = [&](int ks) { return MODE != kDiff || (ks < KT / 2) == ((g & 1) == 0); };
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const bool live_head = (n * 8 + g) < mt.nrows;
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int kk = 0; kk < KT; kk += 2) {
-                        const int row = n * 8 + (lane & 7);
+                        const int row = (n * 8 + (lane & 7)) / kQRowsPerHead;
                         const int chunk = 2 * kk + (lane >> 3);
                         uint32_t r0, r1, r2, r3;
                         ldsm_x4(qbase + (uint32_t)(row * D * 2 + chunk * 16), r0, r1, r2, r3);
-                        qf[kk][n][0] = live_head ? r0 : 0u;
-                        qf[kk][n][1] = live_head ? r1 : 0u;
-                        qf[kk + 1][n][0] = live_head ? r2 : 0u;
-                        qf[kk + 1][n][1] = live_head ? r3 : 0u;
+                        const bool live = live_head && q_live(kk);
+                        qf[kk][n][0] = live ? r0 : 0u;
+                        qf[kk][n][1] = live ? r1 : 0u;
+                        qf[kk + 1][n][0] = live ? r2 : 0u;
+                        qf[kk + 1][n][1] = live ? r3 : 0u;
                     }
                 } else {
                     // f16 fragments in the E4M3 k-order: k-step ks covers
                     // d = 32*(ks/2) + 16*(ks%2) + {4c..4c+3}.
-                    const int row = n * 8 + g;
+                    const int row = (n * 8 + g) / kQRowsPerHead;
                     const uint8_t *qrow = sb + 2 * Sh::KV_REGION + row * D * 2;
                     if constexpr (QBF16) {
                         // bf16 q into the f16 product.  Direct conversion is
@@ -955,7 +1079,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                         for (int ks = 0; ks < KT; ++ks) {
                             const int d0 = 32 * (ks >> 1) + 16 * (ks & 1) + 4 * c;
-                            const uint2 raw = *reinterpret_cast<const uint2 *>(qrow + d0 * 2);
+                            const uint2 raw = q_live(ks) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
                             const float x0 = __uint_as_float(raw.x << 16), x1 = __uint_as_float(raw.x & 0xffff0000u);
                             const float x2 = __uint_as_float(raw.y << 16), x3 = __uint_as_float(raw.y & 0xffff0000u);
                             amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x0), fabsf(x1))), fmaxf(fabsf(x2), fabsf(x3)));
@@ -979,7 +1103,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                             for (int ks = 0; ks < KT; ++ks) {
                                 const int d0 = 32 * (ks >> 1) + 16 * (ks & 1) + 4 * c;
-                                const uint2 raw = *reinterpret_cast<const uint2 *>(qrow + d0 * 2);
+                                const uint2 raw = q_live(ks) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
                                 const uint32_t w0 = pack_f16x2(__uint_as_float(raw.x << 16) * up,
                                                                __uint_as_float(raw.x & 0xffff0000u) * up);
                                 const uint32_t w1 = pack_f16x2(__uint_as_float(raw.y << 16) * up,
@@ -994,7 +1118,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                         for (int ks = 0; ks < KT; ++ks) {
                             const int d0 = 32 * (ks >> 1) + 16 * (ks & 1) + 4 * c;
-                            const uint2 raw = *reinterpret_cast<const uint2 *>(qrow + d0 * 2);
+                            const uint2 raw = q_live(ks) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
                             qf[ks][n][0] = live_head ? raw.x : 0u;
                             qf[ks][n][1] = live_head ? raw.y : 0u;
                         }
@@ -1030,12 +1154,12 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
             ll[sub] = max(0, vlo - r0);
             any_act |= nl[sub] > ll[sub];
         }
+        float sv[SUBT][NT][4];
         if (any_act) {
             const uint32_t hstride = (uint32_t)(p.boxr * SUBROW);
             // ---------------------------------------------------------- S = K Q^T
             // Two independent accumulator chains per sub-tile (even / odd
             // k-steps) halve the dependent MMA latency of the dot products.
-            float sv[SUBT][NT][4];
 #pragma unroll
             for (int sub = 0; sub < SUBT; ++sub) {
                 const int r0 = (sub * NC + warp) * kTokensPerWarp;
@@ -1119,22 +1243,6 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                     sv[sub][n][1] = v01 ? (sv[sub][n][1] + s2[n][1]) * sc1 : -INFINITY;
                     sv[sub][n][2] = v10 ? (sv[sub][n][2] + s2[n][2]) * sc0 : -INFINITY;
                     sv[sub][n][3] = v11 ? (sv[sub][n][3] + s2[n][3]) * sc1 : -INFINITY;
-                    if constexpr (MODE == kScores) {
-                        // rows of the item's tokens: R = G * fold scores each
-                        const int R = p.G * p.fold;
-                        const int col = mt.hg * QROWS + n * 8 + 2 * c;
-                        const int tok = mt.t0 + r0 + g;
-                        float *to = p.scores + ((size_t)((size_t)mt.b * p.Hkv + mt.kvh) * p.cap + tok) * R + col;
-                        if (col < R) {
-                            const size_t o8 = (size_t)8 * R;
-                            if (v0) to[0] = sv[sub][n][0];
-                            if (v1) to[o8] = sv[sub][n][2];
-                            if (col + 1 < R) {
-                                if (v0) to[1] = sv[sub][n][1];
-                                if (v1) to[o8 + 1] = sv[sub][n][3];
-                            }
-                        }
-                    }
                 }
             }
 
@@ -1176,7 +1284,11 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 }
             }
             uint32_t pb[SUBT][NT][2];
-            uint32_t pl[SUBT][NT][2];  // bf16 V: low parts of the weights (P = hi + lo)
+            uint32_t pl[SUBT][NT][2];  // low parts of the weights (P = hi + lo): bf16 V, and
+                                       // f16 products outside the plain decode (not E4M3 K/V with
+                                       // bf16 q: 11 bits of a weight are below a bf16 output's
+                                       // rounding, and the second product would cost 16%)
+            constexpr bool kPair = KV == KV_BF16 || (MODE != kPlain && !(FP8 && QBF16));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float mn0 = mrow[n][0], mn1 = mrow[n][1];
@@ -1209,6 +1321,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                         const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&x0));
                         const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&x1));
                         wr0 = f0.x; wr1 = f0.y; wr2 = f1.x; wr3 = f1.y;
+                        if constexpr (kPair) {
+                            pl[sub][n][0] = movmatrix_t(pack_f16x2(p0 - f0.x, p1 - f0.y));
+                            pl[sub][n][1] = movmatrix_t(pack_f16x2(p2 - f1.x, p3 - f1.y));
+                        }
                     }
                     if constexpr (MODE == kPlain) {
                         add0 += wr0 + wr2;
@@ -1269,6 +1385,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                                 mma_bf16(o[mi][n], a0, a1, a2, a3, pl[sub][n][0], pl[sub][n][1]);
                             } else {
                                 mma_f16(o[mi][n], a0, a1, a2, a3, pb[sub][n][0], pb[sub][n][1]);
+                                if constexpr (kPair)
+                                    mma_f16(o[mi][n], a0, a1, a2, a3, pl[sub][n][0], pl[sub][n][1]);
                             }
                         }
                     }
@@ -1302,6 +1420,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                             for (int n = 0; n < NT; ++n) {
                                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                                 mma_f16(acc, A[hs][0], A[hs][1], A[hs][2], A[hs][3], pb[sub][n][0], pb[sub][n][1]);
+                                if constexpr (kPair)
+                                    mma_f16(acc, A[hs][0], A[hs][1], A[hs][2], A[hs][3], pl[sub][n][0], pl[sub][n][1]);
                                 float *od = o[2 * jg + hs][n];
                                 od[0] = fmaf(acc[0], vsc, od[0]);
                                 od[1] = fmaf(acc[1], vsc, od[1]);
@@ -1315,8 +1435,39 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
         // Release the stage (all reads of it are done); an item's last stage
         // holding the epilogue scratch is released after the epilogue.
         const int m_kvh = mt.kvh, m_s = mt.s, m_nsplit = mt.nsplit, m_hg = mt.hg, m_nrows = mt.nrows;
+        [[maybe_unused]] const int m_t0 = mt.t0;
         __syncwarp();
         if (lane == 0 && !(scr_in_stage && (flags & kFlagLast))) mbar_arrive(smem_u32(&empty_bar[st]));
+        if constexpr (MODE == kScores) {
+            // The tile's scores, R = G * fold a token: a whole sequence's into
+            // this CTA's own buffer (its totals are formed at the item's end),
+            // a split one's into the call's.  After the stage's release: they
+            // hold up no copy.
+            const int R = p.G * p.fold;
+            float *to = p.w_fused && m_nsplit == 1
+                            ? p.cta_scores + ((size_t)blockIdx.x * p.chunk + m_t0) * R
+                            : p.scores + (((size_t)mb * p.Hkv + m_kvh) * p.cap + m_t0) * R;
+#pragma unroll
+            for (int sub = 0; sub < SUBT; ++sub) {
+                const int row = (sub * NC + warp) * kTokensPerWarp + g;
+                const bool v0 = g >= ll[sub] && g < nl[sub], v1 = (g + 8) >= ll[sub] && (g + 8) < nl[sub];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int col = m_hg * QROWS + n * 8 + 2 * c;
+                    float *t0 = to + row * R + col, *t8 = t0 + 8 * R;
+                    const float *s = sv[sub][n];
+                    if ((R & 1) == 0) {
+                        if (v0 && col < R) *reinterpret_cast<float2 *>(t0) = make_float2(s[0], s[1]);
+                        if (v1 && col < R) *reinterpret_cast<float2 *>(t8) = make_float2(s[2], s[3]);
+                    } else {
+                        if (v0 && col < R) t0[0] = s[0];
+                        if (v0 && col + 1 < R) t0[1] = s[1];
+                        if (v1 && col < R) t8[0] = s[2];
+                        if (v1 && col + 1 < R) t8[1] = s[3];
+                    }
+                }
+            }
+        }
         if (++st == NST) { st = 0; ph ^= 1u; }
         if (!(flags & kFlagLast)) continue;
         // the stage just consumed: st - 1 (mod NST)
@@ -1424,6 +1575,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
             const size_t row = q_row(p, mb, m_kvh, m_hg, h, QROWS);
             if (m_nsplit == 1) {
                 scr_inv[h] = empty ? 0.f : 1.f / Ls;
+                if constexpr (MODE == kScores) scr_lse[h] = empty ? 0.f : M;
                 if (p.lse) p.lse[row] = empty ? -INFINITY : (M + __log2f(Ls)) * kLn2;
             } else {
                 scr_inv[h] = 1.f;
@@ -1432,8 +1584,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
             }
         }
         named_bar_sync(1, NC * 32);
-        for (int idx = tid; idx < G * (D / 4); idx += NC * 32) {
-            const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
+        // The warps' states of row h combined, outputs d .. d + 3.
+        auto combined = [&](int h, int d) {
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < NSLOT; ++w) {
@@ -1444,12 +1596,36 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 acc.z = fmaf(a, v.z, acc.z);
                 acc.w = fmaf(a, v.w, acc.w);
             }
-            const size_t row = q_row(p, mb, m_kvh, m_hg, h, QROWS);
-            if (m_nsplit == 1) {
-                const float inv = scr_inv[h];
-                store_out4(p.out, row * D + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv, p.out_dtype);
-            } else {
-                *reinterpret_cast<float4 *>(p.part_o + (row * p.S + m_s) * D + d) = acc;
+            return acc;
+        };
+        if constexpr (MODE == kDiff) {
+            // D / 4 lanes of a warp share a pair of rows; every lane of a warp
+            // goes round (the norm is a warp reduction).
+            const int total = G / 2 * (D / 4);
+            for (int i0 = warp * 32; i0 < total; i0 += NC * 32) {
+                const int idx = i0 + lane;
+                const bool in = idx < total;
+                const int h = in ? idx / (D / 4) * 2 : 0, d = (idx % (D / 4)) * 4;
+                const float4 a1 = combined(h, d), a2 = combined(h + 1, d);
+                const size_t row = q_row(p, mb, m_kvh, m_hg, h, QROWS);
+                if (m_nsplit == 1) {
+                    finish_pair<D>(p, row, d, a1, scr_inv[h], a2, scr_inv[h + 1], in);
+                } else if (in) {
+                    *reinterpret_cast<float4 *>(p.part_o + (row * p.S + m_s) * D + d) = a1;
+                    *reinterpret_cast<float4 *>(p.part_o + ((row + 1) * p.S + m_s) * D + d) = a2;
+                }
+            }
+        } else {
+            for (int idx = tid; idx < G * (D / 4); idx += NC * 32) {
+                const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
+                const float4 acc = combined(h, d);
+                const size_t row = q_row(p, mb, m_kvh, m_hg, h, QROWS);
+                if (m_nsplit == 1) {
+                    const float inv = scr_inv[h];
+                    store_out4(p.out, row * D + d, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv, p.out_dtype);
+                } else {
+                    *reinterpret_cast<float4 *>(p.part_o + (row * p.S + m_s) * D + d) = acc;
+                }
             }
         }
         if (m_nsplit > 1 && p.fuse_merge) {
@@ -1465,7 +1641,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
             }
             named_bar_sync(1, NC * 32);
             if (*scr_flag) {
-                merge_group<NC, FP8 ? 8 : 16>(p, mb, m_kvh, m_hg, m_nrows, QROWS, m_nsplit, scratch, warp, lane, D);
+                if constexpr (MODE == kDiff)
+                    merge_pairs<NC, D>(p, mb, m_kvh, m_hg, m_nrows, QROWS, m_nsplit, scratch, warp, lane);
+                else
+                    merge_group<NC, FP8 ? 8 : 16>(p, mb, m_kvh, m_hg, m_nrows, QROWS, m_nsplit, scratch, warp, lane, D);
                 if (tid == 0) atomicExch(p.merge_ctr + ((size_t)mb * p.Hkv + m_kvh) * p.nhg + m_hg, 0);
             }
         }
@@ -1491,6 +1670,16 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
         if (scr_in_stage) fence_proxy_async_shared();
         named_bar_sync(1, NC * 32);
         if (scr_in_stage && lane == 0) mbar_arrive(smem_u32(&empty_bar[(st == 0 ? NST : st) - 1]));
+        if constexpr (MODE == kScores) {
+            if (m_nsplit == 1 && p.w_fused) {
+                // The item was the whole sequence: its totals now, from the
+                // scores this CTA just wrote (still in L2) and the rows' max
+                // and denominator, while the producer fills the next item's
+                // stages.
+                add_weights<NC>(p, mb, m_kvh, lens[mb], scr_lse, scr_inv, tid);
+                named_bar_sync(1, NC * 32);  // the buffer and scr_* are the next item's
+            }
+        }
     }
 }
 

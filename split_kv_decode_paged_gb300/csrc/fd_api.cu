@@ -17,7 +17,7 @@ using LaunchDecode = cudaError_t(const fd_problem &, const KernelShape &, const 
                                  const CUtensorMap &, int, size_t, cudaStream_t);
 LaunchDecode launch_decode_f16, launch_decode_bf16, launch_decode_e4m3;
 LaunchDecode launch_decode_scores_f16, launch_decode_scores_bf16, launch_decode_scores_e4m3;  // scores out (weights.cu)
-LaunchDecode launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3;        // diff.cu
+LaunchDecode launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3;        // differential attention
 cudaError_t decode_occupancy_f16(const fd_problem &, const KernelShape &, size_t, int *);
 cudaError_t decode_occupancy_bf16(const fd_problem &, const KernelShape &, size_t, int *);
 cudaError_t decode_occupancy_e4m3(const fd_problem &, const KernelShape &, size_t, int *);
@@ -90,7 +90,7 @@ namespace {
 constexpr int kMaxStages = 8;
 // fd_plan_t::reserved[0]: what the plan was made for.
 constexpr int kPlanPlain = 0;
-constexpr int kPlanDiff = 1;  // fd_plan_diff; reserved[1] = fd_dtype of the output
+constexpr int kPlanDiff = 1;  // fd_plan_diff
 constexpr int kMaxQLen = 64;  // query tokens per sequence (multi-token mode)
 constexpr int kMinStages = 2;
 constexpr int kSmallGridItemTokens = 1024;  // small grids: two CTAs per SM for items up to this long
@@ -625,9 +625,9 @@ namespace {
 struct DecodeMode {
     const DecodeLaunchers *launch = &kPlainDecode;
     int kind = kPlanPlain;     // the plan's kind the call takes
-    float *scores = nullptr;   // kScoresDecode: where the scores go
     int score_width = 0;       // elements of q and k a score is formed over; 0 = D
-    const void *pair_q = nullptr;  // kDiffDecode: the query pairs, to be padded into the call's q
+    void (*fill)(DecodeParams &, const void *) = nullptr;  // sets the mode's own parameters
+    const void *args = nullptr;
 };
 
 fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
@@ -715,17 +715,14 @@ fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages,
     dp.stages = plan->stages;
     dp.scr_in_stage = plan->scratch_in_stage;
     dp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)(mode.score_width > 0 ? mode.score_width : p.D)));
-    dp.scores = mode.scores;
+    if (mode.fill) mode.fill(dp, mode.args);
     dp.timeout_ns = plan->timeout_us > 0 ? (uint64_t)plan->timeout_us * 1000ull : kTimeoutNs;
     dp.stall_ns = (uint64_t)plan->debug_stall_us * 1000ull;
     dp.stall_role = plan->debug_stall_role;
     dp.qn = q_len;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (mode.pair_q) e = launch_diff_expand(mode.pair_q, const_cast<void *>(q), (long long)p.B * (p.Hq / 2), p.D, s);
-    if (e != cudaSuccess) return FD_ERR_CUDA;
-    e = mode.launch->of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
+    cudaError_t e = mode.launch->of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
     if (e != cudaSuccess) return FD_ERR_CUDA;
     if (!plan->fuse_merge && plan->num_splits > 1) {
         MergeParams mp;
@@ -978,18 +975,27 @@ fd_status fd_append_kv_rotary(const fd_problem *problem, const void *k_new, cons
 
 namespace {
 
-// Byte layout of the weights workspace: lse, then the scores.
+// Byte layout of the weights workspace: lse, the scores of split rows (of all
+// rows where a KV head's query rows take several items), each CTA's scores.
 struct WeightsLayout {
-    size_t scores, bytes;
+    size_t scores, cta_scores, bytes;
+    bool fused;     // rows that are not split are finished by the decode kernel
+    bool separate;  // some rows are not
 };
 
 bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
     const fd_problem &p = plan->problem;
     if (validate_problem(&p) != FD_OK || plan->reserved[0] != kPlanPlain || plan->kv_rows < 1 || plan->row_fold < 1 ||
-        plan->kv_rows * plan->row_fold != p.B || plan->num_splits < 1 || plan->chunk_tokens < 1)
+        plan->kv_rows * plan->row_fold != p.B || plan->num_splits < 1 || plan->chunk_tokens < 1 || plan->grid_ctas < 1 ||
+        plan->head_subgroups < 1)
         return false;
+    const size_t row = (size_t)plan->chunk_tokens * sizeof(float);  // one chunk's scores of one query row
+    l->fused = plan->head_subgroups == 1;
+    l->separate = plan->num_splits > 1 || !l->fused;
     l->scores = align256((size_t)p.B * p.Hq * sizeof(float));
-    l->bytes = l->scores + align256((size_t)p.B * p.Hq * (size_t)plan->num_splits * (size_t)plan->chunk_tokens * sizeof(float));
+    l->cta_scores = l->scores + (l->separate ? align256((size_t)p.B * p.Hq * plan->num_splits * row) : 0);
+    l->bytes = l->cta_scores +
+               (l->fused ? align256((size_t)plan->grid_ctas * (p.Hq / p.Hkv) * plan->row_fold * row) : 0);
     return true;
 }
 
@@ -1035,16 +1041,31 @@ fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const vo
     const fd_problem &p = plan->problem;
     if (half_overlaps(weights, weights_out, (size_t)plan->kv_rows * p.Hkv * weights_stride)) return FD_ERR_INVALID_ARG;
     uint8_t *ww = static_cast<uint8_t *>(weights_workspace);
+    struct Args {
+        float *scores, *cta_scores, *out;
+        const float *in;
+        int stride, fused;
+    } wa = {reinterpret_cast<float *>(ww + l.scores), reinterpret_cast<float *>(ww + l.cta_scores), weights_out, weights,
+            weights_stride, l.fused ? 1 : 0};
     DecodeMode mode;
     mode.launch = &kScoresDecode;
-    mode.scores = reinterpret_cast<float *>(ww + l.scores);
+    mode.args = &wa;
+    mode.fill = [](DecodeParams &dp, const void *args) {
+        const Args &a = *static_cast<const Args *>(args);
+        dp.scores = a.scores;
+        dp.cta_scores = a.cta_scores;
+        dp.w_in = a.in;
+        dp.w_out = a.out;
+        dp.w_stride = a.stride;
+        dp.w_fused = a.fused;
+    };
     float *use_lse = lse ? lse : reinterpret_cast<float *>(ww);
     const fd_status r = decode_impl(plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, nullptr, out,
                                     use_lse, workspace, workspace_bytes, status_dev, stream, mode);
-    if (r != FD_OK) return r;
+    if (r != FD_OK || !l.separate) return r;
     WeightParams wp;
     std::memset(&wp, 0, sizeof(wp));
-    wp.scores = mode.scores;
+    wp.scores = wa.scores;
     wp.lse = use_lse;
     wp.in = weights;
     wp.out = weights_out;
@@ -1058,6 +1079,7 @@ fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const vo
     wp.R = wp.G * wp.fold;
     wp.cap = plan->num_splits * plan->chunk_tokens;
     wp.weights_stride = weights_stride;
+    wp.skip_to = l.fused ? plan->chunk_tokens : 0;
     return launch_weights(wp, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
@@ -1107,6 +1129,7 @@ fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *arg
     np.sin = a.rotary_sin;
     np.rotary_dim = a.rotary_cos ? a.rotary_dim : 0;
     np.max_pos = a.max_pos;
+    np.interleaved = a.interleaved ? 1 : 0;
     np.k_pages = k_pages;
     np.v_pages = v_pages;
     np.k_scale = k_scale;
@@ -1125,7 +1148,7 @@ fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *arg
     np.num_pages = p.num_pages;
     np.kv_kind = p.kv_dtype == FD_F16 ? KV_F16 : (p.kv_dtype == FD_BF16 ? KV_BF16 : KV_E4M3);
     np.is_bf16 = p.q_dtype == FD_BF16 ? 1 : 0;
-    const cudaError_t e = launch_append_norm(np, p.D, a.interleaved ? 1 : 0, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_append_norm(np, p.D, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FD_OK : (e == cudaErrorInvalidConfiguration ? FD_ERR_UNSUPPORTED : FD_ERR_CUDA);
 }
 
@@ -1183,26 +1206,6 @@ fd_status fd_evict_kv(const fd_problem *problem, void *k_pages, void *v_pages, c
 
 }  // extern "C"
 
-namespace {
-
-// Byte layout behind a differential plan's decode workspace: the padded
-// queries, both maps' outputs, and their lse.
-struct DiffLayout {
-    size_t q, o, lse, bytes;
-};
-
-DiffLayout diff_layout(const fd_problem &p) {  // p: the doubled problem
-    const size_t rows = (size_t)p.B * p.Hq;
-    DiffLayout l;
-    l.q = 0;
-    l.o = align256(rows * p.D * 2);
-    l.lse = l.o + align256(rows * p.D * sizeof(float));
-    l.bytes = l.lse + align256(rows * sizeof(float));
-    return l;
-}
-
-}  // namespace
-
 extern "C" {
 
 fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
@@ -1214,12 +1217,10 @@ fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host, 
     if (options && options->shared_kv) return FD_ERR_UNSUPPORTED;
     fd_problem p = *problem;
     p.Hq *= 2;
-    p.out_dtype = FD_F32;
     const fd_status r = fd_plan(&p, seq_lens_host, options, plan);
     if (r != FD_OK) return r;
+    plan->fuse_merge = 1;  // a pair's two states meet in the merge that finishes them
     plan->reserved[0] = kPlanDiff;
-    plan->reserved[1] = problem->out_dtype;
-    plan->workspace_bytes += diff_layout(plan->problem).bytes;
     return FD_OK;
 }
 
@@ -1232,41 +1233,33 @@ fd_status fd_decode_paged_diff(const fd_plan_t *plan, const void *q, const void 
     const fd_problem &p = plan->problem;
     const fd_status st = validate_problem(&p);
     if (st != FD_OK) return st;
-    const fd_dtype out_dtype = (fd_dtype)plan->reserved[1];
-    if (out_dtype != p.q_dtype && out_dtype != FD_F32) return FD_ERR_INVALID_ARG;
+    if ((p.Hq / p.Hkv) % 2 != 0 || plan->fuse_merge != 1) return FD_ERR_INVALID_ARG;
     if (!q || !lambda || !out || !workspace) return FD_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lambda, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
         return FD_ERR_INVALID_ARG;
     if (!norm_weight_ok(norm_weight, norm_weight_dtype, p.q_dtype)) return FD_ERR_INVALID_ARG;
     if (norm_weight && (!(eps > 0.f) || !std::isfinite(eps))) return FD_ERR_INVALID_ARG;
-    const DiffLayout l = diff_layout(p);
-    if (workspace_bytes < plan->workspace_bytes) return FD_ERR_WORKSPACE_TOO_SMALL;
-    if (plan->workspace_bytes < l.bytes) return FD_ERR_INVALID_ARG;
-    uint8_t *ws = static_cast<uint8_t *>(workspace) + (plan->workspace_bytes - l.bytes);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const long long rows = (long long)p.B * (p.Hq / 2);
+    struct Args {
+        const float *lambda;
+        const void *w;
+        int w_dtype;
+        float eps, scale;
+    } da = {lambda, norm_weight, norm_weight_dtype, eps, out_scale};
     DecodeMode mode;
     mode.launch = &kDiffDecode;
     mode.kind = kPlanDiff;
     mode.score_width = p.D / 2;
-    mode.pair_q = q;
-    const fd_status r = decode_impl(plan, ws + l.q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, nullptr,
-                                    ws + l.o, lse ? lse : reinterpret_cast<float *>(ws + l.lse), workspace,
-                                    workspace_bytes, status_dev, stream, mode);
-    if (r != FD_OK) return r;
-    DiffCombineParams dp;
-    std::memset(&dp, 0, sizeof(dp));
-    dp.o = reinterpret_cast<const float *>(ws + l.o);
-    dp.lambda = lambda;
-    dp.w = norm_weight;
-    dp.out = out;
-    dp.rows = rows;
-    dp.Hq = p.Hq / 2;
-    dp.w_dtype = norm_weight_dtype;
-    dp.out_dtype = out_dtype;
-    dp.eps = eps;
-    dp.out_scale = out_scale;
-    return launch_diff_combine(dp, p.D, s) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+    mode.args = &da;
+    mode.fill = [](DecodeParams &dp, const void *args) {
+        const Args &a = *static_cast<const Args *>(args);
+        dp.lambda = a.lambda;
+        dp.norm_w = a.w;
+        dp.norm_w_dtype = a.w_dtype;
+        dp.norm_eps = a.eps;
+        dp.out_scale = a.scale;
+    };
+    return decode_impl(plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, nullptr, out, lse, workspace,
+                       workspace_bytes, status_dev, stream, mode);
 }
 
 }  // extern "C"

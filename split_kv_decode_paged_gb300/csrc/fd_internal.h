@@ -59,7 +59,18 @@ struct DecodeParams {
     uint64_t stall_ns;         // test hook (0 = off): idle time of stall_role
     int stall_role;            // 1: producer before its first load; 2: consumers before the first release
     int qn;                    // query tokens per KV row, causal among them (1: one-token decode)
-    float *scores;             // [Bkv, Hkv, cap, G * fold] log2-unit scores, or null (the score-writing instances only)
+    // Score-writing instances (attention-weight totals) only.
+    float *scores;             // [Bkv, Hkv, cap, G * fold] log2-unit scores of rows that are split (or not w_fused)
+    float *cta_scores;         // w_fused: [grid, chunk, G * fold], each CTA's scores of its current whole row
+    const float *w_in;         // [Bkv, Hkv, w_stride] or null (zeros)
+    float *w_out;
+    int w_stride;
+    int w_fused;               // rows that are not split: totals formed by the decode kernel (nhg == 1)
+    // Differential instances only.
+    const float *lambda;       // [Hq / 2] (Hq counts the padded query rows)
+    const void *norm_w;        // [D] or null: no norm
+    int norm_w_dtype;
+    float norm_eps, out_scale;
 };
 
 // Attention-weight totals from the scores and lse of a decode call.
@@ -71,6 +82,7 @@ struct WeightParams {
     const int32_t *seq_lens;
     int *status;
     int Bkv, Hq, Hkv, G, fold, R, cap, weights_stride;
+    int skip_to;               // rows of at most this length were done by the decode kernel
     int chunk_tokens;          // tokens per CTA (set at launch)
 };
 
@@ -82,7 +94,7 @@ struct NormAppendParams {
     int w_f32;                 // norm weights in fp32 (else in q's type)
     float eps;
     const float *cos, *sin;    // null: no rotation
-    int rotary_dim, max_pos;
+    int rotary_dim, max_pos, interleaved;
     void *k_pages, *v_pages;
     const float *k_scale, *v_scale;
     const int32_t *block_table, *seq_lens, *positions, *new_lens;
@@ -91,6 +103,7 @@ struct NormAppendParams {
     int page_size, max_blocks, num_pages;
     int kv_kind, is_bf16;
     int parts;                 // warps per token (set at launch)
+    int w_vec;                 // both norm weights 8-byte aligned (set at launch)
 };
 
 struct EvictParams {
@@ -103,16 +116,6 @@ struct EvictParams {
     int *status;
     int B, Hkv, D, page_size, max_blocks, num_pages, row_bytes;
     int weights_stride, budget, sinks, recent;
-};
-
-struct DiffCombineParams {
-    const float *o;            // [2 rows, D]
-    const float *lambda;       // [Hq]
-    const void *w;             // [D] or null: no norm
-    void *out;                 // [rows, D]
-    long long rows;
-    int Hq, w_dtype, out_dtype;
-    float eps, out_scale;
 };
 
 struct MergeParams {
@@ -169,10 +172,8 @@ cudaError_t decode_occupancy(const fd_problem &p, const KernelShape &ks, size_t 
 cudaError_t launch_merge(const MergeParams &mp, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &ap, cudaStream_t stream);
 cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream);
-cudaError_t launch_append_norm(NormAppendParams p, int D, int interleaved, cudaStream_t stream);
+cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
-cudaError_t launch_diff_expand(const void *q, void *out, long long rows, int D, cudaStream_t stream);
-cudaError_t launch_diff_combine(const DiffCombineParams &p, int D, cudaStream_t stream);
 cudaError_t launch_merge_two(const float *oa, const float *la, const float *ob, const float *lb, int rows, int D,
                              int out_dtype, void *out, float *lse, cudaStream_t stream);
 

@@ -5,22 +5,23 @@
 // s_r(t) in log2 units (-inf where row r does not see t), R of them a token,
 // and lse.  A weight cannot be formed before the row's lse is known, and the
 // scores are 4 R bytes a token and KV head where K's row is up to 256.
-#include "fd_internal.h"
-#include "ptx.cuh"
+#include "weights.cuh"
 
 namespace fd {
 
-constexpr int kWeightThreads = 256;
+constexpr int kWeightThreads = 128;
+constexpr int kWeightFly = 8;  // tokens per thread: one round of loads a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 
 __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid_constant__ WeightParams p, int chunks) {
     grid_dependency_wait();
-    extern __shared__ float lse2[];  // R: the rows' lse in log2 units
+    extern __shared__ float lse2[];  // R: the rows' lse in log2 units, then R ones
     const long long bh = blockIdx.x / chunks;
     const int chunk = (int)(blockIdx.x % chunks);
     const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv);
     int L = p.seq_lens[b];
     if (L > p.cap) L = p.cap;  // flagged by the decode kernel
+    if (L <= p.skip_to) return;
     if (L > p.weights_stride) {
         if (threadIdx.x == 0 && chunk == 0 && h == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
         L = p.weights_stride;
@@ -29,26 +30,19 @@ __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid
     if (t0 >= t1) return;
     for (int r = threadIdx.x; r < p.R; r += kWeightThreads) {
         const size_t row = ((size_t)b * p.fold + r / p.G) * p.Hq + (size_t)h * p.G + r % p.G;
-        lse2[r] = p.lse[row] * kLog2e;
+        const float l = p.lse[row];
+        lse2[r] = l == -INFINITY ? 0.f : l * kLog2e;
+        lse2[p.R + r] = 1.f;
     }
     __syncthreads();
-    const float *sc = p.scores + (size_t)bh * p.cap * p.R;
-    const float *in = p.in ? p.in + (size_t)bh * p.weights_stride : nullptr;
-    float *out = p.out + (size_t)bh * p.weights_stride;
-    for (int t = t0 + threadIdx.x; t < t1; t += kWeightThreads) {
-        const float *s = sc + (size_t)t * p.R;
-        float sum = 0.f;
-        for (int r = 0; r < p.R; ++r) {
-            // a row that sees nothing has lse = -inf: it adds nothing
-            if (lse2[r] != -INFINITY) sum += ex2(s[r] - lse2[r]);
-        }
-        out[t] = in ? in[t] + sum : sum;
-    }
+    const size_t at = (size_t)bh * p.weights_stride;
+    sum_weights<kWeightThreads, kWeightFly>(p.scores + (size_t)bh * p.cap * p.R, p.R, lse2, lse2 + p.R,
+                                            p.in ? p.in + at : nullptr, p.out + at, t0, t1, threadIdx.x);
 }
 
 cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream) {
     WeightParams p = wp;
-    p.chunk_tokens = 4 * kWeightThreads;
+    p.chunk_tokens = kWeightFly * kWeightThreads;
     const long long chunks = (p.cap + p.chunk_tokens - 1) / p.chunk_tokens;
     const long long blocks = (long long)p.Bkv * p.Hkv * chunks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -58,7 +52,7 @@ cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kWeightThreads);
-    cfg.dynamicSmemBytes = (size_t)p.R * sizeof(float);
+    cfg.dynamicSmemBytes = (size_t)p.R * 2 * sizeof(float);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

@@ -26,7 +26,7 @@ class DiffDecoder:
         self.problem = problem
         self.plan = _lib.fd_plan_diff(problem, seq_lens_host, **plan_opts)
         self.device = torch.device(device)
-        self.workspace = torch.zeros(int(self.plan.workspace_bytes), dtype=torch.uint8, device=self.device)
+        self.workspace = torch.zeros(max(256, int(self.plan.workspace_bytes)), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     @classmethod
