@@ -496,8 +496,8 @@ fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const vo
  * true positions (fd_norm_append.positions).
  *   problem           Hkv, D, page_size, ..., kv_dtype (Hq is not used)
  *   weights           device fp32 [B, Hkv, weights_stride]
- *   weights_out       the kept weights, then zeros up to L (entries beyond L
- *                     are not written): weights itself, disjoint, or NULL
+ *   weights_out       the kept weights (a NaN is a NaN, -0 may be +0), then
+ *                     zeros up to L (entries beyond L are not written): weights itself, disjoint, or NULL
  *   dst_table         device int32 [B, max_blocks_per_seq]: the pages that
  *                     receive the rows, or NULL: the sequence's own, in place.
  *                     Given, it must name no page that block_table's live
@@ -508,8 +508,8 @@ fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const vo
  *                     order of every kept token, -1 past the new length
  * In place, no page that changes may belong to another sequence.  E4M3 codes
  * that move to a page with another scale become
- * e4m3_rne_satfinite(code * scale_from / scale_to), multiplied and divided in
- * fp32; the scales are not changed.
+ * e4m3_rne_satfinite(code * (scale_from / scale_to)), divided and multiplied
+ * in fp32; the scales are not changed.
  * A length outside [0, min(weights_stride, max_blocks_per_seq * page_size)]
  * sets FD_DEV_CAPACITY: the sequence is left as it was, new_lens[b] =
  * seq_lens[b], kept = -1.  A page out of range sets FD_DEV_BAD_PAGE and the

@@ -4,167 +4,286 @@
 // weights move up into the first n = min(L, budget) slots.  Every KV head
 // chooses its own tokens.
 //
-// Two launches.  fd_evict_select_kernel, one CTA per (sequence, KV head),
-// finds the smallest weight that stays (radix select over an order-preserving
-// 32-bit key, 8 bits a round) and lists the tokens that stay with a running
-// scan (ties: lowest index first).  fd_evict_move_*_kernel copies the rows.
+// Two launches.  fd_evict_select_kernel finds the smallest weight that stays
+// (radix select over an order-preserving 32-bit key, 11 + 11 + 10 bits) and
+// lists the tokens that stay in order (ties: lowest index first).
+// fd_evict_copy_kernel or fd_evict_shift_kernel moves the rows; it is launched
+// while the first still runs and waits for it.
+//
+// Selection is bound by instructions and by the rounds' latency, not by bytes:
+// a row's tokens are dealt to the CTAs of a cluster in tiles of 8192, one CTA
+// for short rows or many of them, up to 8 for few long ones, and a tile that
+// is a CTA's only one is read once and kept in registers as keys.  The CTAs
+// add up their histograms and counts through distributed shared memory.
+#include <algorithm>
+
 #include "fd_internal.h"
 #include "ptx.cuh"
 
 namespace fd {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelPer = 4;  // consecutive tokens per thread and tile of the scan
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelPer = 16;       // tokens per thread and tile: token base + k * kSelThreads + tid
+constexpr int kSelTile = kSelThreads * kSelPer;
+constexpr int kBins = 2048;       // 4 a thread
+constexpr int kMaxSelCtas = 8;    // portable cluster size
 constexpr int kMoveThreads = 256;
 
-// Unsigned key in the order of the weights: -0 counts as +0, NaN as the smallest.
+// Unsigned keys in the order of the weights: -0 counts as +0, NaN (key 1) as
+// the smallest; the smallest number, -inf, has 0x007fffff, the largest 0xff800000.
+constexpr uint32_t kKeyNan = 1u;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-    if (w != w) return 0u;
-    uint32_t u = __float_as_uint(w);
-    if (u == 0x80000000u) u = 0u;
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(w + 0.f);  // -0 + 0 = +0
+    const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return w == w ? key : kKeyNan;
+}
+// The weight of a key (a NaN loses its payload, -0 its sign).
+__device__ __forceinline__ float key_weight(uint32_t key) {
+    if (key == kKeyNan) return __uint_as_float(0x7fffffffu);
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-__global__ void __launch_bounds__(kSelThreads) fd_evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t warp_sum[kSelThreads / 32];
+// Exclusive prefix over the CTA of v (one value a thread) and its total; two
+// barriers, sums is scratch of kSelWarps words.
+__device__ __forceinline__ uint32_t cta_prefix(uint32_t v, uint32_t *sums, int warp, int lane, uint32_t &total) {
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    const uint32_t s = lane < kSelWarps ? sums[lane] : 0u;
+    uint32_t all = s;
+#pragma unroll
+    for (int o = 1; o < kSelWarps; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += x;
+    }
+    total = __shfl_sync(0xffffffffu, all, kSelWarps - 1);
+    const uint32_t before = __shfl_sync(0xffffffffu, all - s, warp);
+    __syncthreads();  // sums may be used again
+    return before + incl - v;
+}
+
+// A barrier of the cluster's CTAs that also publishes their shared memory.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Words at this CTA's shared address p, in the cluster's CTA `rank`.  (No
+// memory clobber: cluster_sync orders them, and several are to be in flight.)
+__device__ __forceinline__ uint32_t cluster_addr(const uint32_t *p, uint32_t rank) {
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    return addr;
+}
+__device__ __forceinline__ uint32_t cluster_read(const uint32_t *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)));
+    return v;
+}
+__device__ __forceinline__ uint4 cluster_read4(const uint32_t *p, uint32_t rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(cluster_addr(p, rank)));
+    return v;
+}
+
+// One cluster of `ctas` CTAs (a power of two) per (sequence, KV head); tile i * ctas + rank of
+// the row is CTA rank's in round i.  All branches that hold a barrier depend on
+// the row alone, so the cluster's CTAs take them together.
+__global__ void __launch_bounds__(kSelThreads, 2) fd_evict_select_kernel(const __grid_constant__ EvictParams p,
+                                                                        int ctas) {
+    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ uint32_t places[kSelPer * kSelWarps];  // counts of every (k, warp) of a tile, then their prefix
+    __shared__ uint32_t sums[kSelWarps];
+    __shared__ uint32_t tile_total[2];                // of rounds i and i + 1
     __shared__ uint32_t sh_bin, sh_left;
+    static_assert(kBins == 4 * kSelThreads && kSelPer * kSelWarps <= kSelThreads, "bins and places per thread");
+    grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = (int)(blockIdx.x / p.Hkv), h = (int)(blockIdx.x % p.Hkv);
-    const size_t row = (size_t)b * p.Hkv + h;
-    const float *w = p.weights + row * p.weights_stride;
-    float *wo = p.weights_out ? p.weights_out + row * p.weights_stride : nullptr;
-    int32_t *kept = p.kept + row * p.budget;
+    const long long bh = blockIdx.x / ctas;
+    const int rank = (int)(blockIdx.x % ctas);
+    const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv);
+    const float *w = p.weights + (size_t)bh * p.weights_stride;
+    float *wo = p.weights_out ? p.weights_out + (size_t)bh * p.weights_stride : nullptr;
+    int32_t *kept = p.kept + (size_t)bh * p.budget;
     const int L = p.seq_lens[b];
+    const int part = rank * kSelThreads + tid, parts = ctas * kSelThreads;  // of the cluster's threads
     if (L < 0 || L > p.weights_stride || (long long)L > (long long)p.max_blocks * p.page_size) {
         // nothing of this sequence is touched
-        for (int t = tid; t < p.budget; t += kSelThreads) kept[t] = -1;
-        if (tid == 0 && h == 0) {
+        for (int t = part; t < p.budget; t += parts) kept[t] = -1;
+        if (part == 0 && h == 0) {
             p.new_lens[b] = L;
             if (p.status) atomicOr(p.status, FD_DEV_CAPACITY);
         }
         return;
     }
     const int n = min(L, p.budget);
-    if (tid == 0 && h == 0) p.new_lens[b] = n;
-    for (int t = n + tid; t < p.budget; t += kSelThreads) kept[t] = -1;
+    if (part == 0 && h == 0) p.new_lens[b] = n;
+    for (int t = n + part; t < p.budget; t += parts) kept[t] = -1;
     if (L <= p.budget) {
-        for (int t = tid; t < L; t += kSelThreads) {
-            kept[t] = t;
-            if (wo && wo != w) wo[t] = w[t];
-        }
+        for (int t = part; t < L; t += parts) kept[t] = t;
+        if (wo && wo != w)
+            for (int t = part; t < L; t += parts) wo[t] = w[t];
         return;
     }
     const int mid0 = p.sinks, mid1 = L - p.recent;
     const int many = p.budget - p.sinks - p.recent;  // stay of [mid0, mid1); fewer than there are
+    const int round_tokens = ctas * kSelTile, first = rank * kSelTile;
+    const bool one_round = L <= round_tokens;
+    // Keys of the tile at hand; bit k of mid: token k is one to choose from, of
+    // always: it is among the first or last ones and stays.
+    uint32_t keys[kSelPer], mid = 0, always = 0;
+    auto load_tile = [&](int base) {
+        mid = always = 0;
+#pragma unroll
+        for (int k = 0; k < kSelPer; ++k) {
+            const int t = base + k * kSelThreads + tid;
+            keys[k] = t < L ? weight_key(w[t]) : 0u;
+            const bool in = t >= mid0 && t < mid1;
+            mid |= in ? 1u << k : 0u;
+            always |= (t < L && !in) ? 1u << k : 0u;
+        }
+    };
+    load_tile(first);
     uint32_t cut = 0xffffffffu;  // keys above it stay, and the first `ties` equal to it
     uint32_t ties = 0;
     if (many > 0) {
         uint32_t prefix = 0, mask = 0, left = (uint32_t)many;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
+#pragma unroll 1
+        for (int digits = 0; digits < 3; ++digits) {
+            const int shift = digits == 0 ? 21 : (digits == 1 ? 10 : 0);
+            const uint32_t digit = digits == 2 ? 1023u : 2047u;
+            *reinterpret_cast<uint4 *>(&hist[4 * tid]) = make_uint4(0u, 0u, 0u, 0u);
             __syncthreads();
-            for (int t = mid0 + tid; t < mid1; t += kSelThreads) {
-                const uint32_t k = weight_key(w[t]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // bins from the top, 8 per lane: the one where the count reaches `left`
-                uint32_t c[8], sum = 0;
+#pragma unroll 1
+            for (int base = first; base < L; base += round_tokens) {
+                if (!one_round) load_tile(base);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    c[e] = hist[255 - (lane * 8 + e)];
-                    sum += c[e];
-                }
-                uint32_t incl = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += v;
-                }
-                uint32_t above = incl - sum;
-                if (above < left && incl >= left) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (above < left && above + c[e] >= left) {
-                            sh_bin = 255u - (uint32_t)(lane * 8 + e);
-                            sh_left = left - above;
-                        }
-                        above += c[e];
-                    }
+                for (int k = 0; k < kSelPer; ++k) {
+                    const uint32_t key = keys[k];
+                    if ((mid >> k & 1u) && ((key ^ prefix) & mask) == 0u)
+                        atomicAdd(&hist[(key >> shift) & digit], 1u);
                 }
             }
-            __syncthreads();
+            if (ctas > 1) cluster_sync(); else __syncthreads();
+            // the bin, from the top, where the cluster's count reaches `left`
+            uint32_t c[4];  // bins kBins - 1 - 4 tid and down
+            {
+                const uint32_t *mine = &hist[kBins - 4 - 4 * tid];
+                uint4 v[kMaxSelCtas];
+                v[0] = *reinterpret_cast<const uint4 *>(mine);
+#pragma unroll
+                for (int r = 1; r < kMaxSelCtas; ++r)
+                    v[r] = r < ctas ? cluster_read4(mine, (uint32_t)((rank + r) & (ctas - 1))) : make_uint4(0u, 0u, 0u, 0u);
+                c[0] = c[1] = c[2] = c[3] = 0u;
+#pragma unroll
+                for (int r = 0; r < kMaxSelCtas; ++r) {
+                    c[0] += v[r].w;
+                    c[1] += v[r].z;
+                    c[2] += v[r].y;
+                    c[3] += v[r].x;
+                }
+            }
+            uint32_t total;
+            uint32_t above = cta_prefix(c[0] + c[1] + c[2] + c[3], sums, warp, lane, total);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (above < left && above + c[e] >= left) {
+                    sh_bin = (uint32_t)(kBins - 1 - 4 * tid - e);
+                    sh_left = left - above;
+                }
+                above += c[e];
+            }
+            if (ctas > 1) cluster_sync(); else __syncthreads();  // read everywhere: hist may be cleared
             prefix |= sh_bin << shift;
-            mask |= 255u << shift;
+            mask |= digit << shift;
             left = sh_left;
         }
         cut = prefix;
         ties = left;
     }
     // Places in order: a token that stays goes to (tokens before it that stay
-    // for certain) + min(equal ones before it, ties).
+    // for certain) + min(equal ones before it, ties).  Place and weight of a
+    // token never lie behind it, and every weight of a round is read before
+    // any is written, so the weights may move up in place.
     uint32_t sure_run = 0, tie_run = 0;
-    for (int base = 0; base < L; base += kSelThreads * kSelPer) {
-        float wv[kSelPer];
-        bool sure[kSelPer], tie[kSelPer];
-        uint32_t mine = 0;  // certain ones in the low half, ties in the high half
+    int parity = 0;
+#pragma unroll 1
+    for (int round = 0; round < L; round += round_tokens, parity ^= 1) {
+        const int base = round + first;
+        if (!one_round) load_tile(base);
+        uint32_t stay = always, tied = 0;  // bit k: token k stays for certain, or ties
 #pragma unroll
-        for (int e = 0; e < kSelPer; ++e) {
-            const int t = base + tid * kSelPer + e;
-            wv[e] = t < L ? w[t] : 0.f;
-            const bool inside = t >= mid0 && t < mid1;
-            const uint32_t k = weight_key(wv[e]);
-            sure[e] = t < L && (!inside || (many > 0 && k > cut));
-            tie[e] = t < L && inside && many > 0 && k == cut;
-            mine += (sure[e] ? 1u : 0u) + (tie[e] ? 0x10000u : 0u);
+        for (int k = 0; k < kSelPer; ++k) {
+            stay |= keys[k] > cut ? mid & 1u << k : 0u;
+            tied |= keys[k] == cut ? mid & 1u << k : 0u;
         }
-        uint32_t incl = mine;
+        // counts of both (low and high half), at most kSelTile of each
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+        for (int k = 0; k < kSelPer; ++k) {
+            const uint32_t both = (uint32_t)__popc(__ballot_sync(0xffffffffu, stay >> k & 1u)) |
+                                  ((uint32_t)__popc(__ballot_sync(0xffffffffu, tied >> k & 1u)) << 16);
+            if (lane == 0) places[k * kSelWarps + warp] = both;
         }
-        if (lane == 31) warp_sum[warp] = incl;
-        __syncthreads();  // also: every weight of this tile has been read
-        uint32_t before = 0, total = 0;
+        __syncthreads();
+        uint32_t total;
+        const uint32_t mine = tid < kSelPer * kSelWarps ? places[tid] : 0u;
+        const uint32_t at = cta_prefix(mine, sums, warp, lane, total);
+        if (tid < kSelPer * kSelWarps) places[tid] = at;
+        if (tid == 0) tile_total[parity] = total;
+        if (ctas > 1) cluster_sync(); else __syncthreads();
+        uint32_t sure0 = sure_run, tie0 = tie_run;  // of this CTA's tile
+        {
+            uint32_t x[kMaxSelCtas];
 #pragma unroll
-        for (int k = 0; k < kSelThreads / 32; ++k) {
-            const uint32_t v = warp_sum[k];
-            before += k < warp ? v : 0u;
-            total += v;
-        }
-        uint32_t sure_at = sure_run + ((before + incl - mine) & 0xffffu);
-        uint32_t tie_at = tie_run + ((before + incl - mine) >> 16);
+            for (int r = 0; r < kMaxSelCtas; ++r)
+                x[r] = r < ctas ? (ctas > 1 ? cluster_read(&tile_total[parity], (uint32_t)r) : total) : 0u;
 #pragma unroll
-        for (int e = 0; e < kSelPer; ++e) {
-            if (sure[e] || (tie[e] && tie_at < ties)) {
-                const uint32_t to = sure_at + min(tie_at, ties);
-                kept[to] = base + tid * kSelPer + e;
-                if (wo) wo[to] = wv[e];
+            for (int r = 0; r < kMaxSelCtas; ++r) {
+                sure_run += x[r] & 0xffffu;
+                tie_run += x[r] >> 16;
+                if (r < rank) {
+                    sure0 = sure_run;
+                    tie0 = tie_run;
+                }
             }
-            sure_at += sure[e] ? 1u : 0u;
-            tie_at += tie[e] ? 1u : 0u;
         }
-        sure_run += total & 0xffffu;
-        tie_run += total >> 16;
-        __syncthreads();  // warp_sum is used again
+#pragma unroll
+        for (int k = 0; k < kSelPer; ++k) {
+            const bool sure = stay >> k & 1u, tie = tied >> k & 1u;
+            const unsigned sb = __ballot_sync(0xffffffffu, sure), tb = __ballot_sync(0xffffffffu, tie);
+            const unsigned below = (1u << lane) - 1u;
+            const uint32_t start = places[k * kSelWarps + warp];
+            const uint32_t tie_at = tie0 + (start >> 16) + __popc(tb & below);
+            if (sure || (tie && tie_at < ties)) {
+                const uint32_t to = sure0 + (start & 0xffffu) + __popc(sb & below) + min(tie_at, ties);
+                kept[to] = base + k * kSelThreads + tid;
+                if (wo) wo[to] = key_weight(keys[k]);
+            }
+        }
+        __syncthreads();  // places are used again
     }
     if (wo)
-        for (int t = n + tid; t < L; t += kSelThreads) wo[t] = 0.f;
+        for (int t = n + part; t < L; t += parts) wo[t] = 0.f;
+    if (ctas > 1) cluster_sync();  // no CTA leaves while its counts are read
 }
 
 struct RowPlace {
-    long long src, dst;  // row index (page * page_size + slot) * Hkv + h; src < 0: nothing to copy
-    float k_from, k_to, v_from, v_to;
+    long long src, dst;      // byte offsets in the pools; src < 0: nothing to copy
+    float k_ratio, v_ratio;  // E4M3: scale of the old page / scale of the new one (1: the codes stay)
 };
 
 // Where row j of (b, h) comes from and goes to.
-__device__ __forceinline__ RowPlace place_row(const EvictParams &p, int b, int h, const int32_t *kept, int j, bool fp8) {
+template <int RB, bool FP8>
+__device__ __forceinline__ RowPlace place_row(const EvictParams &p, int b, int h, const int32_t *kept, int j) {
     RowPlace r;
     r.src = r.dst = -1;
-    r.k_from = r.k_to = r.v_from = r.v_to = 1.f;
+    r.k_ratio = r.v_ratio = 1.f;
     const int t = kept[j];
     if (t < 0) return r;
     const int c0 = t / p.page_size, c1 = j / p.page_size;
@@ -177,19 +296,20 @@ __device__ __forceinline__ RowPlace place_row(const EvictParams &p, int b, int h
     const long long src = ((long long)p0 * p.page_size + (t - c0 * p.page_size)) * p.Hkv + h;
     const long long dst = ((long long)p1 * p.page_size + (j - c1 * p.page_size)) * p.Hkv + h;
     if (src == dst) return r;
-    r.src = src;
-    r.dst = dst;
-    if (fp8) {
-        r.k_from = __ldg(p.k_scale + (size_t)p0 * p.Hkv + h);
-        r.k_to = __ldg(p.k_scale + (size_t)p1 * p.Hkv + h);
-        r.v_from = __ldg(p.v_scale + (size_t)p0 * p.Hkv + h);
-        r.v_to = __ldg(p.v_scale + (size_t)p1 * p.Hkv + h);
+    r.src = src * RB;
+    r.dst = dst * RB;
+    if constexpr (FP8) {
+        const size_t s0 = (size_t)p0 * p.Hkv + h, s1 = (size_t)p1 * p.Hkv + h;
+        r.k_ratio = __fdiv_rn(__ldg(p.k_scale + s0), __ldg(p.k_scale + s1));
+        r.v_ratio = __fdiv_rn(__ldg(p.v_scale + s0), __ldg(p.v_scale + s1));
     }
     return r;
 }
 
-// 16 E4M3 codes of a page with scale `from`, as codes of a page with scale `to`.
-__device__ __forceinline__ uint4 rescale16(uint4 v, float from, float to) {
+// 16 E4M3 codes times the ratio of their pages' scales, rounded to codes again.
+// One product per code: a division for each instead made the copy of E4M3
+// rows twice as slow as its bytes.
+__device__ __forceinline__ uint4 rescale16(uint4 v, float ratio) {
     uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -198,8 +318,7 @@ __device__ __forceinline__ uint4 rescale16(uint4 v, float from, float to) {
         for (int hh = 0; hh < 2; ++hh) {
             const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(w[k] >> (16 * hh)));
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-            out |= (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(__fmul_rn(f.y, from), to), __fdiv_rn(__fmul_rn(f.x, from), to))
-                   << (16 * hh);
+            out |= (uint32_t)f32x2_to_e4m3x2(f.y * ratio, f.x * ratio) << (16 * hh);
         }
         w[k] = out;
     }
@@ -208,53 +327,66 @@ __device__ __forceinline__ uint4 rescale16(uint4 v, float from, float to) {
 
 constexpr int kCopyRows = 64;
 
-// Into other pages: no row is read and written, so every CTA copies kCopyRows
-// rows of K and V at their full width.
+// Into other pages: no row is both read and written, so every CTA copies
+// kCopyRows rows of K and V at their full width, all of them in flight.
+template <int RB, bool FP8>
 __global__ void __launch_bounds__(kMoveThreads) fd_evict_copy_kernel(const __grid_constant__ EvictParams p, int chunks) {
+    constexpr int UPR = RB / 16;                        // 16-byte units of a row
+    constexpr int ROWS = kMoveThreads / UPR;            // rows of one step
+    constexpr int STEPS = (kCopyRows + ROWS - 1) / ROWS;
     __shared__ RowPlace rows[kCopyRows];
+    grid_dependency_wait();
     const long long bh = blockIdx.x / chunks;
     const int j0 = (int)(blockIdx.x % chunks) * kCopyRows;
     const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv);
     const int n = min(p.new_lens[b], p.budget);
     if (j0 >= n) return;
-    const bool fp8 = p.row_bytes == p.D;
     const int32_t *kept = p.kept + (size_t)bh * p.budget;
     if (threadIdx.x < kCopyRows) {
         const int j = j0 + threadIdx.x;
-        if (j < n) rows[threadIdx.x] = place_row(p, b, h, kept, j, fp8);
+        if (j < n) rows[threadIdx.x] = place_row<RB, FP8>(p, b, h, kept, j);
         else rows[threadIdx.x].src = -1;
     }
     __syncthreads();
-    const int upr = p.row_bytes / 16;  // 16-byte units per row
-    const int units = kCopyRows * upr;
-    for (int u = threadIdx.x; u < 2 * units; u += kMoveThreads) {
-        const bool is_v = u >= units;
-        const int x = is_v ? u - units : u;
-        const RowPlace &r = rows[x / upr];
-        if (r.src < 0) continue;
-        uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages);
-        const int off = (x % upr) * 16;
-        uint4 v = *reinterpret_cast<const uint4 *>(pool + r.src * p.row_bytes + off);
-        if (fp8) {
-            const float from = is_v ? r.v_from : r.k_from, to = is_v ? r.v_to : r.k_to;
-            if (from != to) v = rescale16(v, from, to);
+    const int off = (threadIdx.x % UPR) * 16, first = threadIdx.x / UPR;
+    uint8_t *kp = reinterpret_cast<uint8_t *>(p.k_pages) + off, *vp = reinterpret_cast<uint8_t *>(p.v_pages) + off;
+    uint4 k[STEPS], v[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int r = first + s * ROWS;
+        const long long src = r < kCopyRows ? rows[r].src : -1;
+        if (src >= 0) {
+            k[s] = *reinterpret_cast<const uint4 *>(kp + src);
+            v[s] = *reinterpret_cast<const uint4 *>(vp + src);
         }
-        *reinterpret_cast<uint4 *>(pool + r.dst * p.row_bytes + off) = v;
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int r = first + s * ROWS;
+        if (r >= kCopyRows || rows[r].src < 0) continue;
+        if constexpr (FP8) {
+            if (rows[r].k_ratio != 1.f) k[s] = rescale16(k[s], rows[r].k_ratio);
+            if (rows[r].v_ratio != 1.f) v[s] = rescale16(v[s], rows[r].v_ratio);
+        }
+        const long long dst = rows[r].dst;
+        *reinterpret_cast<uint4 *>(kp + dst) = k[s];
+        *reinterpret_cast<uint4 *>(vp + dst) = v[s];
     }
 }
 
 // In place: row j comes from row kept[j] >= j of the same sequence, so rows
 // are moved in order, a chunk of them read before any of it is written.  What
 // can run at once is the width: a CTA takes one slice of K's or V's row.
+template <int RB, bool FP8>
 __global__ void __launch_bounds__(kMoveThreads) fd_evict_shift_kernel(const __grid_constant__ EvictParams p, int slices) {
     __shared__ RowPlace rows[kMoveThreads];
+    grid_dependency_wait();
     const long long bh = blockIdx.x / (2 * slices);
     const int part = (int)(blockIdx.x % (2 * slices));
     const bool is_v = part >= slices;
     const int sl = is_v ? part - slices : part;
     const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv);
     const int n = min(p.new_lens[b], p.budget);
-    const bool fp8 = p.row_bytes == p.D;
     const int32_t *kept = p.kept + (size_t)bh * p.budget;
     if (n <= 0 || kept[n - 1] <= n - 1) return;  // nothing left out: nothing moves
     // the first row that moves (kept[j] - j never falls)
@@ -263,31 +395,49 @@ __global__ void __launch_bounds__(kMoveThreads) fd_evict_shift_kernel(const __gr
         const int mid = (lo + hi) >> 1;
         if (kept[mid] > mid) hi = mid; else lo = mid + 1;
     }
-    uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages);
-    const int ups = p.row_bytes / slices / 16;  // 16-byte units of the slice
-    const int per = kMoveThreads / ups;         // rows per chunk
-    const int rl = threadIdx.x / ups, off = sl * (p.row_bytes / slices) + (threadIdx.x % ups) * 16;
+    const int ups = RB / slices / 16;    // 16-byte units of the slice
+    const int per = kMoveThreads / ups;  // rows per chunk
+    const int rl = threadIdx.x / ups;
+    uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) + sl * (RB / slices) +
+                    (threadIdx.x % ups) * 16;
     for (int j0 = lo; j0 < n; j0 += per) {
         __syncthreads();
         if (threadIdx.x < per) {
             const int j = j0 + threadIdx.x;
-            if (j < n) rows[threadIdx.x] = place_row(p, b, h, kept, j, fp8);
+            if (j < n) rows[threadIdx.x] = place_row<RB, FP8>(p, b, h, kept, j);
             else rows[threadIdx.x].src = -1;
         }
         __syncthreads();
         const RowPlace r = rows[rl];
         uint4 v;
-        if (r.src >= 0) v = *reinterpret_cast<const uint4 *>(pool + r.src * p.row_bytes + off);
+        if (r.src >= 0) v = *reinterpret_cast<const uint4 *>(pool + r.src);
         __syncthreads();  // the chunk is read
         if (r.src >= 0) {
-            if (fp8) {
-                const float from = is_v ? r.v_from : r.k_from, to = is_v ? r.v_to : r.k_to;
-                if (from != to) v = rescale16(v, from, to);
-            }
-            *reinterpret_cast<uint4 *>(pool + r.dst * p.row_bytes + off) = v;
+            const float ratio = is_v ? r.v_ratio : r.k_ratio;
+            if (FP8 && ratio != 1.f) v = rescale16(v, ratio);
+            *reinterpret_cast<uint4 *>(pool + r.dst) = v;
         }
     }
 }
+
+namespace {
+
+template <int RB, bool FP8>
+cudaError_t launch_move(const EvictParams &p, bool in_place, int per_row, unsigned blocks, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (in_place) return cudaLaunchKernelEx(&cfg, fd_evict_shift_kernel<RB, FP8>, p, per_row);
+    return cudaLaunchKernelEx(&cfg, fd_evict_copy_kernel<RB, FP8>, p, per_row);
+}
+
+}  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
     const long long bh = (long long)p.B * p.Hkv;
@@ -298,14 +448,32 @@ cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
     while (slices * 32 < p.row_bytes && bh * 2 * slices < 2LL * sms) slices *= 2;
     const long long blocks = in_place ? bh * 2 * slices : bh * chunks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    fd_evict_select_kernel<<<(unsigned)bh, kSelThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (in_place)
-        fd_evict_shift_kernel<<<(unsigned)blocks, kMoveThreads, 0, stream>>>(p, slices);
-    else
-        fd_evict_copy_kernel<<<(unsigned)blocks, kMoveThreads, 0, stream>>>(p, (int)chunks);
-    return cudaGetLastError();
+    // CTAs per row: up to one per tile of the longest row there can be, while
+    // all of them still run at once.
+    const long long longest = std::min<long long>(p.weights_stride, (long long)p.max_blocks * p.page_size);
+    int ctas = 1;
+    while (ctas < kMaxSelCtas && (long long)ctas * kSelTile < longest && bh * ctas * 2 <= 2LL * sms) ctas *= 2;
+    if (bh * ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(bh * ctas));
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, fd_evict_select_kernel, p, ctas);
+        if (e != cudaSuccess) return e;
+    }
+    const int per_row = in_place ? slices : (int)chunks;
+    const bool fp8 = p.row_bytes == p.D;
+    if (p.row_bytes == 256) return launch_move<256, false>(p, in_place, per_row, (unsigned)blocks, stream);
+    if (p.row_bytes == 64) return launch_move<64, true>(p, in_place, per_row, (unsigned)blocks, stream);
+    return fp8 ? launch_move<128, true>(p, in_place, per_row, (unsigned)blocks, stream)
+               : launch_move<128, false>(p, in_place, per_row, (unsigned)blocks, stream);
 }
 
 }  // namespace fd

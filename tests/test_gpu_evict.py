@@ -60,8 +60,8 @@ def check(kv, lens, Hkv, D, ps, budget, sinks, recent, fresh, seed=0, w=None, we
                     continue
                 a, z = sc[p0, h][:, None], sc[p1, h][:, None]
                 x = old.view(torch.uint8)[p0, s0, h].view(DT[kv]).float()
-                want = (x * a / z).clamp(-448, 448).to(DT[kv]).view(torch.uint8)
-                same = (a == z).expand_as(x)
+                want = (x * (a / z)).clamp(-448, 448).to(DT[kv]).view(torch.uint8)
+                same = (a / z == 1).expand_as(x)
                 want = torch.where(same, old.view(torch.uint8)[p0, s0, h], want)
                 assert torch.equal(new.view(torch.uint8)[p1, s1, h], want)
             if wout is not None:
