@@ -9,6 +9,8 @@ binds it with ctypes and uses PyTorch only for device memory and streams.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -81,6 +83,12 @@ class PagedDecoder:
         track_weights=True.  Returns (out, lse, weights_out)."""
         if self.weights_workspace is None:
             raise ValueError("decode_weights: make the decoder with track_weights=True")
+        if stream is None and (fast := _lib.fast()):
+            done = fast.decode_weights(ctypes.addressof(self.plan), q, k_pages, v_pages, block_table, seq_lens, weights,
+                                       weights_out, k_scale, v_scale, out, lse, want_lse, self.workspace,
+                                       self.weights_workspace, self.status)
+            if done is not None:
+                return done
         p, plan = self.problem, self.plan
         lead = (p.B,) if plan.q_len <= 1 else (p.B, plan.q_len)
         if weights_out is None:

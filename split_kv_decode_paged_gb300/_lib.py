@@ -8,6 +8,11 @@ fd_decode_paged_weights, fd_evict_kv, fd_plan_diff, fd_decode_paged_diff, ...). 
 data_ptr(); the stream is torch's current CUDA stream unless given.  No
 computation happens here and there is no fallback: if libfd.so is missing or
 fails to load, every call raises.
+
+The calls a serving loop makes once a layer and step (append_kv_norm,
+evict_kv, PagedDecoder.decode_weights, DiffDecoder) first try fast(), the same
+marshalling in C++; it hands back every call that is not the ordinary case,
+and the functions here then check it, name what is wrong and raise.
 """
 from __future__ import annotations
 
@@ -149,6 +154,26 @@ def load(path: str = LIB_PATH):
     L.fd_api_version.argtypes = []
     _lib = L
     return L
+
+
+_fast = None  # module, or False where it is not built
+
+
+def fast():
+    """The native marshalling of libfd.so's hot calls, or False."""
+    global _fast
+    if _fast is None:
+        lib = load()
+        try:
+            from . import _fd_torch
+        except ImportError:
+            _fast = False
+        else:
+            at = [ctypes.cast(f, ctypes.c_void_p).value for f in
+                  (lib.fd_append_kv_norm, lib.fd_evict_kv, lib.fd_decode_paged_weights, lib.fd_decode_paged_diff)]
+            _fd_torch.init(*at)
+            _fast = _fd_torch
+    return _fast
 
 
 def _ptr(t):

@@ -2,7 +2,9 @@
 
 One -gencode (sm_103a), translation units compiled in parallel, then linked
 into split_kv_decode_paged_gb300/libfd.so.  No cmake, no torch extension
-machinery: the library is plain C ABI over the CUDA runtime.
+machinery: the library is plain C ABI over the CUDA runtime.  Beside it the
+host compiler builds _fd_torch.so (csrc/torch_binding.cpp), the native
+marshalling of the calls made once a layer and step.
 """
 import concurrent.futures as cf
 import os
@@ -14,6 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfd.so")
+BINDING = os.path.join(HERE, "_fd_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["fd_api.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e4m3.cu", "decode_scores_f16.cu",
            "decode_scores_bf16.cu", "decode_scores_e4m3.cu", "decode_diff_f16.cu", "decode_diff_bf16.cu",
@@ -34,10 +37,33 @@ def _deps():
     return files
 
 
+def build_binding() -> str:
+    """Compile _fd_torch.so against the installed torch; returns its path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    inc = cpp_extension.include_paths() + [cuda, sysconfig.get_paths()["include"]]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [a for i in inc for a in ("-isystem", i)] + [os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp]
+    cmd += [f"-L{d}" for d in cpp_extension.library_paths()] + ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for torch_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA source for sm_103a and link libfd.so; returns its path."""
+    """Compile every CUDA source for sm_103a and link libfd.so, and the torch
+    binding beside it; returns the library's path."""
     newest = max(os.path.getmtime(f) for f in _deps())
-    if not force and not verbose_ptxas and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
+    if not force and not verbose_ptxas and all(os.path.exists(f) and os.path.getmtime(f) >= newest
+                                               for f in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -54,8 +80,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)

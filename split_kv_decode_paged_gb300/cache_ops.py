@@ -25,6 +25,12 @@ def append_kv_norm(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, q_w
     token (None: seq_lens, right while nothing was evicted); new_lens int32
     [B]: tokens of each sequence in this call (None: T; rows of q_out beyond
     are not written).  seq_lens is not advanced."""
+    if stream is None and (fast := _lib.fast()):
+        done = fast.append_kv_norm(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, q_weight, k_weight, eps,
+                                   rotary_cos, rotary_sin, interleaved, positions, new_lens, k_scale, v_scale, q_out,
+                                   status)
+        if done is not None:
+            return done[0]
     if not isinstance(k_new, torch.Tensor) or k_new.dim() not in (3, 4):
         raise ValueError("append_kv_norm: k_new must be a tensor [B, T, Hkv, D] or [B, Hkv, D]")
     if q is not None and (not isinstance(q, torch.Tensor) or q.dim() != k_new.dim()):
@@ -52,6 +58,11 @@ def evict_kv(k_pages, v_pages, block_table, seq_lens, weights, budget, sinks=0, 
     block_table must not name.  weights_out (weights for in place; None: not
     kept) receives the kept weights.  Returns (new_lens int32 [B], kept int32
     [B, Hkv, budget], the old indices, -1 past a row's new length)."""
+    if stream is None and (fast := _lib.fast()):
+        done = fast.evict_kv(k_pages, v_pages, block_table, seq_lens, weights, budget, sinks, recent, dst_table,
+                             weights_out, k_scale, v_scale, status)
+        if done is not None:
+            return done
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("evict_kv: k_pages must be a tensor [num_pages, page_size, Hkv, D]")
     num_pages, page_size, Hkv, D = k_pages.shape

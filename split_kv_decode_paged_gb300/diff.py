@@ -12,6 +12,8 @@ the weights; out_scale its 1 - lam_init.  All compute runs in libfd.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -46,6 +48,12 @@ class DiffDecoder:
                  k_scale=None, v_scale=None, out=None, lse=None, want_lse=True, stream=None):
         """lam fp32 [Hq]; norm_weight [D] in q's type or fp32 (None: no norm).
         Returns (out like q, lse fp32 [..., Hq, 2] of both maps or None)."""
+        if stream is None and (fast := _lib.fast()):
+            done = fast.decode_diff(ctypes.addressof(self.plan), q, k_pages, v_pages, block_table, seq_lens, lam,
+                                    norm_weight, eps, out_scale, k_scale, v_scale, out, lse, want_lse, self.workspace,
+                                    self.status)
+            if done is not None:
+                return done
         p, plan = self.problem, self.plan
         lead = (p.B,) if plan.q_len <= 1 else (p.B, plan.q_len)
         if out is None:
