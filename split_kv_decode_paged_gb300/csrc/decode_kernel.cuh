@@ -562,6 +562,13 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     // [q1 | 0] and [0 | q2] of one head; memory holds [q1 | q2].  All the
     // counts of rows here are of the padded ones (even in number).
     constexpr int kQRowsPerHead = MODE == kDiff ? 2 : 1;
+    // With two tiles of query columns the first takes the [q1 | 0] rows and
+    // the second the [0 | q2] rows of the item's 8 heads, so each tile needs
+    // half of the K Q^T products and fragments; with one, rows lie in order.
+    constexpr bool kMapTiles = MODE == kDiff && NT == 2;
+    // Column slot (8 n + column of tile n) of query row h of the item, and back.
+    auto slot_of = [](int h) { return kMapTiles ? (h & 1) * 8 + (h >> 1) : h; };
+    auto row_of = [](int slot) { return kMapTiles ? (slot & 7) * 2 + (slot >> 3) : slot; };
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1041,18 +1048,20 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
         if (flags & kFlagFirst) {
             // Query fragments (B operand of QK), zero for padded heads and, in
             // a differential item, for the half that is not this row's.
-            auto q_live = [&](int ks) { return MODE != kDiff || (ks < KT / 2) == ((g & 1) == 0); };
+            auto q_live = [&](int ks, int n) {
+                return MODE != kDiff || (ks < KT / 2) == (kMapTiles ? n == 0 : (g & 1) == 0);
+            };
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const bool live_head = (n * 8 + g) < mt.nrows;
+                const bool live_head = row_of(n * 8 + g) < mt.nrows;
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int kk = 0; kk < KT; kk += 2) {
-                        const int row = (n * 8 + (lane & 7)) / kQRowsPerHead;
+                        const int row = kMapTiles ? (lane & 7) : (n * 8 + (lane & 7)) / kQRowsPerHead;
                         const int chunk = 2 * kk + (lane >> 3);
                         uint32_t r0, r1, r2, r3;
                         ldsm_x4(qbase + (uint32_t)(row * D * 2 + chunk * 16), r0, r1, r2, r3);
-                        const bool live = live_head && q_live(kk);
+                        const bool live = live_head && q_live(kk, n);
                         qf[kk][n][0] = live ? r0 : 0u;
                         qf[kk][n][1] = live ? r1 : 0u;
                         qf[kk + 1][n][0] = live ? r2 : 0u;
@@ -1061,7 +1070,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 } else {
                     // f16 fragments in the E4M3 k-order: k-step ks covers
                     // d = 32*(ks/2) + 16*(ks%2) + {4c..4c+3}.
-                    const int row = (n * 8 + g) / kQRowsPerHead;
+                    const int row = kMapTiles ? g : (n * 8 + g) / kQRowsPerHead;
                     const uint8_t *qrow = sb + 2 * Sh::KV_REGION + row * D * 2;
                     if constexpr (QBF16) {
                         // bf16 q into the f16 product.  Direct conversion is
@@ -1079,7 +1088,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                         for (int ks = 0; ks < KT; ++ks) {
                             const int d0 = 32 * (ks >> 1) + 16 * (ks & 1) + 4 * c;
-                            const uint2 raw = q_live(ks) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
+                            const uint2 raw = q_live(ks, n) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
                             const float x0 = __uint_as_float(raw.x << 16), x1 = __uint_as_float(raw.x & 0xffff0000u);
                             const float x2 = __uint_as_float(raw.y << 16), x3 = __uint_as_float(raw.y & 0xffff0000u);
                             amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x0), fabsf(x1))), fmaxf(fabsf(x2), fabsf(x3)));
@@ -1103,7 +1112,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                             for (int ks = 0; ks < KT; ++ks) {
                                 const int d0 = 32 * (ks >> 1) + 16 * (ks & 1) + 4 * c;
-                                const uint2 raw = q_live(ks) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
+                                const uint2 raw = q_live(ks, n) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
                                 const uint32_t w0 = pack_f16x2(__uint_as_float(raw.x << 16) * up,
                                                                __uint_as_float(raw.x & 0xffff0000u) * up);
                                 const uint32_t w1 = pack_f16x2(__uint_as_float(raw.y << 16) * up,
@@ -1118,7 +1127,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                         for (int ks = 0; ks < KT; ++ks) {
                             const int d0 = 32 * (ks >> 1) + 16 * (ks & 1) + 4 * c;
-                            const uint2 raw = q_live(ks) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
+                            const uint2 raw = q_live(ks, n) ? *reinterpret_cast<const uint2 *>(qrow + d0 * 2) : make_uint2(0u, 0u);
                             qf[ks][n][0] = live_head ? raw.x : 0u;
                             qf[ks][n][1] = live_head ? raw.y : 0u;
                         }
@@ -1181,6 +1190,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                             ldsm_x4(kbox + (uint32_t)h * hstride + swz<SUBROW>(row_a, chunk), a0, a1, a2, a3);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
+                                if (kMapTiles && (kk < KT / 2) != (n == 0)) continue;  // the other map's half
                                 float *acc = (kk & 1) ? s2[n] : sv[sub][n];
                                 if constexpr (KV == KV_BF16)
                                     mma_bf16(acc, a0, a1, a2, a3, qf[kk][n][0], qf[kk][n][1]);
@@ -1206,6 +1216,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                             const uint32_t a13 = e4m3x2_to_f16x2((uint16_t)(q3 >> 16));
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
+                                if (kMapTiles && (2 * jg < KT / 2) != (n == 0)) continue;  // the other map's half
                                 mma_f16(sv[sub][n], a00, a01, a02, a03, qf[2 * jg][n][0], qf[2 * jg][n][1]);
                                 mma_f16(s2[n], a10, a11, a12, a13, qf[2 * jg + 1][n][0], qf[2 * jg + 1][n][1]);
                             }
@@ -1229,15 +1240,19 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                         // the KV row and sees the cached tokens
                         // [0, L - qn + i / G + 1); token t of the tile row is
                         // hidden from the score columns (q rows 2c, 2c + 1 of
-                        // head tile n) whose limit it reaches
-                        const int ta = mt.t0 + r0 + g;
-                        const int i0 = mt.hg * QROWS + n * 8 + 2 * c;
+                        // head tile n) whose limit it reaches.  Only a tile
+                        // that passes the first query token's limit is cut
+                        // (the divisions cost more than the rest of the mask).
                         const int L = lens[mt.b];  // the row's attended length (dispatch table)
-                        const int l0 = L - p.qn + i0 / p.G + 1, l1 = L - p.qn + (i0 + 1) / p.G + 1;
-                        v00 = v00 && ta < l0;
-                        v01 = v01 && ta < l1;
-                        v10 = v10 && ta + 8 < l0;
-                        v11 = v11 && ta + 8 < l1;
+                        if (mt.t0 + TILE > L - p.qn + 1) {
+                            const int ta = mt.t0 + r0 + g;
+                            const int i0 = mt.hg * QROWS + row_of(n * 8 + 2 * c), i1 = mt.hg * QROWS + row_of(n * 8 + 2 * c + 1);
+                            const int l0 = L - p.qn + i0 / p.G + 1, l1 = L - p.qn + i1 / p.G + 1;
+                            v00 = v00 && ta < l0;
+                            v01 = v01 && ta < l1;
+                            v10 = v10 && ta + 8 < l0;
+                            v11 = v11 && ta + 8 < l1;
+                        }
                     }
                     sv[sub][n][0] = v00 ? (sv[sub][n][0] + s2[n][0]) * sc0 : -INFINITY;
                     sv[sub][n][1] = v01 ? (sv[sub][n][1] + s2[n][1]) * sc1 : -INFINITY;
@@ -1560,16 +1575,16 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
         // Per head: combined max, the warps' weights (in place of their max)
         // and the combined denominator; then the D outputs in float4 groups.
         if (tid < G) {
-            const int h = tid;
+            const int h = tid, sl = slot_of(h);
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < NSLOT; ++w) M = fmaxf(M, scr_m[w * QROWS + h]);
+            for (int w = 0; w < NSLOT; ++w) M = fmaxf(M, scr_m[w * QROWS + sl]);
             float Ls = 0.f;
 #pragma unroll
             for (int w = 0; w < NSLOT; ++w) {
-                const float a = (M == -INFINITY) ? 0.f : ex2(scr_m[w * QROWS + h] - M);
-                scr_m[w * QROWS + h] = a;
-                Ls += a * scr_l[w * QROWS + h];
+                const float a = (M == -INFINITY) ? 0.f : ex2(scr_m[w * QROWS + sl] - M);
+                scr_m[w * QROWS + sl] = a;
+                Ls += a * scr_l[w * QROWS + sl];
             }
             const bool empty = !(Ls > 0.f);
             const size_t row = q_row(p, mb, m_kvh, m_hg, h, QROWS);
@@ -1584,7 +1599,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
             }
         }
         named_bar_sync(1, NC * 32);
-        // The warps' states of row h combined, outputs d .. d + 3.
+        // The warps' states of the row in slot h combined, outputs d .. d + 3.
         auto combined = [&](int h, int d) {
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1606,7 +1621,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 const int idx = i0 + lane;
                 const bool in = idx < total;
                 const int h = in ? idx / (D / 4) * 2 : 0, d = (idx % (D / 4)) * 4;
-                const float4 a1 = combined(h, d), a2 = combined(h + 1, d);
+                const float4 a1 = combined(slot_of(h), d), a2 = combined(slot_of(h + 1), d);
                 const size_t row = q_row(p, mb, m_kvh, m_hg, h, QROWS);
                 if (m_nsplit == 1) {
                     finish_pair<D>(p, row, d, a1, scr_inv[h], a2, scr_inv[h + 1], in);
