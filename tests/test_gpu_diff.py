@@ -139,3 +139,39 @@ def test_length_past_the_plan_is_flagged(fdlib):
     with pytest.raises(_lib.FdError) as e:
         dec.check()
     assert e.value.code == _lib.FD_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("mode", ["diff", "weights"])
+@pytest.mark.parametrize("opts", [dict(), dict(num_splits=3), dict(tile_tokens=128, ctas_per_sm=2), dict(tile_tokens=64)])
+def test_e4m3_pages_of_very_different_scales(fdlib, mode, opts):
+    """V scales from 2^-10 to 2^10, some zero."""
+    lens, D, ps = [1000, 37, 300], 128, 32
+    q, kp, vp, ks, vs, bt = setup("e4m3", "bf16", lens, 8, 2, D, ps, seed=9)
+    gen = torch.Generator().manual_seed(3)
+    vs = torch.exp2(torch.rand(vs.shape, generator=gen) * 20 - 10) / 448 * (torch.rand(vs.shape, generator=gen) > 0.1)
+    g = lambda t: t.cuda()  # noqa: E731
+    dl = torch.tensor(lens, dtype=torch.int32).cuda()
+    if mode == "diff":
+        dec = fd.DiffDecoder.for_pools(g(q), g(kp), g(vp), g(bt), lens, out_dtype=torch.float32, **opts)
+        out, _ = dec(g(q), g(kp), g(vp), g(bt), dl, torch.full((8,), 0.5).cuda(), k_scale=g(ks), v_scale=g(vs))
+    else:
+        dec = fd.PagedDecoder.for_pools(g(q), g(kp), g(vp), g(bt), lens, out_dtype=torch.float32, track_weights=True, **opts)
+        out, _, _ = dec.decode_weights(g(q), g(kp), g(vp), g(bt), dl, torch.zeros(3, 2, 1000).cuda(), k_scale=g(ks),
+                                       v_scale=g(vs))
+    torch.cuda.synchronize()
+    dec.check()
+    out = out.cpu().double().reshape(3, 2, 4, D)
+    kd, vd = R.values(kp, ks), R.values(vp, vs)
+    for b, L in enumerate(lens):
+        k, v = R.seq_tokens(kd, bt[b], L, ps), R.seq_tokens(vd, bt[b], L, ps)
+        qd = q[b].float().double().reshape(2, 4, D)
+        ref, tol = torch.zeros(2, 4, D, dtype=torch.float64), torch.zeros(2, 4, D, dtype=torch.float64)
+        for m, f in (((0, 1.0), (1, -0.5)) if mode == "diff" else ((0, 1.0),)):
+            width = D // 2 if mode == "diff" else D
+            p, _, err = R.attend(qd, k, L, width, m * width)
+            ref += f * torch.einsum("hgn,nhd->hgd", p, v)
+            # a weight's rounding for the product (2^-11) and its exponent's error, the fp32
+            # steps (2^-18), and f16's floor of 2^-25
+            tol += abs(f) * ((2.0 ** -11 + 2 * err + 2.0 ** -18) * torch.einsum("hgn,nhd->hgd", p, v.abs()) +
+                             2.0 ** -25 * v.abs().sum(0)[:, None])
+        assert ((out[b] - ref).abs() <= tol).all(), float(((out[b] - ref).abs() / tol).max())
