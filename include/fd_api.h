@@ -476,7 +476,8 @@ fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *arg
  *                     and lse); need not be zeroed; one per call in flight
  *   other arguments as fd_decode_paged.
  * After a call that set an FD_DEV_* bit, weights_out of the rows concerned is
- * unspecified.  Not for shared_kv plans (FD_ERR_UNSUPPORTED). */
+ * unspecified.  Not for shared_kv plans, nor for more than 6144 query rows per
+ * KV head (FD_ERR_UNSUPPORTED). */
 fd_status fd_decode_weights_workspace(const fd_plan_t *plan, size_t *bytes);
 fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const void *k_pages,
                                   const void *v_pages, const float *k_scale, const float *v_scale,

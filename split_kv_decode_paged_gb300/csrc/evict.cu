@@ -375,11 +375,17 @@ __global__ void __launch_bounds__(kMoveThreads) fd_evict_copy_kernel(const __gri
 }
 
 // In place: row j comes from row kept[j] >= j of the same sequence, so rows
-// are moved in order, a chunk of them read before any of it is written.  What
-// can run at once is the width: a CTA takes one slice of K's or V's row.
+// are moved in order, a chunk of them read before any of it is written (what a
+// chunk writes no later chunk reads).  What can run at once is the width: a
+// CTA takes one slice of K's or V's row, kShiftUnits 16-byte units a thread in
+// flight, and finds the next chunk's places while they are.
+constexpr int kShiftUnits = 8;
+constexpr int kShiftRows = kMoveThreads * kShiftUnits / 2;  // of the narrowest slice, 32 bytes
+
 template <int RB, bool FP8>
 __global__ void __launch_bounds__(kMoveThreads) fd_evict_shift_kernel(const __grid_constant__ EvictParams p, int slices) {
-    __shared__ RowPlace rows[kMoveThreads];
+    __shared__ long long src_at[2][kShiftRows], dst_at[2][kShiftRows];
+    __shared__ float ratio_at[2][FP8 ? kShiftRows : 1];
     grid_dependency_wait();
     const long long bh = blockIdx.x / (2 * slices);
     const int part = (int)(blockIdx.x % (2 * slices));
@@ -395,28 +401,49 @@ __global__ void __launch_bounds__(kMoveThreads) fd_evict_shift_kernel(const __gr
         const int mid = (lo + hi) >> 1;
         if (kept[mid] > mid) hi = mid; else lo = mid + 1;
     }
-    const int ups = RB / slices / 16;    // 16-byte units of the slice
-    const int per = kMoveThreads / ups;  // rows per chunk
+    const int ups = RB / slices / 16;                    // 16-byte units of the slice
+    const int step = kMoveThreads / ups;                 // rows of one unit a thread
+    const int chunk = step * kShiftUnits;
     const int rl = threadIdx.x / ups;
     uint8_t *pool = reinterpret_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) + sl * (RB / slices) +
                     (threadIdx.x % ups) * 16;
-    for (int j0 = lo; j0 < n; j0 += per) {
-        __syncthreads();
-        if (threadIdx.x < per) {
-            const int j = j0 + threadIdx.x;
-            if (j < n) rows[threadIdx.x] = place_row<RB, FP8>(p, b, h, kept, j);
-            else rows[threadIdx.x].src = -1;
+    auto find = [&](int j0, int buf) {
+        for (int i = threadIdx.x; i < chunk; i += kMoveThreads) {
+            long long s = -1, d = -1;
+            float f = 1.f;
+            if (j0 + i < n) {
+                const RowPlace r = place_row<RB, FP8>(p, b, h, kept, j0 + i);
+                s = r.src;
+                d = r.dst;
+                f = is_v ? r.v_ratio : r.k_ratio;
+            }
+            src_at[buf][i] = s;
+            dst_at[buf][i] = d;
+            if constexpr (FP8) ratio_at[buf][i] = f;
         }
-        __syncthreads();
-        const RowPlace r = rows[rl];
-        uint4 v;
-        if (r.src >= 0) v = *reinterpret_cast<const uint4 *>(pool + r.src);
-        __syncthreads();  // the chunk is read
-        if (r.src >= 0) {
-            const float ratio = is_v ? r.v_ratio : r.k_ratio;
-            if (FP8 && ratio != 1.f) v = rescale16(v, ratio);
-            *reinterpret_cast<uint4 *>(pool + r.dst) = v;
+    };
+    find(lo, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int j0 = lo; j0 < n; j0 += chunk, buf ^= 1) {
+        uint4 v[kShiftUnits];
+#pragma unroll
+        for (int u = 0; u < kShiftUnits; ++u) {
+            const long long s = src_at[buf][rl + u * step];
+            if (s >= 0) v[u] = *reinterpret_cast<const uint4 *>(pool + s);
         }
+        if (j0 + chunk < n) find(j0 + chunk, buf ^ 1);
+        __syncthreads();  // the chunk is read, the next one's places are known
+#pragma unroll
+        for (int u = 0; u < kShiftUnits; ++u) {
+            const int r = rl + u * step;
+            if (src_at[buf][r] < 0) continue;
+            if constexpr (FP8) {
+                if (ratio_at[buf][r] != 1.f) v[u] = rescale16(v[u], ratio_at[buf][r]);
+            }
+            *reinterpret_cast<uint4 *>(pool + dst_at[buf][r]) = v[u];
+        }
+        __syncthreads();  // these places are overwritten next
     }
 }
 

@@ -91,6 +91,7 @@ constexpr int kMaxStages = 8;
 // fd_plan_t::reserved[0]: what the plan was made for.
 constexpr int kPlanPlain = 0;
 constexpr int kPlanDiff = 1;  // fd_plan_diff
+constexpr int kMaxHeads = 1 << 20;
 constexpr int kMaxQLen = 64;  // query tokens per sequence (multi-token mode)
 constexpr int kMinStages = 2;
 constexpr int kSmallGridItemTokens = 1024;  // small grids: two CTAs per SM for items up to this long
@@ -1020,6 +1021,10 @@ fd_status fd_decode_weights_workspace(const fd_plan_t *plan, size_t *bytes) {
     WeightsLayout l;
     if (!weights_layout(plan, &l)) return FD_ERR_INVALID_ARG;
     if (plan->row_fold != std::max(1, plan->q_len)) return FD_ERR_UNSUPPORTED;  // shared_kv
+    if (l.separate && !weights_launchable(plan->kv_rows, plan->problem.Hkv,
+                                          (long long)plan->num_splits * plan->chunk_tokens,
+                                          (long long)(plan->problem.Hq / plan->problem.Hkv) * plan->row_fold))
+        return FD_ERR_UNSUPPORTED;
     *bytes = l.bytes;
     return FD_OK;
 }
@@ -1095,6 +1100,7 @@ fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *arg
     const bool fp8 = p.kv_dtype == FD_E4M3;
     if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr)) return FD_ERR_INVALID_ARG;
     if ((a.q == nullptr) != (a.q_out == nullptr)) return FD_ERR_INVALID_ARG;
+    if (p.Hq > kMaxHeads) return FD_ERR_UNSUPPORTED;  // the kernel's row offsets are ints
     if (a.tokens < 1 || !(a.eps > 0.f) || !std::isfinite(a.eps)) return FD_ERR_INVALID_ARG;
     if (!aligned(a.q, 16) || !aligned(a.q_out, 16) || !aligned(a.k_new, 16) || !aligned(a.v_new, 16) ||
         !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
@@ -1173,7 +1179,11 @@ fd_status fd_evict_kv(const fd_problem *problem, void *k_pages, void *v_pages, c
     // other CTAs still read a length while the first one of its sequence writes the new one
     if (new_lens == seq_lens) return FD_ERR_INVALID_ARG;
     DeviceInfo di;
-    const fd_status ds = device_info(di);
+    fd_status ds = FD_ERR_CUDA;
+    try {
+        ds = device_info(di);
+    } catch (...) {
+    }
     if (ds != FD_OK) return ds;
     EvictParams ep;
     std::memset(&ep, 0, sizeof(ep));
@@ -1213,11 +1223,15 @@ fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host, 
     if (!plan || !seq_lens_host) return FD_ERR_INVALID_ARG;
     const fd_status st = validate_problem(problem);
     if (st != FD_OK) return st;
-    if (problem->Hq > (1 << 20)) return FD_ERR_UNSUPPORTED;
+    if (problem->Hq > kMaxHeads) return FD_ERR_UNSUPPORTED;
     if (options && options->shared_kv) return FD_ERR_UNSUPPORTED;
     fd_problem p = *problem;
     p.Hq *= 2;
-    const fd_status r = fd_plan(&p, seq_lens_host, options, plan);
+    fd_status r = FD_ERR_UNSUPPORTED;
+    try {
+        r = fd_plan(&p, seq_lens_host, options, plan);
+    } catch (...) {  // no memory for the lengths
+    }
     if (r != FD_OK) return r;
     plan->fuse_merge = 1;  // a pair's two states meet in the merge that finishes them
     plan->reserved[0] = kPlanDiff;

@@ -83,7 +83,6 @@ struct WeightParams {
     int *status;
     int Bkv, Hq, Hkv, G, fold, R, cap, weights_stride;
     int skip_to;               // rows of at most this length were done by the decode kernel
-    int chunk_tokens;          // tokens per CTA (set at launch)
 };
 
 struct NormAppendParams {
@@ -171,6 +170,8 @@ cudaError_t decode_occupancy(const fd_problem &p, const KernelShape &ks, size_t 
 
 cudaError_t launch_merge(const MergeParams &mp, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &ap, cudaStream_t stream);
+// Whether launch_weights can launch for these sizes (R: query rows per KV head).
+bool weights_launchable(int Bkv, int Hkv, long long cap, long long R);
 cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream);
 cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);

@@ -129,6 +129,12 @@ long long as_int(PyObject *o) {
     return v;
 }
 
+bool as_bool(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Other();
+    return v != 0;
+}
+
 float as_float(PyObject *o) {
     if (!PyFloat_CheckExact(o) && !PyLong_CheckExact(o)) throw Other();
     const double v = PyFloat_AsDouble(o);
@@ -275,9 +281,7 @@ PyObject *append(PyObject *const *a) {
         n.rotary_dim = 2 * (int)cs.size(1);
         n.rotary_cos = c.data<const float>(a[10], at::kFloat, {cs.size(0), cs.size(1)});
         n.rotary_sin = c.data<const float>(a[11], at::kFloat, {cs.size(0), cs.size(1)});
-        const int il = PyObject_IsTrue(a[12]);
-        if (il < 0) throw Other();
-        n.interleaved = il;
+        n.interleaved = as_bool(a[12]);
     }
     n.positions = c.maybe<const int32_t>(a[13], at::kInt, {p.B});
     n.new_lens = c.maybe<const int32_t>(a[14], at::kInt, {p.B});
@@ -363,7 +367,7 @@ PyObject *weights(PyObject *const *a) {
     void *ws = c.bytes(a[13], &ws_bytes), *ww = c.bytes(a[14], &ww_bytes);
     int32_t *status = c.status(a[15]);
     void *stream = c.stream();
-    const bool want_lse = a[12] == Py_True || a[11] != Py_None;
+    const bool want_lse = a[11] != Py_None || as_bool(a[12]);
     const Output out = output(c, a[10], Shape(pl, {p.Hq, p.D}), torch_type(p.out_dtype));
     Output lse;
     if (want_lse) lse = output(c, a[11], Shape(pl, {p.Hq}), at::kFloat);
@@ -403,7 +407,7 @@ PyObject *diff(PyObject *const *a) {
     void *ws = c.bytes(a[15], &ws_bytes);
     int32_t *status = c.status(a[16]);
     void *stream = c.stream();
-    const bool want_lse = a[14] == Py_True || a[13] != Py_None;
+    const bool want_lse = a[13] != Py_None || as_bool(a[14]);
     const Output out = output(c, a[12], Shape(pl, {heads, p.D}), torch_type(p.out_dtype));
     Output lse;
     if (want_lse) lse = output(c, a[13], Shape(pl, {heads, 2}), at::kFloat);

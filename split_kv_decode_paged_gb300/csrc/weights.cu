@@ -11,6 +11,7 @@ namespace fd {
 
 constexpr int kWeightThreads = 128;
 constexpr int kWeightFly = 8;  // tokens per thread: one round of loads a CTA
+constexpr int kWeightChunk = kWeightThreads * kWeightFly;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid_constant__ WeightParams p, int chunks) {
@@ -26,7 +27,7 @@ __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid
         if (threadIdx.x == 0 && chunk == 0 && h == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
         L = p.weights_stride;
     }
-    const int t0 = chunk * p.chunk_tokens, t1 = min(L, t0 + p.chunk_tokens);
+    const int t0 = chunk * kWeightChunk, t1 = min(L, t0 + kWeightChunk);
     if (t0 >= t1) return;
     for (int r = threadIdx.x; r < p.R; r += kWeightThreads) {
         const size_t row = ((size_t)b * p.fold + r / p.G) * p.Hq + (size_t)h * p.G + r % p.G;
@@ -40,23 +41,26 @@ __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid
                                             p.in ? p.in + at : nullptr, p.out + at, t0, t1, threadIdx.x);
 }
 
+bool weights_launchable(int Bkv, int Hkv, long long cap, long long R) {
+    const long long chunks = (cap + kWeightChunk - 1) / kWeightChunk;
+    return chunks <= 0x7fffffffLL / ((long long)Bkv * Hkv) && R * 2 * (long long)sizeof(float) <= 48 * 1024;
+}
+
+// For sizes that weights_launchable() takes.
 cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream) {
-    WeightParams p = wp;
-    p.chunk_tokens = kWeightFly * kWeightThreads;
-    const long long chunks = (p.cap + p.chunk_tokens - 1) / p.chunk_tokens;
-    const long long blocks = (long long)p.Bkv * p.Hkv * chunks;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const long long chunks = (wp.cap + kWeightChunk - 1) / kWeightChunk;
+    const long long blocks = (long long)wp.Bkv * wp.Hkv * chunks;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kWeightThreads);
-    cfg.dynamicSmemBytes = (size_t)p.R * 2 * sizeof(float);
+    cfg.dynamicSmemBytes = (size_t)wp.R * 2 * sizeof(float);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fd_weights_kernel, p, (int)chunks);
+    return cudaLaunchKernelEx(&cfg, fd_weights_kernel, wp, (int)chunks);
 }
 
 }  // namespace fd

@@ -64,6 +64,7 @@ def test_append_rejects_bad_pools_and_problems(fdlib):
     assert call_append(fdlib, n, p=p8, ks=A, vs=A + 2) == BAD
     assert call_append(fdlib, n, p=prob(D=96)) == UNSUP
     assert call_append(fdlib, n, p=prob(page_size=24)) == BAD
+    assert call_append(fdlib, norm_args(q_stride=1 << 40, q_out_stride=1 << 40), p=prob(Hq=1 << 21)) == UNSUP
     # a grid beyond what a launch can have
     big = prob(B=8192)
     assert call_append(fdlib, norm_args(tokens=0x7fffffff), p=big) == UNSUP
@@ -94,6 +95,8 @@ def test_weights_rejects_bad_arguments(fdlib):
     diff = _lib.fd_plan_diff(prob(), [100, 50], num_sms=152)
     assert fdlib.fd_decode_weights_workspace(REF(diff), REF(ctypes.c_size_t())) == BAD
     assert fdlib.fd_decode_weights_workspace(None, REF(ctypes.c_size_t())) == BAD
+    wide = _lib.fd_plan(prob(Hq=8 * 1024, Hkv=1, D=64), [100, 50], num_sms=152)
+    assert fdlib.fd_decode_weights_workspace(REF(wide), REF(ctypes.c_size_t())) == UNSUP
 
 
 def test_weights_workspace_covers_the_capacity(fdlib):

@@ -102,6 +102,17 @@ def test_sizes(fdlib, B, T, Hq, Hkv, ps):
     check("e4m3", "bf16", B, T, Hq, Hkv, 64, ps, rd=34, seed=B + 1)
 
 
+@pytest.mark.parametrize("rot", ["none", "full", "pairs", "half", "odd"])
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("e4m3", 64)])
+def test_many_tokens(fdlib, kv, D, rot):
+    """Enough tokens that a warp takes several steps of a token, or all of them."""
+    rd = {"none": 0, "full": D, "pairs": D, "half": D // 2, "odd": D // 4 + 2}[rot]
+    il = rot == "pairs"
+    check(kv, "bf16", 3, 700, 32, 8, D, 16, rd=rd, interleaved=il, ragged=[700, 0, 333], lens=[0, 5, 16])
+    check(kv, "bf16", 2, 2500, 9, 3, D, 64, rd=rd, interleaved=il, lens=[7, 0], seed=1)
+    check(kv, "bf16", 6, 2100, 5, 1, D, 32, rd=rd, interleaved=il, ragged=[2100, 1, 2099, 0, 1000, 5], lens=[0] * 6, seed=2)
+
+
 def test_padded_batch_with_empty_rows(fdlib):
     check("bf16", "bf16", 5, 37, 8, 2, 128, 16, rd=128, ragged=[0, 37, 1, 16, 0])
     check("f16", "f16", 3, 1, 4, 4, 64, 16, rd=64, ragged=[1, 0, 1])
