@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(cons
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     constexpr int NCS = ROT == ROT_NONE ? 1 : (ROT == ROT_PAIRS || ROT == ROT_FULL ? 4 : 8);  // cosines a lane holds
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();    // launched while the kernel before drains
+    grid_launch_dependents();  // and the next one (the decode) may be, too
     const int sub = lane / LPR, l = lane % LPR;
     // elements 0-3 of the lane are da .. da + 3 of the row, 4-7 db .. db + 3
     const int da = ROT == ROT_FULL ? 4 * l : 8 * l, db = ROT == ROT_FULL ? D / 2 + 4 * l : 8 * l + 4;
@@ -330,11 +332,17 @@ namespace {
 
 template <int D, bool BF16, bool FP8, int ROT>
 cudaError_t launch_rot(const NormAppendParams &p, bool one, unsigned blocks, cudaStream_t stream) {
-    if (one)
-        fd_append_kv_norm_kernel<D, BF16, FP8, ROT, true><<<blocks, kNormWarps * 32, 0, stream>>>(p);
-    else
-        fd_append_kv_norm_kernel<D, BF16, FP8, ROT, false><<<blocks, kNormWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kNormWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (one) return cudaLaunchKernelEx(&cfg, fd_append_kv_norm_kernel<D, BF16, FP8, ROT, true>, p);
+    return cudaLaunchKernelEx(&cfg, fd_append_kv_norm_kernel<D, BF16, FP8, ROT, false>, p);
 }
 
 template <int D, bool BF16, bool FP8>

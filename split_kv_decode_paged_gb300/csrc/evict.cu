@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) fd_evict_select_kernel(const _
     __shared__ uint32_t tile_total[2];                // of rounds i and i + 1
     __shared__ uint32_t sh_bin, sh_left;
     static_assert(kBins == 4 * kSelThreads && kSelPer * kSelWarps <= kSelThreads, "bins and places per thread");
+    grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long bh = blockIdx.x / ctas;
@@ -482,16 +483,18 @@ cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
     while (ctas < kMaxSelCtas && (long long)ctas * kSelTile < longest && bh * ctas * 2 <= 2LL * sms) ctas *= 2;
     if (bh * ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     {
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)ctas;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(bh * ctas));
         cfg.blockDim = dim3(kSelThreads);
         cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, fd_evict_select_kernel, p, ctas);
         if (e != cudaSuccess) return e;
     }
