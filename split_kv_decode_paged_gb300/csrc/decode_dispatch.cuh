@@ -13,7 +13,11 @@ template <int KV, int D, int NT, bool QBF16, int MODE>
 cudaError_t launch_decode_d(const KernelShape &ks, const DecodeParams &dp, const CUtensorMap &tmk,
                             const CUtensorMap &tmv, int grid, size_t smem, cudaStream_t stream) {
     if (dp.qn > 1) {
-        // several causal query tokens per KV row: the 128-token, 8-warp shape only
+        // several causal query tokens per KV row: the 128-token, 8-warp shape,
+        // and 256 tokens for differential attention over E4M3 K/V
+        if constexpr (KV == KV_E4M3 && MODE == kDiff)
+            if (ks.consumer_warps == 8 && ks.subtiles == 2)
+                return launch_decode_t<KV, D, NT, 8, 2, QBF16, true, false, MODE>(dp, tmk, tmv, grid, smem, stream);
         if (ks.consumer_warps == 8 && ks.subtiles == 1)
             return launch_decode_t<KV, D, NT, 8, 1, QBF16, true, false, MODE>(dp, tmk, tmv, grid, smem, stream);
         return cudaErrorInvalidValue;

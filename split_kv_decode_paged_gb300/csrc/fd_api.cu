@@ -335,8 +335,13 @@ fd_status fd_status_from_device(int32_t w) {
     return FD_OK;
 }
 
-fd_status fd_plan(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
-                  fd_plan_t *plan) {
+}  // extern "C"
+
+namespace {
+
+// fd_plan; diff: for differential attention (problem: its padded heads).
+fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
+                    fd_plan_t *plan, bool diff) {
     if (!plan || !seq_lens_host) return FD_ERR_INVALID_ARG;
     fd_status st = validate_problem(problem);
     if (st != FD_OK) return st;
@@ -471,9 +476,13 @@ fd_status fd_plan(const fd_problem *problem, const int32_t *seq_lens_host, const
     int tile_opt = opt.tile_tokens;
     if (q_len > 1) {
         // several causal query tokens per sequence: one CTA per SM, 128-token
-        // stages of 8 consumer warps (the shape built with the causal limits)
+        // stages of 8 consumer warps (the shape built with the causal limits).
+        // Differential attention over E4M3 pages also has 256-token stages,
+        // taken as below: two sub-tiles a warp overlap its chains of dependent
+        // products and conversions (8 sequences of 8192-32768 tokens, 4 query
+        // tokens, 4 heads a KV head: 186 -> 148 us)
         if ((opt.tile_tokens != 0 && opt.tile_tokens != 128) || cps_opt != 1) return FD_ERR_UNSUPPORTED;
-        tile_opt = 128;
+        if (!(diff && p.kv_dtype == FD_E4M3)) tile_opt = 128;
     }
     if (tile_opt == 0 && p.kv_dtype == FD_E4M3) {
         const KernelShape k256 = kernel_shape(p, 256, fold, cps_opt);
@@ -618,6 +627,15 @@ fd_status fd_plan(const fd_problem *problem, const int32_t *seq_lens_host, const
     return FD_OK;
 }
 
+}  // namespace
+
+extern "C" {
+
+fd_status fd_plan(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
+                  fd_plan_t *plan) {
+    return plan_impl(problem, seq_lens_host, options, plan, false);
+}
+
 }  // extern "C"
 
 namespace {
@@ -655,7 +673,7 @@ fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages,
     if (fold > 1 && ex && (ex->cache_batch_idx || ex->cache_leftpad)) return FD_ERR_UNSUPPORTED;
     if (plan->ctas_per_sm < 0 || plan->ctas_per_sm > 8) return FD_ERR_INVALID_ARG;
     const KernelShape ks = kernel_shape(p, plan->tile_tokens, fold, std::max(1, plan->ctas_per_sm));
-    if (q_len > 1 && !(ks.consumer_warps == 8 && ks.subtiles == 1)) return FD_ERR_UNSUPPORTED;
+    if (q_len > 1 && !(ks.consumer_warps == 8 && (ks.subtiles == 1 || mode.kind == kPlanDiff))) return FD_ERR_UNSUPPORTED;
     if (plan->head_subgroups != ((p.Hq / p.Hkv) * fold + 8 * ks.nt - 1) / (8 * ks.nt)) return FD_ERR_INVALID_ARG;
     if (plan->tile_tokens != ks.tile || plan->chunk_tokens < ks.tile || plan->chunk_tokens % ks.tile != 0 ||
         plan->num_splits < 1 || plan->num_splits > kMaxSplits || plan->stages < kMinStages ||
@@ -1229,7 +1247,7 @@ fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host, 
     p.Hq *= 2;
     fd_status r = FD_ERR_UNSUPPORTED;
     try {
-        r = fd_plan(&p, seq_lens_host, options, plan);
+        r = plan_impl(&p, seq_lens_host, options, plan, true);
     } catch (...) {  // no memory for the lengths
     }
     if (r != FD_OK) return r;

@@ -88,6 +88,14 @@ def test_query_tokens(fdlib, kv, q_len, Hq, Hkv):
     check(kv, "f16" if kv == "f16" else "bf16", [q_len, 40, 700], Hq, Hkv, 128, 16, q_len=q_len, seed=q_len)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("D,Hq,Hkv,ps,q_len", [(128, 8, 2, 64, 4), (64, 4, 1, 32, 6), (128, 2, 1, 128, 3), (128, 3, 3, 64, 2)])
+def test_query_tokens_over_e4m3_pages_of_256_token_stages(fdlib, act, D, Hq, Hkv, ps, q_len):
+    """Causal limits that fall in either sub-tile of a warp, lengths around a stage."""
+    check("e4m3", act, [q_len, 255, 256, 257, 520, 1000], Hq, Hkv, D, ps, q_len=q_len, seed=q_len)
+    check("e4m3", act, [2000, q_len + 1], Hq, Hkv, D, ps, q_len=q_len, seed=q_len, num_splits=3, out_dtype=torch.float32)
+
+
 def test_long_split_sequence(fdlib):
     check("bf16", "bf16", [20011], 8, 2, 128, 64, seed=4)
     check("e4m3", "bf16", [9000, 16], 8, 2, 128, 128, seed=5)
