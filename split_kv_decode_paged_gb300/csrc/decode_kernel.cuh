@@ -383,7 +383,7 @@ __device__ __forceinline__ void add_weights(const DecodeParams &p, int b, int kv
         if (tid == 0) flag_status(p.status, FD_DEV_CAPACITY);
         L = p.w_stride;
     }
-    sum_weights<NC * 32, 8>(p.cta_scores + (size_t)blockIdx.x * p.chunk * R, R, row_max, row_inv,
+    sum_weights<NC * 32, 8>(p.cta_scores + (size_t)blockIdx.x * p.chunk * score_stride(R), R, row_max, row_inv,
                             p.w_in ? p.w_in + at : nullptr, p.w_out + at, 0, L, tid);
 }
 
@@ -1454,11 +1454,11 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
         __syncwarp();
         if (lane == 0 && !(scr_in_stage && (flags & kFlagLast))) mbar_arrive(smem_u32(&empty_bar[st]));
         if constexpr (MODE == kScores) {
-            // The tile's scores, R = G * fold a token: a whole sequence's into
-            // this CTA's own buffer (its totals are formed at the item's end),
-            // a split one's into the call's.  After the stage's release: they
-            // hold up no copy.
-            const int R = p.G * p.fold;
+            // The tile's scores, score_stride(R) for a token's R = G * fold
+            // query rows: a whole sequence's into this CTA's own buffer (its
+            // totals are formed at the item's end), a split one's into the
+            // call's.
+            const int R = score_stride(p.G * p.fold);
             float *to = p.w_fused && m_nsplit == 1
                             ? p.cta_scores + ((size_t)blockIdx.x * p.chunk + m_t0) * R
                             : p.scores + (((size_t)mb * p.Hkv + m_kvh) * p.cap + m_t0) * R;
@@ -1471,14 +1471,12 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                     const int col = m_hg * QROWS + n * 8 + 2 * c;
                     float *t0 = to + row * R + col, *t8 = t0 + 8 * R;
                     const float *s = sv[sub][n];
-                    if ((R & 1) == 0) {
+                    if (R > 1) {
                         if (v0 && col < R) *reinterpret_cast<float2 *>(t0) = make_float2(s[0], s[1]);
                         if (v1 && col < R) *reinterpret_cast<float2 *>(t8) = make_float2(s[2], s[3]);
                     } else {
                         if (v0 && col < R) t0[0] = s[0];
-                        if (v0 && col + 1 < R) t0[1] = s[1];
                         if (v1 && col < R) t8[0] = s[2];
-                        if (v1 && col + 1 < R) t8[1] = s[3];
                     }
                 }
             }
@@ -1597,6 +1595,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 p.part_m[row * p.S + m_s] = (M == -INFINITY) ? -INFINITY : M * kLn2;
                 p.part_d[row * p.S + m_s] = Ls;
             }
+        }
+        if constexpr (MODE == kScores) {
+            // the padding columns of the scores count for nothing
+            if (tid >= G && tid < QROWS) scr_lse[tid] = scr_inv[tid] = 0.f;
         }
         named_bar_sync(1, NC * 32);
         // The warps' states of the row in slot h combined, outputs d .. d + 3.

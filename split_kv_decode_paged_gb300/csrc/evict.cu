@@ -22,12 +22,19 @@
 
 namespace fd {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelPer = 16;       // tokens per thread and tile: token base + k * kSelThreads + tid
-constexpr int kSelTile = kSelThreads * kSelPer;
-constexpr int kBins = 2048;       // 4 a thread
+constexpr int kSelPer = 16;       // tokens per thread and tile: token base + k * threads + tid
 constexpr int kMaxSelCtas = 8;    // portable cluster size
+
+// Threads of a selecting CTA and bits of a round's digit: 512 threads and
+// 11 + 11 + 10 bits; rows of at most 2048 tokens, of which there are often
+// many, 128 threads and 9 + 9 + 9 + 5 bits (eight CTAs an SM instead of two).
+template <int THREADS>
+struct SelShape {
+    static constexpr int WARPS = THREADS / 32, TILE = THREADS * kSelPer;
+    static constexpr int BITS = THREADS == 512 ? 11 : 9, BINS = 1 << BITS, ROUNDS = (32 + BITS - 1) / BITS;
+    static constexpr int PLACES = kSelPer * WARPS;  // counts of a tile: one per (k, warp)
+    static_assert(BINS == 4 * THREADS && PLACES <= THREADS && WARPS <= 32, "bins and places per thread");
+};
 constexpr int kMoveThreads = 256;
 
 // Unsigned keys in the order of the weights: -0 counts as +0, NaN (key 1) as
@@ -45,7 +52,8 @@ __device__ __forceinline__ float key_weight(uint32_t key) {
 }
 
 // Exclusive prefix over the CTA of v (one value a thread) and its total; two
-// barriers, sums is scratch of kSelWarps words.
+// barriers, sums is scratch of WARPS words.
+template <int WARPS>
 __device__ __forceinline__ uint32_t cta_prefix(uint32_t v, uint32_t *sums, int warp, int lane, uint32_t &total) {
     uint32_t incl = v;
 #pragma unroll
@@ -55,14 +63,14 @@ __device__ __forceinline__ uint32_t cta_prefix(uint32_t v, uint32_t *sums, int w
     }
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    const uint32_t s = lane < kSelWarps ? sums[lane] : 0u;
+    const uint32_t s = lane < WARPS ? sums[lane] : 0u;
     uint32_t all = s;
 #pragma unroll
-    for (int o = 1; o < kSelWarps; o <<= 1) {
+    for (int o = 1; o < WARPS; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xffffffffu, all, o);
         if (lane >= o) all += x;
     }
-    total = __shfl_sync(0xffffffffu, all, kSelWarps - 1);
+    total = __shfl_sync(0xffffffffu, all, WARPS - 1);
     const uint32_t before = __shfl_sync(0xffffffffu, all - s, warp);
     __syncthreads();  // sums may be used again
     return before + incl - v;
@@ -95,14 +103,16 @@ __device__ __forceinline__ uint4 cluster_read4(const uint32_t *p, uint32_t rank)
 // One cluster of `ctas` CTAs (a power of two) per (sequence, KV head); tile i * ctas + rank of
 // the row is CTA rank's in round i.  All branches that hold a barrier depend on
 // the row alone, so the cluster's CTAs take them together.
-__global__ void __launch_bounds__(kSelThreads, 2) fd_evict_select_kernel(const __grid_constant__ EvictParams p,
-                                                                        int ctas) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kernel(const __grid_constant__ EvictParams p,
+                                                                                  int ctas) {
+    using Sh = SelShape<THREADS>;
+    constexpr int kSelThreads = THREADS, kSelWarps = Sh::WARPS, kSelTile = Sh::TILE, kBins = Sh::BINS;
     __shared__ __align__(16) uint32_t hist[kBins];
-    __shared__ uint32_t places[kSelPer * kSelWarps];  // counts of every (k, warp) of a tile, then their prefix
+    __shared__ uint32_t places[Sh::PLACES];  // counts of every (k, warp) of a tile, then their prefix
     __shared__ uint32_t sums[kSelWarps];
-    __shared__ uint32_t tile_total[2];                // of rounds i and i + 1
+    __shared__ uint32_t tile_total[2];       // of rounds i and i + 1
     __shared__ uint32_t sh_bin, sh_left;
-    static_assert(kBins == 4 * kSelThreads && kSelPer * kSelWarps <= kSelThreads, "bins and places per thread");
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -156,9 +166,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) fd_evict_select_kernel(const _
     if (many > 0) {
         uint32_t prefix = 0, mask = 0, left = (uint32_t)many;
 #pragma unroll 1
-        for (int digits = 0; digits < 3; ++digits) {
-            const int shift = digits == 0 ? 21 : (digits == 1 ? 10 : 0);
-            const uint32_t digit = digits == 2 ? 1023u : 2047u;
+        for (int digits = 0; digits < Sh::ROUNDS; ++digits) {
+            const int shift = max(0, 32 - Sh::BITS * (digits + 1));
+            const uint32_t digit = digits == Sh::ROUNDS - 1 ? (1u << (32 - Sh::BITS * (Sh::ROUNDS - 1))) - 1u : kBins - 1u;
             *reinterpret_cast<uint4 *>(&hist[4 * tid]) = make_uint4(0u, 0u, 0u, 0u);
             __syncthreads();
 #pragma unroll 1
@@ -191,7 +201,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) fd_evict_select_kernel(const _
                 }
             }
             uint32_t total;
-            uint32_t above = cta_prefix(c[0] + c[1] + c[2] + c[3], sums, warp, lane, total);
+            uint32_t above = cta_prefix<kSelWarps>(c[0] + c[1] + c[2] + c[3], sums, warp, lane, total);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (above < left && above + c[e] >= left) {
@@ -233,9 +243,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) fd_evict_select_kernel(const _
         }
         __syncthreads();
         uint32_t total;
-        const uint32_t mine = tid < kSelPer * kSelWarps ? places[tid] : 0u;
-        const uint32_t at = cta_prefix(mine, sums, warp, lane, total);
-        if (tid < kSelPer * kSelWarps) places[tid] = at;
+        const uint32_t mine = tid < Sh::PLACES ? places[tid] : 0u;
+        const uint32_t at = cta_prefix<kSelWarps>(mine, sums, warp, lane, total);
+        if (tid < Sh::PLACES) places[tid] = at;
         if (tid == 0) tile_total[parity] = total;
         if (ctas > 1) cluster_sync(); else __syncthreads();
         uint32_t sure0 = sure_run, tie0 = tie_run;  // of this CTA's tile
@@ -479,23 +489,27 @@ cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
     // CTAs per row: up to one per tile of the longest row there can be, while
     // all of them still run at once.
     const long long longest = std::min<long long>(p.weights_stride, (long long)p.max_blocks * p.page_size);
+    const bool short_rows = longest <= SelShape<128>::TILE;
     int ctas = 1;
-    while (ctas < kMaxSelCtas && (long long)ctas * kSelTile < longest && bh * ctas * 2 <= 2LL * sms) ctas *= 2;
+    while (!short_rows && ctas < kMaxSelCtas && (long long)ctas * SelShape<512>::TILE < longest &&
+           bh * ctas * 2 <= 2LL * sms)
+        ctas *= 2;
     if (bh * ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     {
         cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ctas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)ctas;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(bh * ctas));
-        cfg.blockDim = dim3(kSelThreads);
+        cfg.blockDim = dim3(short_rows ? 128 : 512);
         cfg.stream = stream;
         cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, fd_evict_select_kernel, p, ctas);
+        cfg.numAttrs = ctas > 1 ? 2 : 1;
+        const cudaError_t e = short_rows ? cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<128>, p, ctas)
+                                         : cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<512>, p, ctas);
         if (e != cudaSuccess) return e;
     }
     const int per_row = in_place ? slices : (int)chunks;

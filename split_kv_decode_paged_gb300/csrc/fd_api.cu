@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "fd_internal.h"
+#include "weights.cuh"
 
 namespace fd {
 
@@ -1008,13 +1009,13 @@ bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
         plan->kv_rows * plan->row_fold != p.B || plan->num_splits < 1 || plan->chunk_tokens < 1 || plan->grid_ctas < 1 ||
         plan->head_subgroups < 1)
         return false;
-    const size_t row = (size_t)plan->chunk_tokens * sizeof(float);  // one chunk's scores of one query row
+    // one chunk's scores of a KV head
+    const size_t chunk = (size_t)plan->chunk_tokens * score_stride((p.Hq / p.Hkv) * plan->row_fold) * sizeof(float);
     l->fused = plan->head_subgroups == 1;
     l->separate = plan->num_splits > 1 || !l->fused;
     l->scores = align256((size_t)p.B * p.Hq * sizeof(float));
-    l->cta_scores = l->scores + (l->separate ? align256((size_t)p.B * p.Hq * plan->num_splits * row) : 0);
-    l->bytes = l->cta_scores +
-               (l->fused ? align256((size_t)plan->grid_ctas * (p.Hq / p.Hkv) * plan->row_fold * row) : 0);
+    l->cta_scores = l->scores + (l->separate ? align256((size_t)plan->kv_rows * p.Hkv * plan->num_splits * chunk) : 0);
+    l->bytes = l->cta_scores + (l->fused ? align256((size_t)plan->grid_ctas * chunk) : 0);
     return true;
 }
 

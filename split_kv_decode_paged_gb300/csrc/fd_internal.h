@@ -60,8 +60,8 @@ struct DecodeParams {
     int stall_role;            // 1: producer before its first load; 2: consumers before the first release
     int qn;                    // query tokens per KV row, causal among them (1: one-token decode)
     // Score-writing instances (attention-weight totals) only.
-    float *scores;             // [Bkv, Hkv, cap, G * fold] log2-unit scores of rows that are split (or not w_fused)
-    float *cta_scores;         // w_fused: [grid, chunk, G * fold], each CTA's scores of its current whole row
+    float *scores;             // [Bkv, Hkv, cap, score_stride(G * fold)] log2-unit scores of rows that are split (or not w_fused)
+    float *cta_scores;         // w_fused: [grid, chunk, score_stride(G * fold)], each CTA's scores of its current whole row
     const float *w_in;         // [Bkv, Hkv, w_stride] or null (zeros)
     float *w_out;
     int w_stride;
@@ -75,7 +75,7 @@ struct DecodeParams {
 
 // Attention-weight totals from the scores and lse of a decode call.
 struct WeightParams {
-    const float *scores;       // [Bkv, Hkv, cap, R]
+    const float *scores;       // [Bkv, Hkv, cap, score_stride(R)]
     const float *lse;          // [Bkv * fold, Hq]
     const float *in;           // [Bkv, Hkv, weights_stride] or null (zeros)
     float *out;                // [Bkv, Hkv, weights_stride]

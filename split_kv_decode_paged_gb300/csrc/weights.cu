@@ -16,7 +16,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid_constant__ WeightParams p, int chunks) {
     grid_dependency_wait();
-    extern __shared__ float lse2[];  // R: the rows' lse in log2 units, then R ones
+    extern __shared__ float lse2[];  // the rows' lse in log2 units, then ones (padding: zeros)
+    const int stride = score_stride(p.R);
     const long long bh = blockIdx.x / chunks;
     const int chunk = (int)(blockIdx.x % chunks);
     const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv);
@@ -33,17 +34,18 @@ __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid
         const size_t row = ((size_t)b * p.fold + r / p.G) * p.Hq + (size_t)h * p.G + r % p.G;
         const float l = p.lse[row];
         lse2[r] = l == -INFINITY ? 0.f : l * kLog2e;
-        lse2[p.R + r] = 1.f;
+        lse2[stride + r] = 1.f;
     }
+    for (int r = p.R + threadIdx.x; r < stride; r += kWeightThreads) lse2[r] = lse2[stride + r] = 0.f;
     __syncthreads();
     const size_t at = (size_t)bh * p.weights_stride;
-    sum_weights<kWeightThreads, kWeightFly>(p.scores + (size_t)bh * p.cap * p.R, p.R, lse2, lse2 + p.R,
+    sum_weights<kWeightThreads, kWeightFly>(p.scores + (size_t)bh * p.cap * stride, p.R, lse2, lse2 + stride,
                                             p.in ? p.in + at : nullptr, p.out + at, t0, t1, threadIdx.x);
 }
 
 bool weights_launchable(int Bkv, int Hkv, long long cap, long long R) {
     const long long chunks = (cap + kWeightChunk - 1) / kWeightChunk;
-    return chunks <= 0x7fffffffLL / ((long long)Bkv * Hkv) && R * 2 * (long long)sizeof(float) <= 48 * 1024;
+    return chunks <= 0x7fffffffLL / ((long long)Bkv * Hkv) && (R + 3) * 2 * (long long)sizeof(float) <= 48 * 1024;
 }
 
 // For sizes that weights_launchable() takes.
@@ -56,7 +58,7 @@ cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kWeightThreads);
-    cfg.dynamicSmemBytes = (size_t)wp.R * 2 * sizeof(float);
+    cfg.dynamicSmemBytes = (size_t)score_stride(wp.R) * 2 * sizeof(float);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
