@@ -11,6 +11,17 @@ import torch
 from . import _lib
 
 
+def _pool_sizes(entry, k_pages, block_table):
+    """(num_pages, page_size, Hkv, D), max_blocks of the pool and its table."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError(f"{entry}: k_pages must be a tensor [num_pages, page_size, Hkv, D]")
+    if k_pages.dtype not in (torch.float16, torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"{entry}: k_pages must be float16, bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError(f"{entry}: block_table must be a tensor [B, max_blocks]")
+    return k_pages.shape, block_table.shape[1]
+
+
 def append_kv_norm(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, q_weight=None, k_weight=None, eps=1e-6,
                    rotary_cos=None, rotary_sin=None, interleaved=False, positions=None, new_lens=None, k_scale=None,
                    v_scale=None, q_out=None, status=None, stream=None):
@@ -35,11 +46,12 @@ def append_kv_norm(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, q_w
         raise ValueError("append_kv_norm: k_new must be a tensor [B, T, Hkv, D] or [B, Hkv, D]")
     if q is not None and (not isinstance(q, torch.Tensor) or q.dim() != k_new.dim()):
         raise ValueError("append_kv_norm: q must have k_new's dimensions")
+    if k_new.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"append_kv_norm: k_new must be float16 or bfloat16, got {k_new.dtype}")
     Hkv, D = k_new.shape[-2:]
     Hq = Hkv if q is None else q.shape[-2]
-    num_pages, page_size = k_pages.shape[:2]
-    prob = _lib.make_problem(k_new.shape[0], Hq, Hkv, D, page_size, block_table.shape[1], num_pages, k_new.dtype,
-                             k_pages.dtype)
+    (num_pages, page_size, _, _), max_blocks = _pool_sizes("append_kv_norm", k_pages, block_table)
+    prob = _lib.make_problem(k_new.shape[0], Hq, Hkv, D, page_size, max_blocks, num_pages, k_new.dtype, k_pages.dtype)
     if q is not None and q_out is None:
         q_out = _lib.empty_on(q.shape, q.dtype, q.device, stream)
     _lib.fd_append_kv_norm(prob, q, k_new, v_new, q_out, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
@@ -63,10 +75,8 @@ def evict_kv(k_pages, v_pages, block_table, seq_lens, weights, budget, sinks=0, 
                              weights_out, k_scale, v_scale, status)
         if done is not None:
             return done
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("evict_kv: k_pages must be a tensor [num_pages, page_size, Hkv, D]")
-    num_pages, page_size, Hkv, D = k_pages.shape
-    B, max_blocks = block_table.shape
+    (num_pages, page_size, Hkv, D), max_blocks = _pool_sizes("evict_kv", k_pages, block_table)
+    B = block_table.shape[0]
     act = torch.bfloat16 if k_pages.dtype == torch.float8_e4m3fn else k_pages.dtype  # the op has no activations
     prob = _lib.make_problem(B, Hkv, Hkv, D, page_size, max_blocks, num_pages, act, k_pages.dtype)
     if int(budget) < 1:

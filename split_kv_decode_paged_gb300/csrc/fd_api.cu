@@ -1120,6 +1120,7 @@ fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *arg
     if (fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr)) return FD_ERR_INVALID_ARG;
     if ((a.q == nullptr) != (a.q_out == nullptr)) return FD_ERR_INVALID_ARG;
     if (p.Hq > kMaxHeads) return FD_ERR_UNSUPPORTED;  // the kernel's row offsets are ints
+    if (a.q && a.q == a.q_out && a.q_stride != a.q_out_stride) return FD_ERR_INVALID_ARG;
     if (a.tokens < 1 || !(a.eps > 0.f) || !std::isfinite(a.eps)) return FD_ERR_INVALID_ARG;
     if (!aligned(a.q, 16) || !aligned(a.q_out, 16) || !aligned(a.k_new, 16) || !aligned(a.v_new, 16) ||
         !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||

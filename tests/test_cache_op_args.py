@@ -64,6 +64,7 @@ def test_append_rejects_bad_pools_and_problems(fdlib):
     assert call_append(fdlib, n, p=p8, ks=A, vs=A + 2) == BAD
     assert call_append(fdlib, n, p=prob(D=96)) == UNSUP
     assert call_append(fdlib, n, p=prob(page_size=24)) == BAD
+    assert call_append(fdlib, norm_args(q_out_stride=2048)) == BAD  # q itself at another stride
     assert call_append(fdlib, norm_args(q_stride=1 << 40, q_out_stride=1 << 40), p=prob(Hq=1 << 21)) == UNSUP
     # a grid beyond what a launch can have
     big = prob(B=8192)
@@ -214,7 +215,9 @@ def append_kw(**kw):
     (dict(rotary_cos=z(9, dtype=torch.float32)), "2-D"), (dict(positions=z(B, dtype=torch.int64)), "positions.*dtype"),
     (dict(new_lens=z(B + 1, dtype=torch.int32)), "new_lens.*shape"), (dict(k_scale=z(1)), "k_scale must be None"),
     (dict(v_pages=z(NP, PS, HKV, 64)), "v_pages.*shape"), (dict(block_table=z(B, MB)), "block_table.*dtype"),
-    (dict(q=None), "q_out must be None"), (dict(q_out=z(B, T, HQ, D, dtype=torch.float32)), "q_out.*dtype"),
+    (dict(k_new=z(B, T, HKV, D, dtype=torch.float32)), "k_new must be float16 or bfloat16"),
+    (dict(k_pages=None), "k_pages must be a tensor"), (dict(k_pages=z(NP, PS, HKV, D, dtype=torch.float32)), "k_pages must be float16"),
+    (dict(block_table=None), "block_table must be a tensor"), (dict(q=None), "q_out must be None"), (dict(q_out=z(B, T, HQ, D, dtype=torch.float32)), "q_out.*dtype"),
     (dict(), "must be a CUDA tensor"),
 ])
 def test_append_binding_refusals(fdlib, kw, msg):
@@ -223,7 +226,7 @@ def test_append_binding_refusals(fdlib, kw, msg):
 
 
 @pytest.mark.parametrize("kw,msg", [
-    (dict(budget=0), "budget"), (dict(k_pages=None), "k_pages"), (dict(weights=z(B, HKV, 50)), "weights.*dtype"),
+    (dict(budget=0), "budget"), (dict(k_pages=None), "k_pages"), (dict(block_table=z(B)), "block_table must be a tensor"), (dict(weights=z(B, HKV, 50)), "weights.*dtype"),
     (dict(weights=z(B, HKV + 1, 50, dtype=torch.float32)), "weights.*shape"),
     (dict(weights_out=z(B, HKV, 51, dtype=torch.float32)), "weights_out.*shape"),
     (dict(dst_table=z(B, MB + 1, dtype=torch.int32)), "dst_table.*shape"), (dict(seq_lens=z(B)), "seq_lens.*dtype"),

@@ -175,3 +175,32 @@ def test_graph_replay_and_other_stream(fdlib):
     torch.cuda.synchronize()
     assert torch.equal(n1, n2) and torch.equal(k1, k2)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_graph_replay_of_long_rows(fdlib):
+    """Rows that a cluster of CTAs selects, captured and replayed on other weights."""
+    gen = torch.Generator().manual_seed(4)
+    L, ps, budget = 40000, 64, 20000
+    bt, pages, spare = R.make_table(gen, [L], ps, extra=400)
+    kp, _ = R.make_pool(gen, pages, ps, 1, 64, torch.bfloat16)
+    dst = torch.full_like(bt, -1)
+    dst[0, :313] = spare[:313]
+    gk, gv, bt, dst = kp.cuda(), kp.cuda().clone(), bt.cuda(), dst.cuda()
+    lens = torch.tensor([L], dtype=torch.int32).cuda()
+    w = torch.zeros(1, 1, L, device="cuda")
+    call = lambda: fd.evict_kv(gk, gv, bt, lens, w, budget, 4, 1000, dst_table=dst)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n, kept = call()
+    for seed in range(3):
+        v = torch.rand(1, 1, L, generator=torch.Generator().manual_seed(seed))
+        w.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        keep = R.evict(v[0, 0], L, budget, 4, 1000)
+        assert n.tolist() == [budget] and kept[0, 0].tolist() == keep.tolist()
+        j = torch.arange(budget)
+        old = kp[bt.cpu()[0, keep // ps].long(), keep % ps, 0]
+        assert torch.equal(gk.cpu()[dst.cpu()[0, j // ps].long(), j % ps, 0], old)
