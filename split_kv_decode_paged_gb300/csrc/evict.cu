@@ -107,12 +107,15 @@ __device__ __forceinline__ uint4 cluster_read4(const uint32_t *p, uint32_t rank)
     return v;
 }
 
-// One cluster of `ctas` CTAs (a power of two) per (sequence, KV head); tile i * ctas + rank of
-// the row is CTA rank's in round i.  All branches that hold a barrier depend on
-// the row alone, so the cluster's CTAs take them together.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kernel(const __grid_constant__ EvictParams p,
-                                                                                  int ctas) {
+// One cluster of `ctas` CTAs (a power of two; CLUSTER: more than one) per
+// (sequence, KV head); tile i * ctas + rank of the row is CTA rank's in round
+// i.  All branches that hold a barrier depend on the row alone, so the
+// cluster's CTAs take them together.  64 registers: three or four CTAs of 512
+// threads an SM instead of two spill and measured 1 to 2% slower.
+template <int THREADS, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    fd_evict_select_kernel(const __grid_constant__ EvictParams p, int ctas_in) {
+    const int ctas = CLUSTER ? ctas_in : 1;
     using Sh = SelShape<THREADS>;
     constexpr int kSelThreads = THREADS, kSelWarps = Sh::WARPS, kSelTile = Sh::TILE, kBins = Sh::BINS;
     __shared__ __align__(16) uint32_t hist[kBins];
@@ -188,23 +191,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kerne
                         atomicAdd(&hist[(key >> shift) & digit], 1u);
                 }
             }
-            if (ctas > 1) cluster_sync(); else __syncthreads();
+            if constexpr (CLUSTER) cluster_sync(); else __syncthreads();
             // the bin, from the top, where the cluster's count reaches `left`
             uint32_t c[4];  // bins kBins - 1 - 4 tid and down
             {
                 const uint32_t *mine = &hist[kBins - 4 - 4 * tid];
-                uint4 v[kMaxSelCtas];
-                v[0] = *reinterpret_cast<const uint4 *>(mine);
+                const uint4 own = *reinterpret_cast<const uint4 *>(mine);
+                c[0] = own.w;
+                c[1] = own.z;
+                c[2] = own.y;
+                c[3] = own.x;
+                if constexpr (CLUSTER) {
+                    uint4 v[kMaxSelCtas - 1];
 #pragma unroll
-                for (int r = 1; r < kMaxSelCtas; ++r)
-                    v[r] = r < ctas ? cluster_read4(mine, (uint32_t)((rank + r) & (ctas - 1))) : make_uint4(0u, 0u, 0u, 0u);
-                c[0] = c[1] = c[2] = c[3] = 0u;
+                    for (int r = 1; r < kMaxSelCtas; ++r)
+                        v[r - 1] = r < ctas ? cluster_read4(mine, (uint32_t)((rank + r) & (ctas - 1))) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int r = 0; r < kMaxSelCtas; ++r) {
-                    c[0] += v[r].w;
-                    c[1] += v[r].z;
-                    c[2] += v[r].y;
-                    c[3] += v[r].x;
+                    for (int r = 0; r < kMaxSelCtas - 1; ++r) {
+                        c[0] += v[r].w;
+                        c[1] += v[r].z;
+                        c[2] += v[r].y;
+                        c[3] += v[r].x;
+                    }
                 }
             }
             uint32_t total;
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kerne
                 }
                 above += c[e];
             }
-            if (ctas > 1) cluster_sync(); else __syncthreads();  // read everywhere: hist may be cleared
+            if constexpr (CLUSTER) cluster_sync(); else __syncthreads();  // read everywhere: hist may be cleared
             prefix |= sh_bin << shift;
             mask |= digit << shift;
             left = sh_left;
@@ -254,13 +262,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kerne
         const uint32_t at = cta_prefix<kSelWarps>(mine, sums, warp, lane, total);
         if (tid < Sh::PLACES) places[tid] = at;
         if (tid == 0) tile_total[parity] = total;
-        if (ctas > 1) cluster_sync(); else __syncthreads();
+        if constexpr (CLUSTER) cluster_sync(); else __syncthreads();
         uint32_t sure0 = sure_run, tie0 = tie_run;  // of this CTA's tile
-        {
+        if constexpr (CLUSTER) {
             uint32_t x[kMaxSelCtas];
 #pragma unroll
-            for (int r = 0; r < kMaxSelCtas; ++r)
-                x[r] = r < ctas ? (ctas > 1 ? cluster_read(&tile_total[parity], (uint32_t)r) : total) : 0u;
+            for (int r = 0; r < kMaxSelCtas; ++r) x[r] = r < ctas ? cluster_read(&tile_total[parity], (uint32_t)r) : 0u;
 #pragma unroll
             for (int r = 0; r < kMaxSelCtas; ++r) {
                 sure_run += x[r] & 0xffffu;
@@ -270,6 +277,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kerne
                     tie0 = tie_run;
                 }
             }
+        } else {
+            sure_run += total & 0xffffu;
+            tie_run += total >> 16;
         }
 #pragma unroll
         for (int k = 0; k < kSelPer; ++k) {
@@ -288,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fd_evict_select_kerne
     }
     if (wo)
         for (int t = n + part; t < L; t += parts) wo[t] = 0.f;
-    if (ctas > 1) cluster_sync();  // no CTA leaves while its counts are read
+    if constexpr (CLUSTER) cluster_sync();  // no CTA leaves while its counts are read
 }
 
 struct RowPlace {
@@ -515,8 +525,9 @@ cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = ctas > 1 ? 2 : 1;
-        const cudaError_t e = short_rows ? cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<128>, p, ctas)
-                                         : cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<512>, p, ctas);
+        const cudaError_t e = short_rows ? cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<128, false>, p, ctas)
+                              : ctas > 1 ? cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<512, true>, p, ctas)
+                                         : cudaLaunchKernelEx(&cfg, fd_evict_select_kernel<512, false>, p, ctas);
         if (e != cudaSuccess) return e;
     }
     const int per_row = in_place ? slices : (int)chunks;
