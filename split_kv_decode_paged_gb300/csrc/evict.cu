@@ -17,8 +17,8 @@
 // add up their histograms and counts through distributed shared memory.
 //
 // Measured: 64 sequences x 8 heads of 512-8192 tokens to at most 4096, bf16, D =
-// 128, into other pages 278 us (1.72 GB, 6.2 TB/s, 91% of the copy rate): the
-// copy 249, the selection 28.  Four E4M3 sequences x 8 heads of 60000-65536
+// 128, into other pages 274 us (1.72 GB, 6.3 TB/s, 93% of the copy rate): the
+// copy 249, the selection 25.  Four E4M3 sequences x 8 heads of 60000-65536
 // tokens halved 125 us: the copy 88 (floor 79), the selection 36, of which a
 // digit of the radix select costs 6 through the cluster (1.2 in one CTA).  In
 // place 247 and 347 us: few rows leave few slices to work on at once.

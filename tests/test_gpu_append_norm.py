@@ -95,6 +95,35 @@ def test_types_and_rotations(fdlib, kv, act, D, rot):
     check(kv, act, B=3, T=1, Hq=6, Hkv=3, D=D, ps=16, rd=rd, interleaved=rot.endswith("pairs"), seed=len(rot) + D)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rd", [(64, 2), (64, 8), (64, 24), (64, 62), (128, 40), (128, 120), (128, 126), (128, 4)])
+def test_partial_rotations(fdlib, D, rd, interleaved):
+    check("bf16", "bf16", B=2, T=5, Hq=4, Hkv=2, D=D, ps=16, rd=rd, interleaved=interleaved, seed=rd)
+    check("e4m3", "f16", B=2, T=1, Hq=2, Hkv=1, D=D, ps=16, rd=rd, interleaved=interleaved, seed=rd + 1)
+
+
+def test_tables_and_weights_off_alignment(fdlib):
+    """Cosines, sines and norm weights that start 4 (2) bytes off 16: read element by element."""
+    gen = torch.Generator().manual_seed(7)
+    B, H, D, ps = 2, 3, 128, 16
+    bt, pages, _ = R.make_table(gen, [30] * B, ps)
+    kp = torch.zeros(pages, ps, H, D, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(B, H, D, generator=gen).bfloat16().cuda()
+    cos, sin = (t.cuda() for t in tables(64, D // 2))
+    w = (1 + torch.randn(D, generator=gen)).bfloat16().cuda()
+    lens = torch.tensor([20, 3], dtype=torch.int32).cuda()
+    off = lambda t: torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)  # noqa: E731
+    for interleaved in (False, True):
+        ref = fd.append_kv_norm(x, x, x, kp, kp.clone(), bt.cuda(), lens, q_weight=w, k_weight=w, rotary_cos=cos,
+                                rotary_sin=sin, interleaved=interleaved)
+        one = kp.clone()
+        got = fd.append_kv_norm(x, x, x, kp, kp.clone(), bt.cuda(), lens, q_weight=off(w), k_weight=off(w),
+                                rotary_cos=off(cos), rotary_sin=off(sin), interleaved=interleaved)
+        torch.cuda.synchronize()
+        assert off(cos).data_ptr() % 16 == 4 and off(w).data_ptr() % 4 == 2
+        assert torch.equal(bits(ref), bits(got)) and torch.equal(bits(one), bits(kp))
+
+
 @pytest.mark.parametrize("B,T,Hq,Hkv,ps", [(1, 1, 1, 1, 16), (1, 1, 32, 8, 64), (2, 5, 7, 7, 48), (1, 300, 5, 1, 16),
                                            (40, 33, 12, 2, 32), (700, 1, 3, 1, 16)])
 def test_sizes(fdlib, B, T, Hq, Hkv, ps):
