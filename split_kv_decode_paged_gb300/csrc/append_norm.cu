@@ -373,10 +373,11 @@ cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream) {
     const int rpw = 256 / D;
     const int steps = (p.Hq + rpw - 1) / rpw + 2 * ((p.Hkv + rpw - 1) / rpw);
     // Few tokens: a step a warp.  Many: a warp per token (measured on 16.6K
-    // tokens of 24 steps: 71.6 us; 2 warps a token 75.4, 4 warps 96.7), or as
-    // many as give every SM its 64 warps.
+    // tokens of 24 steps: 70 us; 2 warps a token 75, 4 warps 97); between, as
+    // many as give every SM 12 warps (1000 tokens of 24 steps 8.7 us; 64 warps
+    // an SM 11.7, a step a warp 11.1).
     const bool one = tokens * steps <= 16384;
-    p.parts = one ? steps : (int)std::min<long long>(steps, (9728 + tokens - 1) / tokens);
+    p.parts = one ? steps : (int)std::min<long long>(steps, (152 * 12 + tokens - 1) / tokens);
     const long long blocks = (tokens * p.parts + kNormWarps - 1) / kNormWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto al = [](const void *x, size_t n) { return reinterpret_cast<uintptr_t>(x) % n == 0; };

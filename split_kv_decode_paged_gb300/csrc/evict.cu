@@ -19,8 +19,9 @@
 // Measured: 64 sequences x 8 heads of 512-8192 tokens to at most 4096, bf16, D =
 // 128, into other pages 274 us (1.72 GB, 6.3 TB/s, 93% of the copy rate): the
 // copy 249, the selection 25.  Four E4M3 sequences x 8 heads of 60000-65536
-// tokens halved 125 us: the copy 88 (floor 79), the selection 36, of which a
-// digit of the radix select costs 6 through the cluster (1.2 in one CTA).  In
+// tokens halved 115 us: the copy 88 (floor 79), the selection 26.  A digit of
+// the radix select costs 1.2 us in one CTA; through the cluster 6 with every
+// CTA reading all the others' bins, 3 with their sums read first.  In
 // place 247 and 347 us: few rows leave few slices to work on at once.
 #include <algorithm>
 
@@ -56,6 +57,17 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 __device__ __forceinline__ float key_weight(uint32_t key) {
     if (key == kKeyNan) return __uint_as_float(0x7fffffffu);
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// Exclusive prefix over the warp of v.
+__device__ __forceinline__ uint32_t warp_prefix(uint32_t v, int lane) {
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    return incl - v;
 }
 
 // Exclusive prefix over the CTA of v (one value a thread) and its total; two
@@ -191,41 +203,69 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                         atomicAdd(&hist[(key >> shift) & digit], 1u);
                 }
             }
-            if constexpr (CLUSTER) cluster_sync(); else __syncthreads();
-            // the bin, from the top, where the cluster's count reaches `left`
-            uint32_t c[4];  // bins kBins - 1 - 4 tid and down
-            {
-                const uint32_t *mine = &hist[kBins - 4 - 4 * tid];
-                const uint4 own = *reinterpret_cast<const uint4 *>(mine);
-                c[0] = own.w;
-                c[1] = own.z;
-                c[2] = own.y;
-                c[3] = own.x;
-                if constexpr (CLUSTER) {
-                    uint4 v[kMaxSelCtas - 1];
+            __syncthreads();
+            // The bin, from the top, where the count reaches `left`.  Thread i
+            // has the bins kBins - 1 - 4 i and down.
+            const uint4 own = *reinterpret_cast<const uint4 *>(&hist[kBins - 4 - 4 * tid]);
+            if constexpr (!CLUSTER) {
+                const uint32_t c[4] = {own.w, own.z, own.y, own.x};
+                uint32_t total;
+                uint32_t above = cta_prefix<kSelWarps>(c[0] + c[1] + c[2] + c[3], sums, warp, lane, total);
 #pragma unroll
-                    for (int r = 1; r < kMaxSelCtas; ++r)
-                        v[r - 1] = r < ctas ? cluster_read4(mine, (uint32_t)((rank + r) & (ctas - 1))) : make_uint4(0u, 0u, 0u, 0u);
+                for (int e = 0; e < 4; ++e) {
+                    if (above < left && above + c[e] >= left) {
+                        sh_bin = (uint32_t)(kBins - 1 - 4 * tid - e);
+                        sh_left = left - above;
+                    }
+                    above += c[e];
+                }
+                __syncthreads();  // read: hist may be cleared
+            } else {
+                // Every CTA's sums of a warp's 128 bins first, then the bins of
+                // the one warp that holds the place: little goes between the SMs.
+                uint32_t s = own.x + own.y + own.z + own.w;
 #pragma unroll
-                    for (int r = 0; r < kMaxSelCtas - 1; ++r) {
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) sums[warp] = s;
+                cluster_sync();
+                if (warp == 0) {
+                    static_assert(kSelWarps <= 32, "a lane per warp's sum");
+                    uint32_t x[kMaxSelCtas];
+#pragma unroll
+                    for (int r = 0; r < kMaxSelCtas; ++r)
+                        x[r] = r < ctas && lane < kSelWarps ? cluster_read(&sums[lane], (uint32_t)r) : 0u;
+                    uint32_t sum = 0;
+#pragma unroll
+                    for (int r = 0; r < kMaxSelCtas; ++r) sum += x[r];
+                    const uint32_t above_w = warp_prefix(sum, lane);
+                    const unsigned hit = __ballot_sync(0xffffffffu, above_w < left && above_w + sum >= left);
+                    const int at_warp = __ffs(hit) - 1;
+                    const uint32_t base = __shfl_sync(0xffffffffu, above_w, at_warp);
+                    const int i = at_warp * 32 + lane;
+                    uint4 v[kMaxSelCtas];
+#pragma unroll
+                    for (int r = 0; r < kMaxSelCtas; ++r)
+                        v[r] = r < ctas ? cluster_read4(&hist[kBins - 4 - 4 * i], (uint32_t)r) : make_uint4(0u, 0u, 0u, 0u);
+                    uint32_t c[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int r = 0; r < kMaxSelCtas; ++r) {
                         c[0] += v[r].w;
                         c[1] += v[r].z;
                         c[2] += v[r].y;
                         c[3] += v[r].x;
                     }
-                }
-            }
-            uint32_t total;
-            uint32_t above = cta_prefix<kSelWarps>(c[0] + c[1] + c[2] + c[3], sums, warp, lane, total);
+                    uint32_t above = base + warp_prefix(c[0] + c[1] + c[2] + c[3], lane);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (above < left && above + c[e] >= left) {
-                    sh_bin = (uint32_t)(kBins - 1 - 4 * tid - e);
-                    sh_left = left - above;
+                    for (int e = 0; e < 4; ++e) {
+                        if (above < left && above + c[e] >= left) {
+                            sh_bin = (uint32_t)(kBins - 1 - 4 * i - e);
+                            sh_left = left - above;
+                        }
+                        above += c[e];
+                    }
                 }
-                above += c[e];
+                cluster_sync();  // read everywhere: hist and sums may be cleared
             }
-            if constexpr (CLUSTER) cluster_sync(); else __syncthreads();  // read everywhere: hist may be cleared
             prefix |= sh_bin << shift;
             mask |= digit << shift;
             left = sh_left;
