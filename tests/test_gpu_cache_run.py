@@ -118,3 +118,50 @@ def test_serving_loop(fdlib, kv, diff):
         for h in range(Hkv):
             assert held[b][h] == sorted(held[b][h]) and held[b][h][:sinks] == list(range(sinks))
             assert held[b][h][-recent:] == list(range(int(pos[b]) - recent, int(pos[b])))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_back_to_back_calls_equal_waited_ones(fdlib, kv):
+    """Kernels that start while the one before drains: the same results, bit for
+    bit, as with a synchronisation after every call."""
+    dt = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[kv]
+    B, Hq, Hkv, D, ps, room, budget = 24, 16, 4, 128, 16, 2304, 1500
+    res = []
+    for wait in (True, False):
+        gen = torch.Generator().manual_seed(5)
+        dev = torch.Generator(device="cuda").manual_seed(6)
+        bt = torch.randperm(B * room // ps, generator=gen).to(torch.int32).view(B, -1).cuda()
+        kp, ks = R.make_pool(gen, bt.numel(), ps, Hkv, D, dt)
+        vp, vs = R.make_pool(gen, bt.numel(), ps, Hkv, D, dt)
+        kp, vp, ks, vs = (None if t is None else t.cuda() for t in (kp, vp, ks, vs))
+        sc = dict(k_scale=ks, v_scale=vs)
+        cos, sin = (t.cuda() for t in tables(6000, D // 2))
+        w, lam = torch.ones(D, dtype=torch.bfloat16, device="cuda"), torch.rand(Hq, generator=dev, device="cuda")
+        lens = torch.randint(1400, 1900, (B,), generator=dev, device="cuda", dtype=torch.int32)
+        pos = lens.clone()
+        prob = fd.make_problem(B, Hq, Hkv, D, ps, room // ps, bt.numel(), torch.bfloat16, dt)
+        dec, dif = fd.PagedDecoder(prob, [1900] * B, track_weights=True), fd.DiffDecoder(prob, [1900] * B)
+        totals = torch.zeros(B, Hkv, room, device="cuda")
+        feed = [torch.randn(B, 7, (Hq + 2 * Hkv) * D, generator=dev, device="cuda").bfloat16() for _ in range(6)]
+        outs = []
+        step = torch.cuda.synchronize if wait else (lambda: None)
+        torch.cuda.synchronize()
+        for x in feed:
+            q, k, v = (t.unflatten(-1, (-1, D)) for t in x.split([Hq * D, Hkv * D, Hkv * D], -1))
+            q = fd.append_kv_norm(q, k, v, kp, vp, bt, lens, q_weight=w, k_weight=w, rotary_cos=cos, rotary_sin=sin,
+                                  positions=pos, **sc)
+            step()
+            lens, pos = lens + 7, pos + 7
+            last = q[:, -1].contiguous()
+            out, lse, _ = dec.decode_weights(last, kp, vp, bt, lens, totals, **sc)
+            step()
+            out2, lse2 = dif(last, kp, vp, bt, lens, lam, norm_weight=w, **sc)
+            step()
+            lens, kept = fd.evict_kv(kp, vp, bt, lens, totals, budget, 4, 200, weights_out=totals, **sc)
+            step()
+            outs += [q, out, lse, out2, lse2, lens, kept]
+        torch.cuda.synchronize()
+        dec.check()
+        dif.check()
+        res.append(outs + [totals, kp.view(torch.uint8), vp.view(torch.uint8)])
+    assert all(torch.equal(a, b) for a, b in zip(*res))

@@ -97,6 +97,15 @@ def test_long_rows(fdlib, fresh):
     check("e4m3", [20000], 1, 128, 128, 9999, 16, 0, fresh, seed=2)
 
 
+@pytest.mark.parametrize("fresh,weights", [(False, "in place"), (True, "out")])
+def test_rows_of_several_rounds(fdlib, fresh, weights):
+    """More tokens than the selecting CTAs hold at once: one row longer than a
+    cluster's tiles, and so many rows that each has one CTA."""
+    check("f16", [140001], 1, 64, 64, 90000, 4, 1000, fresh, seed=1, weights=weights)
+    check("bf16", [140001], 1, 64, 128, 60000, 0, 0, fresh, seed=2, weights=weights, w=torch.full((1, 1, 140004), 0.25))
+    check("e4m3", [9000 + i for i in range(39)], 4, 64, 64, 7000, 4, 100, fresh, seed=3, weights=weights)
+
+
 @pytest.mark.parametrize("weights", ["out", "in place", "none"])
 def test_weights_out(fdlib, weights):
     check("bf16", [700, 5, 90], 2, 64, 16, 77, 3, 20, False, weights=weights)
