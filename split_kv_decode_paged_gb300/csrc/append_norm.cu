@@ -15,8 +15,8 @@
 //
 // One pass: every input is read and every output written once.  Many tokens
 // are bound by instruction issue (63% of the slots) about as much as by DRAM:
-// 16.6K tokens of 32 + 8 + 8 heads, D = 128, bf16, 411 MB in 69 us, 5.97 TB/s,
-// 88% of the copy rate.  A loop per kind of row halved the instructions (no
+// 16.6K tokens of 32 + 8 + 8 heads, D = 128, bf16, 411 MB in 70 us, 5.9 TB/s,
+// 86% of the copy rate.  A loop per kind of row halved the instructions (no
 // selects between q, k and v): 105 -> 75 us.  Few tokens are a chain of
 // latencies (lengths, page id, cosines): 1 token 3.6 us, 256 tokens of 64 + 8 +
 // 8 heads into E4M3 6.2 us.
