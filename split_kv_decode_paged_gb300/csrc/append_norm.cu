@@ -33,9 +33,9 @@ constexpr int kNormUnroll = 4;  // steps of a warp whose rows are requested toge
 // How the pairs of a row lie in the lanes.
 enum RotKind {
     ROT_NONE = 0,
-    ROT_PAIRS = 1,   // (2i, 2i + 1), rotary_dim a multiple of 8: in the lane
+    ROT_PAIRS = 1,   // (2i, 2i + 1): in the lane
     ROT_HALVES = 2,  // halves, rotary_dim a multiple of 8: four elements of each half in the lane
-    ROT_ANY = 3      // through shared memory; also for tables that are not 16-byte aligned
+    ROT_ANY = 3      // other halves: through shared memory
 };
 
 template <bool BF16>
@@ -158,17 +158,23 @@ __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(cons
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int d = da + e;
-                const int ai = p.interleaved ? d >> 1 : (d < half ? d : d - half);
+                const int ai = d < half ? d : d - half;
                 c[e] = d < rd ? __ldg(cr + ai) : 1.f;
                 s[e] = d < rd ? __ldg(sr + ai) : 0.f;
             }
-        } else {
+        } else if (p.cs_vec) {
             // angle indices of the lane's pairs: 4 l .. 4 l + 3 either way
             if (8 * l < rd) {
                 const float4 x = __ldg(reinterpret_cast<const float4 *>(cr + 4 * l));
                 const float4 y = __ldg(reinterpret_cast<const float4 *>(sr + 4 * l));
                 c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
                 s[0] = y.x; s[1] = y.y; s[2] = y.z; s[3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[e] = 4 * l + e < half ? __ldg(cr + 4 * l + e) : 1.f;
+                s[e] = 4 * l + e < half ? __ldg(sr + 4 * l + e) : 0.f;
             }
         }
     }
@@ -206,12 +212,13 @@ __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(cons
                 }
             }
         } else if constexpr (ROT == ROT_PAIRS) {
-            if (da < rd) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = x[2 * e], bb = x[2 * e + 1];
-                    x[2 * e] = turn_first(a, bb, c[e], s[e]);
-                    x[2 * e + 1] = turn_second(bb, a, c[e], s[e]);
+            for (int e = 0; e < 4; ++e) {
+                const float a = x[2 * e], bb = x[2 * e + 1];
+                const float ra = turn_first(a, bb, c[e], s[e]), rb = turn_second(bb, a, c[e], s[e]);
+                if (4 * l + e < half) {
+                    x[2 * e] = ra;
+                    x[2 * e + 1] = rb;
                 }
             }
         } else if constexpr (ROT == ROT_ANY) {
@@ -224,14 +231,12 @@ __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(cons
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int d = da + e;
-                const int other = p.interleaved ? d ^ 1 : (d < half ? d + half : d - half);
-                y[e] = d < rd ? buf[other] : 0.f;
+                y[e] = d < rd ? buf[d < half ? d + half : d - half] : 0.f;
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int d = da + e;
-                const bool lower = p.interleaved ? (e & 1) == 0 : d < half;
-                const float r = lower ? turn_first(x[e], y[e], c[e], s[e]) : turn_second(x[e], y[e], c[e], s[e]);
+                const float r = d < half ? turn_first(x[e], y[e], c[e], s[e]) : turn_second(x[e], y[e], c[e], s[e]);
                 if (d < rd) x[e] = r;
             }
         }
@@ -366,8 +371,8 @@ cudaError_t launch_width(const NormAppendParams &p, int rot, bool one, unsigned 
 
 }  // namespace
 
-// D: 64 or 128 (validated); p.parts and p.w_vec are set here.  A grid that
-// CUDA cannot launch is cudaErrorInvalidConfiguration.
+// D: 64 or 128 (validated); p.parts, p.w_vec and p.cs_vec are set here.  A grid
+// that CUDA cannot launch is cudaErrorInvalidConfiguration.
 cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream) {
     const long long tokens = (long long)p.B * p.T;
     const int rpw = 256 / D;
@@ -384,11 +389,8 @@ cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream) {
     p.w_vec = al(p.qw, 8) && al(p.kw, 8);
     int rot = ROT_NONE;
     if (p.cos) {
-        const bool vec = al(p.cos, 16) && al(p.sin, 16);
-        if (vec && p.rotary_dim % 8 == 0)
-            rot = p.interleaved ? ROT_PAIRS : ROT_HALVES;
-        else
-            rot = ROT_ANY;
+        p.cs_vec = al(p.cos, 16) && al(p.sin, 16) && p.rotary_dim % 8 == 0;  // every row of four
+        rot = p.interleaved ? ROT_PAIRS : (p.rotary_dim % 8 == 0 ? ROT_HALVES : ROT_ANY);
     }
     return D == 128 ? launch_width<128>(p, rot, one, (unsigned)blocks, stream)
                     : launch_width<64>(p, rot, one, (unsigned)blocks, stream);

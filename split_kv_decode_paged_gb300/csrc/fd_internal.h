@@ -103,6 +103,7 @@ struct NormAppendParams {
     int kv_kind, is_bf16;
     int parts;                 // warps per token (set at launch)
     int w_vec;                 // both norm weights 8-byte aligned (set at launch)
+    int cs_vec;                // cosines and sines in groups of four 16-byte aligned (set at launch)
 };
 
 struct EvictParams {
