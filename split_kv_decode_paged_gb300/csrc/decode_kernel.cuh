@@ -1303,11 +1303,13 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 }
             }
             uint32_t pb[SUBT][NT][2];
-            uint32_t pl[SUBT][NT][2];  // low parts of the weights (P = hi + lo): bf16 V, and
-                                       // f16 products outside the plain decode (not E4M3 K/V with
-                                       // bf16 q: 11 bits of a weight are below a bf16 output's
-                                       // rounding, and the second product would cost 16%)
-            constexpr bool kPair = KV == KV_BF16 || (MODE != kPlain && !(FP8 && QBF16));
+            // Low parts of the weights (P = hi + lo): bf16 V, and f16 products
+            // outside the plain decode.  There the denominator sums the weights
+            // unrounded (see MODE), so the roundings of 11 bits alone would not
+            // cancel: up to 2^-12 of sum p |v|, which a difference of similar
+            // maps and its norm scale up and an fp32 output shows.
+            uint32_t pl[SUBT][NT][2];
+            constexpr bool kPair = KV == KV_BF16 || MODE != kPlain;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float mn0 = mrow[n][0], mn1 = mrow[n][1];
