@@ -87,8 +87,10 @@ __device__ __forceinline__ void load_weight4(const void *w, int f32, bool w16, i
 }
 
 // ONE: a warp has one step (few tokens: the latency of a call); its rows are
-// requested before the lengths, positions and page id that say where they go.
-// Otherwise a warp goes through every p.parts-th step of its token.
+// requested before the length, position and page id that say where they go, in
+// a padded batch once new_lens says that the token is there: what lies behind a
+// sequence's tokens is not read.  Otherwise a warp goes through every p.parts-th
+// step of its token.
 template <int D, bool BF16, bool FP8, int ROT, bool ONE>
 __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(const __grid_constant__ NormAppendParams p) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
@@ -120,23 +122,22 @@ __global__ void __launch_bounds__(kNormWarps * 32) fd_append_kv_norm_kernel(cons
     const uint16_t *krow = reinterpret_cast<const uint16_t *>(p.k) + tok * p.k_stride;
     const uint16_t *vrow = reinterpret_cast<const uint16_t *>(p.v) + tok * p.v_stride;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-    int fresh = p.T;
+    if (p.new_lens) {
+        const int fresh = __ldg(p.new_lens + b);
+        if (fresh < 0 || fresh > p.T) {
+            if (lane == 0 && part == 0 && i == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
+            return;
+        }
+        if (i >= fresh) return;
+    }
     uint4 first = none;
     if constexpr (ONE) {
         const int kind = part < sq ? 0 : (part < sq + sk ? 1 : 2);
         const int row = (part - (kind == 0 ? 0 : (kind == 1 ? sq : sq + sk))) * RPW + sub;
         if (row < (kind == 0 ? p.Hq : p.Hkv)) first = load8((kind == 0 ? qrow : (kind == 1 ? krow : vrow)) + row * D);
     }
-    if (p.new_lens) {
-        fresh = __ldg(p.new_lens + b);
-        if (i >= fresh && fresh >= 0) return;
-    }
     const int len = __ldg(p.seq_lens + b);
     const long long pos = (long long)(p.positions ? __ldg(p.positions + b) : len) + i;
-    if (fresh < 0 || fresh > p.T) {
-        if (lane == 0 && part == 0 && i == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
-        return;
-    }
     if (ROT != ROT_NONE && (pos < 0 || pos >= p.max_pos)) {
         if (lane == 0 && part == 0 && p.status) atomicOr(p.status, FD_DEV_CAPACITY);
         return;
