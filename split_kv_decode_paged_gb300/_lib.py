@@ -12,7 +12,8 @@ fails to load, every call raises.
 The calls a serving loop makes once a layer and step (append_kv_norm,
 evict_kv, PagedDecoder.decode_weights, DiffDecoder) first try fast(), the same
 marshalling in C++; it hands back every call that is not the ordinary case,
-and the functions here then check it, name what is wrong and raise.
+and the functions here then check it, name what is wrong and raise.  A call whose
+launches failed is not made a second time: it raises FdError there.
 """
 from __future__ import annotations
 
@@ -171,7 +172,7 @@ def fast():
         else:
             at = [ctypes.cast(f, ctypes.c_void_p).value for f in
                   (lib.fd_append_kv_norm, lib.fd_evict_kv, lib.fd_decode_paged_weights, lib.fd_decode_paged_diff)]
-            _fd_torch.init(*at)
+            _fd_torch.init(*at, FdError)
             _fast = _fd_torch
     return _fast
 

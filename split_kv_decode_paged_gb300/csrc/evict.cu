@@ -534,6 +534,7 @@ cudaError_t launch_move(const EvictParams &p, bool in_place, int per_row, unsign
 
 }  // namespace
 
+// cudaErrorInvalidConfiguration: sizes that cannot be launched, and nothing was.
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
     const long long bh = (long long)p.B * p.Hkv;
     if (bh > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -571,11 +572,13 @@ cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     const int per_row = in_place ? slices : (int)chunks;
-    const bool fp8 = p.row_bytes == p.D;
-    if (p.row_bytes == 256) return launch_move<256, false>(p, in_place, per_row, (unsigned)blocks, stream);
-    if (p.row_bytes == 64) return launch_move<64, true>(p, in_place, per_row, (unsigned)blocks, stream);
-    return fp8 ? launch_move<128, true>(p, in_place, per_row, (unsigned)blocks, stream)
-               : launch_move<128, false>(p, in_place, per_row, (unsigned)blocks, stream);
+    const auto move = p.row_bytes == 256 ? launch_move<256, false>
+                      : p.row_bytes == 64  ? launch_move<64, true>
+                      : p.row_bytes == p.D ? launch_move<128, true>
+                                           : launch_move<128, false>;
+    const cudaError_t e = move(p, in_place, per_row, (unsigned)blocks, stream);
+    // the selection is on its way: no refusal any more
+    return e == cudaErrorInvalidConfiguration ? cudaErrorUnknown : e;
 }
 
 }  // namespace fd

@@ -6,8 +6,10 @@
 //
 // Marshalling only.  Every function returns None where anything is not as the
 // ordinary case has it (another type, shape, layout or device, a stream given,
-// a status other than FD_OK): the Python binding then takes the call from the
-// start, so that its checks, messages and errors are the ones there are.
+// a call that libfd refuses): the Python binding then takes the call from the
+// start, so that its checks, messages and errors are the ones there are.  A call
+// that failed otherwise may have launched some of its kernels; it is not made
+// again, and FdError is raised here.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -27,8 +29,15 @@ decltype(&fd_evict_kv) g_evict = nullptr;
 decltype(&fd_decode_paged_weights) g_weights = nullptr;
 decltype(&fd_decode_paged_diff) g_diff = nullptr;
 
+PyObject *g_error = nullptr;  // FdError
+
 // Thrown where the call is not the ordinary case.
 struct Other {};
+
+// Thrown where the call failed in or after its launches.
+struct Failed {
+    fd_status status;
+};
 
 at::ScalarType torch_type(int t) {
     switch (t) {
@@ -148,14 +157,16 @@ const fd_plan_t *as_plan(PyObject *o) {
     return static_cast<const fd_plan_t *>(p);
 }
 
-// Run a libfd entry point without the interpreter's lock.
+// Run a libfd entry point without the interpreter's lock.  The three statuses
+// of a refusal come before anything is launched.
 template <typename F>
 void run(F &&f) {
     fd_status r;
     Py_BEGIN_ALLOW_THREADS
     r = f();
     Py_END_ALLOW_THREADS
-    if (r != FD_OK) throw Other();
+    if (r == FD_ERR_INVALID_ARG || r == FD_ERR_UNSUPPORTED || r == FD_ERR_WORKSPACE_TOO_SMALL) throw Other();
+    if (r != FD_OK) throw Failed{r};
 }
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
@@ -420,11 +431,25 @@ PyObject *diff(PyObject *const *a) {
     return tuple_of({out.object(), l});
 }
 
-template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
+PyObject *raise(fd_status status, const char *what) {
+    PyObject *e = PyObject_CallFunction(g_error, "is", (int)status, what);
+    if (e) {
+        PyErr_SetObject(g_error, e);
+        Py_DECREF(e);
+    }
+    return nullptr;
+}
+
+constexpr char kAppend[] = "fd_append_kv_norm", kEvict[] = "fd_evict_kv", kWeights[] = "fd_decode_paged_weights",
+               kDiff[] = "fd_decode_paged_diff";
+
+template <PyObject *(*F)(PyObject *const *), Py_ssize_t N, const char *NAME>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n == N) {
         try {
             return F(args);
+        } catch (const Failed &f) {
+            return raise(f.status, NAME);
         } catch (...) {
         }
     }
@@ -434,7 +459,11 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 PyObject *init(PyObject *, PyObject *args) {
     unsigned long long f[4];
-    if (!PyArg_ParseTuple(args, "KKKK", &f[0], &f[1], &f[2], &f[3])) return nullptr;
+    PyObject *error;
+    if (!PyArg_ParseTuple(args, "KKKKO", &f[0], &f[1], &f[2], &f[3], &error)) return nullptr;
+    Py_INCREF(error);
+    Py_XDECREF(g_error);
+    g_error = error;
     g_append = reinterpret_cast<decltype(g_append)>(f[0]);
     g_evict = reinterpret_cast<decltype(g_evict)>(f[1]);
     g_weights = reinterpret_cast<decltype(g_weights)>(f[2]);
@@ -442,12 +471,13 @@ PyObject *init(PyObject *, PyObject *args) {
     Py_RETURN_NONE;
 }
 
-#define FD_FAST(name, f, n) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {{"init", init, METH_VARARGS, "addresses of libfd's entry points"},
-                         FD_FAST("append_kv_norm", append, 19),
-                         FD_FAST("evict_kv", evict, 13),
-                         FD_FAST("decode_weights", weights, 16),
-                         FD_FAST("decode_diff", diff, 17),
+#define FD_FAST(name, f, n, what) \
+    {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n, what>)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {{"init", init, METH_VARARGS, "addresses of libfd's entry points and the error class"},
+                         FD_FAST("append_kv_norm", append, 19, kAppend),
+                         FD_FAST("evict_kv", evict, 13, kEvict),
+                         FD_FAST("decode_weights", weights, 16, kWeights),
+                         FD_FAST("decode_diff", diff, 17, kDiff),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fd_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
