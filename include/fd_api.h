@@ -456,6 +456,13 @@ fd_status fd_append_kv_norm(const fd_problem *problem, const fd_norm_append *arg
                             const int32_t *block_table, const int32_t *seq_lens,
                             int32_t *status_dev, void *stream);
 
+/* fd_plan for fd_decode_paged_weights: the same plan, but where the instances of
+ * the kernel that write scores need more of an SM than the plain ones (two CTAs
+ * per SM are planned only where two of them are resident).  Either call takes
+ * either plan.  No shared_kv (FD_ERR_UNSUPPORTED). */
+fd_status fd_plan_weights(const fd_problem *problem, const int32_t *seq_lens_host,
+                          const fd_plan_options *options, fd_plan_t *plan);
+
 /* fd_decode_paged that also keeps count of the attention every cached token
  * received, per KV head:
  *   weights_out[b][kvh][t] = weights[b][kvh][t] + sum exp(s_r(t) - lse_r)

@@ -30,8 +30,10 @@ class PagedDecoder:
     The plan is made once from host lengths and reused while every device
     length stays within plan.capacity_tokens (pass max_seq_len to reserve
     room for growth).  Calls on one decoder must not overlap on the GPU.
-    track_weights=True adds the workspace of decode_weights (four bytes per
-    token of capacity and query head)."""
+    track_weights=True adds what decode_weights needs: weights_plan (plan
+    itself, or one of its own with its own workspace where the score-writing
+    instances of the kernel need more of an SM; it covers the same capacity)
+    and a workspace for the scores (see fd_decode_weights_workspace)."""
 
     def __init__(self, problem, seq_lens_host, device="cuda", track_weights=False, **plan_opts):
         self.problem = problem
@@ -40,9 +42,15 @@ class PagedDecoder:
         nbytes = max(256, int(self.plan.workspace_bytes))
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self.weights_workspace = None
+        self.weights_plan = self.weights_state = self.weights_workspace = None
         if track_weights:
-            self.weights_workspace = torch.empty(_lib.fd_decode_weights_workspace(self.plan), dtype=torch.uint8,
+            room = min(self.plan.capacity_tokens, problem.page_size * problem.max_blocks_per_seq)
+            opts = {**plan_opts, "max_seq_len": max(room, plan_opts.get("max_seq_len", 0))}
+            self.weights_plan, self.weights_state = _lib.fd_plan_weights(problem, seq_lens_host, **opts), self.workspace
+            if self.weights_plan.as_dict() != self.plan.as_dict():
+                self.weights_state = torch.zeros(max(256, int(self.weights_plan.workspace_bytes)), dtype=torch.uint8,
+                                                 device=self.device)
+            self.weights_workspace = torch.empty(_lib.fd_decode_weights_workspace(self.weights_plan), dtype=torch.uint8,
                                                  device=self.device)
 
     @classmethod
@@ -84,12 +92,12 @@ class PagedDecoder:
         if self.weights_workspace is None:
             raise ValueError("decode_weights: make the decoder with track_weights=True")
         if stream is None and (fast := _lib.fast()):
-            done = fast.decode_weights(ctypes.addressof(self.plan), q, k_pages, v_pages, block_table, seq_lens, weights,
-                                       weights_out, k_scale, v_scale, out, lse, want_lse, self.workspace,
+            done = fast.decode_weights(ctypes.addressof(self.weights_plan), q, k_pages, v_pages, block_table, seq_lens,
+                                       weights, weights_out, k_scale, v_scale, out, lse, want_lse, self.weights_state,
                                        self.weights_workspace, self.status)
             if done is not None:
                 return done
-        p, plan = self.problem, self.plan
+        p, plan = self.problem, self.weights_plan
         lead = (p.B,) if plan.q_len <= 1 else (p.B, plan.q_len)
         if weights_out is None:
             weights_out = weights
@@ -98,7 +106,7 @@ class PagedDecoder:
         if lse is None and want_lse:
             lse = _lib.empty_on(lead + (p.Hq,), torch.float32, self.device, stream)
         _lib.fd_decode_paged_weights(plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
-                                     weights, weights_out, self.workspace, self.weights_workspace, self.status, stream)
+                                     weights, weights_out, self.weights_state, self.weights_workspace, self.status, stream)
         return out, lse, weights_out
 
     def host_step(self):
@@ -126,6 +134,8 @@ class PagedDecoder:
         if word:
             self.status.zero_()
             self.workspace.zero_()
+            if self.weights_state is not None:
+                self.weights_state.zero_()
             if self.device.type == "cuda":
                 # the clears are queued on the current stream: finish them
                 # before a call on any other stream can touch the workspace

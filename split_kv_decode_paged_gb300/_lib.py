@@ -4,7 +4,7 @@ Each function keeps the name of the C entry point it calls (fd_plan,
 fd_decode_paged, fd_decode_paged_ex, fd_decode_paged_host, fd_host_copy_in,
 fd_decode_paged_staged, fd_host_copy_out, fd_merge_states,
 fd_merge_two, fd_append_kv, fd_append_kv_rotary, fd_append_kv_norm,
-fd_decode_paged_weights, fd_evict_kv, fd_plan_diff, fd_decode_paged_diff, ...).  Tensors are passed by
+fd_plan_weights, fd_decode_paged_weights, fd_evict_kv, fd_plan_diff, fd_decode_paged_diff, ...).  Tensors are passed by
 data_ptr(); the stream is torch's current CUDA stream unless given.  No
 computation happens here and there is no fallback: if libfd.so is missing or
 fails to load, every call raises.
@@ -142,6 +142,8 @@ def load(path: str = LIB_PATH):
     L.fd_decode_paged_weights.argtypes = [ctypes.POINTER(FdPlan), P, P, P, P, P, P, P, P, P, P, P, I, P, S, P, S, P, P]
     L.fd_evict_kv.restype = I
     L.fd_evict_kv.argtypes = [ctypes.POINTER(FdProblem), P, P, P, P, P, P, P, P, I, I, I, I, P, P, P, P, P]
+    L.fd_plan_weights.restype = I
+    L.fd_plan_weights.argtypes = [ctypes.POINTER(FdProblem), P, ctypes.POINTER(FdPlanOptions), ctypes.POINTER(FdPlan)]
     L.fd_plan_diff.restype = I
     L.fd_plan_diff.argtypes = [ctypes.POINTER(FdProblem), P, ctypes.POINTER(FdPlanOptions), ctypes.POINTER(FdPlan)]
     L.fd_decode_paged_diff.restype = I
@@ -377,6 +379,11 @@ def fd_plan(problem: FdProblem, seq_lens_host, num_splits=0, num_sms=0, fuse_mer
     return _plan("fd_plan", load().fd_plan, problem, seq_lens_host, num_splits, num_sms, fuse_merge, max_seq_len,
                  ctas_per_sm, split_margin_pct, tile_tokens, shared_kv, timeout_us, debug_stall_us, debug_stall_role,
                  q_len)
+
+
+def fd_plan_weights(problem: FdProblem, seq_lens_host, **opts) -> FdPlan:
+    """Plan a decode that counts attention weights (options as fd_plan, no shared_kv)."""
+    return _plan("fd_plan_weights", load().fd_plan_weights, problem, seq_lens_host, **opts)
 
 
 def fd_plan_diff(problem: FdProblem, seq_lens_host, **opts) -> FdPlan:

@@ -10,4 +10,8 @@ cudaError_t launch_decode_diff_bf16(const fd_problem &p, const KernelShape &ks, 
     return launch_decode_kind<KV_BF16, true, kDiff>(p, ks, dp, tmk, tmv, grid, smem, stream);
 }
 
+cudaError_t decode_occupancy_diff_bf16(const fd_problem &p, const KernelShape &ks, size_t smem, bool scr, int *blocks) {
+    return occupancy_kind<KV_BF16, true, kDiff>(p, ks, smem, scr, blocks);
+}
+
 }  // namespace fd

@@ -12,4 +12,9 @@ cudaError_t launch_decode_diff_e4m3(const fd_problem &p, const KernelShape &ks, 
     return launch_decode_kind<KV_E4M3, false, kDiff>(p, ks, dp, tmk, tmv, grid, smem, stream);
 }
 
+cudaError_t decode_occupancy_diff_e4m3(const fd_problem &p, const KernelShape &ks, size_t smem, bool scr, int *blocks) {
+    if (p.q_dtype == FD_BF16) return occupancy_kind<KV_E4M3, true, kDiff>(p, ks, smem, scr, blocks);
+    return occupancy_kind<KV_E4M3, false, kDiff>(p, ks, smem, scr, blocks);
+}
+
 }  // namespace fd

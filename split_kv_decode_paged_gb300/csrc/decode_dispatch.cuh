@@ -43,23 +43,31 @@ cudaError_t launch_decode_d(const KernelShape &ks, const DecodeParams &dp, const
     return cudaErrorInvalidValue;
 }
 
-template <int KV, int D, int NT, bool QBF16>
-cudaError_t occupancy_d(const KernelShape &ks, size_t smem, int *blocks) {
-    if (ks.consumer_warps == 4 && ks.subtiles == 1) return occupancy_t<KV, D, NT, 4, 1, QBF16>(smem, blocks);
+// Of the one-token instance that launch_decode_d would take (scr: its epilogue
+// scratch in a stage).
+template <int KV, int D, int NT, bool QBF16, int MODE>
+cudaError_t occupancy_d(const KernelShape &ks, size_t smem, bool scr, int *blocks) {
+    if (ks.consumer_warps == 4 && ks.subtiles == 1) return occupancy_t<KV, D, NT, 4, 1, QBF16, false, MODE>(smem, blocks);
     if constexpr (KV == KV_E4M3) {
-        if (ks.consumer_warps == 8 && ks.subtiles == 2) return occupancy_t<KV, D, NT, 8, 2, QBF16>(smem, blocks);
-        if (ks.consumer_warps == 4 && ks.subtiles == 2) return occupancy_t<KV, D, NT, 4, 2, QBF16>(smem, blocks);
+        if (ks.consumer_warps == 8 && ks.subtiles == 2) return occupancy_t<KV, D, NT, 8, 2, QBF16, false, MODE>(smem, blocks);
+        if (ks.consumer_warps == 4 && ks.subtiles == 2) {
+            if constexpr (NT == 1)
+                if (scr) return occupancy_t<KV, D, NT, 4, 2, QBF16, true, MODE>(smem, blocks);
+            return occupancy_t<KV, D, NT, 4, 2, QBF16, false, MODE>(smem, blocks);
+        }
     }
-    if (ks.consumer_warps == 8 && ks.subtiles == 1) return occupancy_t<KV, D, NT, 8, 1, QBF16>(smem, blocks);
+    if (ks.consumer_warps == 8 && ks.subtiles == 1) return occupancy_t<KV, D, NT, 8, 1, QBF16, false, MODE>(smem, blocks);
     return cudaErrorInvalidValue;
 }
 
-template <int KV, bool QBF16>
-cudaError_t occupancy_kind(const fd_problem &p, const KernelShape &ks, size_t smem, int *blocks) {
+template <int KV, bool QBF16, int MODE = kPlain>
+cudaError_t occupancy_kind(const fd_problem &p, const KernelShape &ks, size_t smem, bool scr, int *blocks) {
     if (p.D == 128)
-        return ks.nt == 1 ? occupancy_d<KV, 128, 1, QBF16>(ks, smem, blocks) : occupancy_d<KV, 128, 2, QBF16>(ks, smem, blocks);
+        return ks.nt == 1 ? occupancy_d<KV, 128, 1, QBF16, MODE>(ks, smem, scr, blocks)
+                          : occupancy_d<KV, 128, 2, QBF16, MODE>(ks, smem, scr, blocks);
     if (p.D == 64)
-        return ks.nt == 1 ? occupancy_d<KV, 64, 1, QBF16>(ks, smem, blocks) : occupancy_d<KV, 64, 2, QBF16>(ks, smem, blocks);
+        return ks.nt == 1 ? occupancy_d<KV, 64, 1, QBF16, MODE>(ks, smem, scr, blocks)
+                          : occupancy_d<KV, 64, 2, QBF16, MODE>(ks, smem, scr, blocks);
     return cudaErrorInvalidValue;
 }
 

@@ -54,7 +54,6 @@ constexpr int kCoopBlocks = 4;     // 32-row blocks from which every warp builds
 constexpr int kFlagFirst = 1;
 constexpr int kFlagLast = 2;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPlain = 0, kScores = 1, kDiff = 2;  // MODE of a decode instance
 constexpr float kMaxSlack = 8.f;  // log2 headroom of the softmax reference maximum
 
 struct StageMeta {
@@ -1723,9 +1722,9 @@ size_t decode_smem_for(int stages, int B, bool scr_in_stage) {
 
 // Resident CTAs per SM of this instance with `smem` bytes of dynamic shared
 // memory (registers, threads and shared memory all counted).
-template <int KV, int D, int NT, int NC, int SUBT, bool QBF16>
+template <int KV, int D, int NT, int NC, int SUBT, bool QBF16, bool SCR, int MODE>
 cudaError_t occupancy_t(size_t smem, int *blocks) {
-    auto kern = fd_split_kv_decode_kernel<KV, D, NT, NC, SUBT, QBF16, false>;
+    auto kern = fd_split_kv_decode_kernel<KV, D, NT, NC, SUBT, QBF16, false, SCR, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, kern, DecodeShape<KV, D, NT, NC, SUBT>::THREADS, smem);

@@ -19,9 +19,12 @@ using LaunchDecode = cudaError_t(const fd_problem &, const KernelShape &, const 
 LaunchDecode launch_decode_f16, launch_decode_bf16, launch_decode_e4m3;
 LaunchDecode launch_decode_scores_f16, launch_decode_scores_bf16, launch_decode_scores_e4m3;  // scores out (weights.cu)
 LaunchDecode launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3;        // differential attention
-cudaError_t decode_occupancy_f16(const fd_problem &, const KernelShape &, size_t, int *);
-cudaError_t decode_occupancy_bf16(const fd_problem &, const KernelShape &, size_t, int *);
-cudaError_t decode_occupancy_e4m3(const fd_problem &, const KernelShape &, size_t, int *);
+// Resident CTAs per SM of the one-token instance of a shape with that much
+// dynamic shared memory, its epilogue scratch in a stage or not (needs a device).
+using DecodeOccupancy = cudaError_t(const fd_problem &, const KernelShape &, size_t, bool, int *);
+DecodeOccupancy decode_occupancy_f16, decode_occupancy_bf16, decode_occupancy_e4m3;
+DecodeOccupancy decode_occupancy_scores_f16, decode_occupancy_scores_bf16, decode_occupancy_scores_e4m3;
+DecodeOccupancy decode_occupancy_diff_f16, decode_occupancy_diff_bf16, decode_occupancy_diff_e4m3;
 size_t decode_smem_f16(const fd_problem &, const KernelShape &, int, bool);
 size_t decode_smem_bf16(const fd_problem &, const KernelShape &, int, bool);
 size_t decode_smem_e4m3(const fd_problem &, const KernelShape &, int, bool);
@@ -60,25 +63,25 @@ size_t decode_smem_bytes(const fd_problem &p, const KernelShape &ks, int stages,
     }
 }
 
-cudaError_t decode_occupancy(const fd_problem &p, const KernelShape &ks, size_t smem, int *blocks) {
-    switch (p.kv_dtype) {
-    case FD_F16: return decode_occupancy_f16(p, ks, smem, blocks);
-    case FD_BF16: return decode_occupancy_bf16(p, ks, smem, blocks);
-    default: return decode_occupancy_e4m3(p, ks, smem, blocks);
-    }
-}
-
 namespace {
 
-// Launchers of one kind of decode call, by K/V type (f16, bf16, E4M3).
-struct DecodeLaunchers {
+// The instances of one kind of decode call, by K/V type (f16, bf16, E4M3).
+struct DecodeInstances {
     LaunchDecode *f16, *bf16, *e4m3;
+    DecodeOccupancy *occ_f16, *occ_bf16, *occ_e4m3;
     LaunchDecode *of(fd_dtype kv) const { return kv == FD_F16 ? f16 : (kv == FD_BF16 ? bf16 : e4m3); }
+    DecodeOccupancy *occupancy(fd_dtype kv) const {
+        return kv == FD_F16 ? occ_f16 : (kv == FD_BF16 ? occ_bf16 : occ_e4m3);
+    }
 };
-constexpr DecodeLaunchers kPlainDecode = {launch_decode_f16, launch_decode_bf16, launch_decode_e4m3};
-constexpr DecodeLaunchers kScoresDecode = {launch_decode_scores_f16, launch_decode_scores_bf16,
-                                           launch_decode_scores_e4m3};
-constexpr DecodeLaunchers kDiffDecode = {launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3};
+constexpr DecodeInstances kInstances[] = {
+    {launch_decode_f16, launch_decode_bf16, launch_decode_e4m3, decode_occupancy_f16, decode_occupancy_bf16,
+     decode_occupancy_e4m3},
+    {launch_decode_scores_f16, launch_decode_scores_bf16, launch_decode_scores_e4m3, decode_occupancy_scores_f16,
+     decode_occupancy_scores_bf16, decode_occupancy_scores_e4m3},
+    {launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3, decode_occupancy_diff_f16,
+     decode_occupancy_diff_bf16, decode_occupancy_diff_e4m3}};
+static_assert(kPlain == 0 && kScores == 1 && kDiff == 2, "kInstances goes by MODE");
 
 }  // namespace
 
@@ -340,9 +343,9 @@ fd_status fd_status_from_device(int32_t w) {
 
 namespace {
 
-// fd_plan; diff: for differential attention (problem: its padded heads).
+// fd_plan for the kernel instances of a mode (kDiff: problem has the padded heads).
 fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
-                    fd_plan_t *plan, bool diff) {
+                    fd_plan_t *plan, int mode) {
     if (!plan || !seq_lens_host) return FD_ERR_INVALID_ARG;
     fd_status st = validate_problem(problem);
     if (st != FD_OK) return st;
@@ -481,9 +484,9 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
         // Differential attention over E4M3 pages also has 256-token stages,
         // taken as below: two sub-tiles a warp overlap its chains of dependent
         // products and conversions (8 sequences of 8192-32768 tokens, 4 query
-        // tokens, 4 heads a KV head: 186 -> 148 us)
+        // tokens, 4 heads a KV head: 209 -> 184 us)
         if ((opt.tile_tokens != 0 && opt.tile_tokens != 128) || cps_opt != 1) return FD_ERR_UNSUPPORTED;
-        if (!(diff && p.kv_dtype == FD_E4M3)) tile_opt = 128;
+        if (!(mode == kDiff && p.kv_dtype == FD_E4M3)) tile_opt = 128;
     }
     if (tile_opt == 0 && p.kv_dtype == FD_E4M3) {
         const KernelShape k256 = kernel_shape(p, 256, fold, cps_opt);
@@ -492,6 +495,24 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
     }
     Shape sh;
     if (!make_shape(tile_opt, cps_opt, sh)) return FD_ERR_UNSUPPORTED;
+    // Whether two CTAs of a shape's instance are resident on an SM.  Register
+    // budget of two 5-warp CTAs: three warps share one SM sub-partition's 16K
+    // registers, so at most 168 per thread.  Without a device, the instances
+    // compiled within it: one 8-head tile, or two at D = 64 for 16-bit K/V; over
+    // E4M3 no score-writing ones (175 to 254) and of the differential ones
+    // those of one tile at D = 64 (D = 128: 173 to 182).  256 E4M3 sequences of
+    // 1024 tokens, 32/8 heads, D = 128, 64-token pages, two CTAs planned of which
+    // one is resident against one: differential 167 and 116 us, totals 181 and 137.
+    auto two_fit = [&](const Shape &s2) {
+        if (have_dev) {
+            int blocks = 0;
+            const bool ok = kInstances[mode].occupancy(p.kv_dtype)(p, s2.ks, s2.smem, s2.scr_in_stage, &blocks) == cudaSuccess;
+            cudaGetLastError();
+            return ok && blocks >= 2;
+        }
+        if (p.kv_dtype != FD_E4M3) return s2.ks.nt == 1 || p.D == 64;
+        return s2.ks.nt == 1 && mode != kScores && (mode != kDiff || p.D == 64);
+    };
     // Many short work items: two CTAs per SM with 64-token stages, so one
     // CTA streams while the other is between items (epilogue, next claim,
     // page ids).  Taken when the shape is left to the planner, the average
@@ -512,17 +533,7 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
         const int tile2 = p.kv_dtype == FD_E4M3 ? 128 : 64;
         Shape s2;
         if (mean_item < limit && make_shape(tile2, 2, s2)) {
-            // Register budget of two 5-warp CTAs: three warps share one SM
-            // sub-partition's 16K registers, so at most 168 per thread.  Without
-            // a device, the shapes measured within it: one 8-head tile, or two
-            // at D = 64 for 16-bit K/V.
-            bool fits = s2.ks.nt == 1 || (p.D == 64 && p.kv_dtype != FD_E4M3);
-            if (have_dev) {
-                int blocks = 0;
-                fits = decode_occupancy(p, s2.ks, s2.smem, &blocks) == cudaSuccess && blocks >= 2;
-                cudaGetLastError();
-            }
-            if (fits) sh = s2;
+            if (two_fit(s2)) sh = s2;
         }
     }
     // Small grids: fewer work items than SMs leave SMs idle and each CTA's
@@ -573,15 +584,9 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
             const double mean_item = (double)tok * p.Hkv * s2.nhg / (double)s2.items;
             const int boxr2 = std::gcd(p.page_size, s2.ks.tile);
             const long long box_bytes = (long long)boxr2 * p.D * (p.kv_dtype == FD_E4M3 ? 1 : 2);
-            bool fits = s2.ks.nt == 1 || (p.D == 64 && p.kv_dtype != FD_E4M3);
-            if (have_dev) {
-                int blocks = 0;
-                fits = decode_occupancy(p, s2.ks, s2.smem, &blocks) == cudaSuccess && blocks >= 2;
-                cudaGetLastError();
-            }
             const bool medium_ok =
                 !medium || box_bytes <= 2048 || (p.kv_dtype != FD_E4M3 && mean_item >= 768.0);
-            if (fits && medium_ok && (mean_item <= kSmallGridItemTokens || box_bytes <= 2048)) sh = s2;
+            if (medium_ok && (mean_item <= kSmallGridItemTokens || box_bytes <= 2048) && two_fit(s2)) sh = s2;
         }
     }
     const KernelShape ks = sh.ks;
@@ -634,7 +639,17 @@ extern "C" {
 
 fd_status fd_plan(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
                   fd_plan_t *plan) {
-    return plan_impl(problem, seq_lens_host, options, plan, false);
+    return plan_impl(problem, seq_lens_host, options, plan, kPlain);
+}
+
+fd_status fd_plan_weights(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
+                          fd_plan_t *plan) {
+    if (options && options->shared_kv) return FD_ERR_UNSUPPORTED;
+    try {
+        return plan_impl(problem, seq_lens_host, options, plan, kScores);
+    } catch (...) {  // no memory for the lengths
+        return FD_ERR_UNSUPPORTED;
+    }
 }
 
 }  // extern "C"
@@ -643,7 +658,7 @@ namespace {
 
 // What sets a decode call apart from the plain one.
 struct DecodeMode {
-    const DecodeLaunchers *launch = &kPlainDecode;
+    int instances = kPlain;
     int kind = kPlanPlain;     // the plan's kind the call takes
     int score_width = 0;       // elements of q and k a score is formed over; 0 = D
     void (*fill)(DecodeParams &, const void *) = nullptr;  // sets the mode's own parameters
@@ -742,7 +757,7 @@ fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages,
     dp.qn = q_len;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = mode.launch->of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
+    cudaError_t e = kInstances[mode.instances].of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
     if (e != cudaSuccess) return FD_ERR_CUDA;
     if (!plan->fuse_merge && plan->num_splits > 1) {
         MergeParams mp;
@@ -1072,7 +1087,7 @@ fd_status fd_decode_paged_weights(const fd_plan_t *plan, const void *q, const vo
     } wa = {reinterpret_cast<float *>(ww + l.scores), reinterpret_cast<float *>(ww + l.cta_scores), weights_out, weights,
             weights_stride, l.fused ? 1 : 0};
     DecodeMode mode;
-    mode.launch = &kScoresDecode;
+    mode.instances = kScores;
     mode.args = &wa;
     mode.fill = [](DecodeParams &dp, const void *args) {
         const Args &a = *static_cast<const Args *>(args);
@@ -1249,7 +1264,7 @@ fd_status fd_plan_diff(const fd_problem *problem, const int32_t *seq_lens_host, 
     p.Hq *= 2;
     fd_status r = FD_ERR_UNSUPPORTED;
     try {
-        r = plan_impl(&p, seq_lens_host, options, plan, true);
+        r = plan_impl(&p, seq_lens_host, options, plan, kDiff);
     } catch (...) {  // no memory for the lengths
     }
     if (r != FD_OK) return r;
@@ -1280,7 +1295,7 @@ fd_status fd_decode_paged_diff(const fd_plan_t *plan, const void *q, const void 
         float eps, scale;
     } da = {lambda, norm_weight, norm_weight_dtype, eps, out_scale};
     DecodeMode mode;
-    mode.launch = &kDiffDecode;
+    mode.instances = kDiff;
     mode.kind = kPlanDiff;
     mode.score_width = p.D / 2;
     mode.args = &da;

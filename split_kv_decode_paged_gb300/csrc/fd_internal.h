@@ -148,6 +148,10 @@ struct AppendParams {
     int q_is_bf16;
 };
 
+// MODE of a decode kernel instance: the plain decode, the one that also writes
+// its scores (attention-weight totals), differential attention.
+constexpr int kPlain = 0, kScores = 1, kDiff = 2;
+
 // Kernel configuration chosen at plan time.
 struct KernelShape {
     int consumer_warps;  // 4 or 8
@@ -165,9 +169,6 @@ KernelShape kernel_shape(const fd_problem &p, int tile_tokens, int fold, int cta
 // stages (p.B = KV rows: the dispatch tables); scr_in_stage: the epilogue
 // scratch in the item's last stage (16-bit K/V; 0 where a stage cannot hold it).
 size_t decode_smem_bytes(const fd_problem &p, const KernelShape &ks, int stages, bool scr_in_stage);
-// Resident CTAs per SM of the decode kernel of this shape with smem bytes of
-// dynamic shared memory (needs a device).
-cudaError_t decode_occupancy(const fd_problem &p, const KernelShape &ks, size_t smem, int *blocks);
 
 cudaError_t launch_merge(const MergeParams &mp, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams &ap, cudaStream_t stream);
