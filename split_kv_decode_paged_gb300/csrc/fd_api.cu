@@ -1016,6 +1016,7 @@ struct WeightsLayout {
     size_t scores, cta_scores, bytes;
     bool fused;     // rows that are not split are finished by the decode kernel
     bool separate;  // some rows are not
+    bool launchable;  // the kernel that finishes those can be launched for their sizes (else no bytes are given)
 };
 
 bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
@@ -1024,10 +1025,15 @@ bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
         plan->kv_rows * plan->row_fold != p.B || plan->num_splits < 1 || plan->chunk_tokens < 1 || plan->grid_ctas < 1 ||
         plan->head_subgroups < 1)
         return false;
-    // one chunk's scores of a KV head
-    const size_t chunk = (size_t)plan->chunk_tokens * score_stride((p.Hq / p.Hkv) * plan->row_fold) * sizeof(float);
     l->fused = plan->head_subgroups == 1;
     l->separate = plan->num_splits > 1 || !l->fused;
+    l->launchable = true;
+    const long long rows = (long long)(p.Hq / p.Hkv) * plan->row_fold;
+    if (l->separate && !weights_launchable(plan->kv_rows, p.Hkv, (long long)plan->num_splits * plan->chunk_tokens, rows)) {
+        l->launchable = false;
+        return true;
+    }
+    const size_t chunk = (size_t)plan->chunk_tokens * score_stride((int)rows) * sizeof(float);  // a KV head's scores of one
     l->scores = align256((size_t)p.B * p.Hq * sizeof(float));
     l->cta_scores = l->scores + (l->separate ? align256((size_t)plan->kv_rows * p.Hkv * plan->num_splits * chunk) : 0);
     l->bytes = l->cta_scores + (l->fused ? align256((size_t)plan->grid_ctas * chunk) : 0);
@@ -1055,10 +1061,7 @@ fd_status fd_decode_weights_workspace(const fd_plan_t *plan, size_t *bytes) {
     WeightsLayout l;
     if (!weights_layout(plan, &l)) return FD_ERR_INVALID_ARG;
     if (plan->row_fold != std::max(1, plan->q_len)) return FD_ERR_UNSUPPORTED;  // shared_kv
-    if (l.separate && !weights_launchable(plan->kv_rows, plan->problem.Hkv,
-                                          (long long)plan->num_splits * plan->chunk_tokens,
-                                          (long long)(plan->problem.Hq / plan->problem.Hkv) * plan->row_fold))
-        return FD_ERR_UNSUPPORTED;
+    if (!l.launchable) return FD_ERR_UNSUPPORTED;
     *bytes = l.bytes;
     return FD_OK;
 }

@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid
 
 bool weights_launchable(int Bkv, int Hkv, long long cap, long long R) {
     const long long chunks = (cap + kWeightChunk - 1) / kWeightChunk;
-    return chunks <= 0x7fffffffLL / ((long long)Bkv * Hkv) && (R + 3) * 2 * (long long)sizeof(float) <= 48 * 1024;
+    // the rows' lse and ones in the 48 KB of shared memory that every launch may have
+    constexpr long long kMaxRows = 48 * 1024 / (2 * sizeof(float));
+    return chunks <= 0x7fffffffLL / ((long long)Bkv * Hkv) && R <= kMaxRows && score_stride((int)R) <= kMaxRows;
 }
 
 // For sizes that weights_launchable() takes.
