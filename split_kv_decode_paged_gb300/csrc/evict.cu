@@ -346,6 +346,10 @@ struct RowPlace {
     float k_ratio, v_ratio;  // E4M3: scale of the old page / scale of the new one (1: the codes stay)
 };
 
+// What codes are multiplied by between pages of these scales; equal ones (0
+// and infinity too, of which there is no quotient) leave them as they are.
+__device__ __forceinline__ float scale_ratio(float from, float to) { return from == to ? 1.f : __fdiv_rn(from, to); }
+
 // Where row j of (b, h) comes from and goes to.
 template <int RB, bool FP8>
 __device__ __forceinline__ RowPlace place_row(const EvictParams &p, int b, int h, const int32_t *kept, int j) {
@@ -368,8 +372,8 @@ __device__ __forceinline__ RowPlace place_row(const EvictParams &p, int b, int h
     r.dst = dst * RB;
     if constexpr (FP8) {
         const size_t s0 = (size_t)p0 * p.Hkv + h, s1 = (size_t)p1 * p.Hkv + h;
-        r.k_ratio = __fdiv_rn(__ldg(p.k_scale + s0), __ldg(p.k_scale + s1));
-        r.v_ratio = __fdiv_rn(__ldg(p.v_scale + s0), __ldg(p.v_scale + s1));
+        r.k_ratio = scale_ratio(__ldg(p.k_scale + s0), __ldg(p.k_scale + s1));
+        r.v_ratio = scale_ratio(__ldg(p.v_scale + s0), __ldg(p.v_scale + s1));
     }
     return r;
 }
