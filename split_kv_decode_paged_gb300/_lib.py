@@ -254,6 +254,13 @@ class _Args:
             self._fail(name, f"must have a token stride that is a multiple of 8 and at least {heads * D} elements")
         return stride
 
+    def whole(self, name, x):
+        """x as the C int it is passed as (ctypes would cut it to 32 bits)."""
+        n = int(x)
+        if n != x or not -(1 << 31) <= n < 1 << 31:
+            self._fail(name, f"must be a whole number of at most 31 bits, got {x}")
+        return n
+
     def absent(self, name, t, why):
         if t is not None:
             self._fail(name, f"must be None ({why})")
@@ -623,7 +630,7 @@ def fd_append_kv_norm(problem: FdProblem, q, k_new, v_new, q_out, k_pages, v_pag
         if rotary_cos.dim() != 2:
             a._fail("rotary_cos", f"must be 2-D [max_pos, rotary_dim / 2], got shape {tuple(rotary_cos.shape)}")
         a.tensor("rotary_sin", rotary_sin, torch.float32, tuple(rotary_cos.shape))
-        n.max_pos, half = rotary_cos.shape
+        n.max_pos, half = a.whole("the rows of rotary_cos", rotary_cos.shape[0]), rotary_cos.shape[1]
         n.rotary_dim = 2 * half
         n.rotary_cos, n.rotary_sin = rotary_cos.data_ptr(), rotary_sin.data_ptr()
         n.interleaved = 1 if interleaved else 0
@@ -669,11 +676,12 @@ def fd_decode_paged_weights(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale,
     lead = (plan.kv_rows, plan.problem.Hkv)
     if weights_out.dim() != 3 or weights_out.shape[:2] != lead or weights_out.shape[2] < 1:
         a._fail("weights_out", f"must have shape {lead + ('N',)}, got {tuple(weights_out.shape)}")
+    room = a.whole("the last dimension of weights_out", weights_out.shape[2])
     a.tensor("weights", weights, torch.float32, tuple(weights_out.shape), optional=True)
     a.tensor("weights_workspace", weights_workspace, None, None)
     _launch("fd_decode_paged_weights", a.done(), stream, load().fd_decode_paged_weights, ctypes.byref(plan), _ptr(q),
             _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(out),
-            _ptr(lse), _ptr(weights), _ptr(weights_out), weights_out.shape[2], _ptr(workspace), workspace.nbytes,
+            _ptr(lse), _ptr(weights), _ptr(weights_out), room, _ptr(workspace), workspace.nbytes,
             _ptr(weights_workspace), weights_workspace.nbytes, _ptr(status))
 
 
@@ -683,6 +691,7 @@ def fd_evict_kv(problem: FdProblem, k_pages, v_pages, k_scale, v_scale, block_ta
     [B]; kept int32 [B, Hkv, budget]."""
     p = problem
     a = _Args("fd_evict_kv")
+    budget, sinks, recent = a.whole("budget", budget), a.whole("sinks", sinks), a.whole("recent", recent)
     _check_pools(a, p, FD_TO_TORCH[p.kv_dtype], k_pages, v_pages, k_scale, v_scale)
     a.tensor("block_table", block_table, torch.int32, (p.B, p.max_blocks_per_seq))
     a.tensor("dst_table", dst_table, torch.int32, (p.B, p.max_blocks_per_seq), optional=True)
@@ -690,13 +699,14 @@ def fd_evict_kv(problem: FdProblem, k_pages, v_pages, k_scale, v_scale, block_ta
     a.tensor("weights", weights, torch.float32)
     if weights.dim() != 3 or weights.shape[:2] != (p.B, p.Hkv) or weights.shape[2] < 1:
         a._fail("weights", f"must have shape {(p.B, p.Hkv, 'N')}, got {tuple(weights.shape)}")
+    room = a.whole("the last dimension of weights", weights.shape[2])
     a.tensor("weights_out", weights_out, torch.float32, tuple(weights.shape), optional=True)
     a.tensor("new_lens", new_lens, torch.int32, (p.B,))
-    a.tensor("kept", kept, torch.int32, (p.B, p.Hkv, int(budget)))
+    a.tensor("kept", kept, torch.int32, (p.B, p.Hkv, budget))
     a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)
     _launch("fd_evict_kv", a.done(), stream, load().fd_evict_kv, ctypes.byref(p), _ptr(k_pages), _ptr(v_pages),
             _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(weights), _ptr(weights_out),
-            weights.shape[2], int(budget), int(sinks), int(recent), _ptr(dst_table), _ptr(new_lens), _ptr(kept),
+            room, budget, sinks, recent, _ptr(dst_table), _ptr(new_lens), _ptr(kept),
             _ptr(status))
 
 

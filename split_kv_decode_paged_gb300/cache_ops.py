@@ -81,6 +81,8 @@ def evict_kv(k_pages, v_pages, block_table, seq_lens, weights, budget, sinks=0, 
     prob = _lib.make_problem(B, Hkv, Hkv, D, page_size, max_blocks, num_pages, act, k_pages.dtype)
     if int(budget) < 1:
         raise ValueError("evict_kv: budget must be at least 1")
+    if budget > page_size * max_blocks:  # as the call itself would, but before kept is allocated
+        raise _lib.FdError(_lib.FD_ERR_INVALID_ARG, f"evict_kv: budget {budget} of a table for {page_size * max_blocks}")
     new_lens = _lib.empty_on((B,), torch.int32, k_pages.device, stream)
     kept = _lib.empty_on((B, Hkv, int(budget)), torch.int32, k_pages.device, stream)
     _lib.fd_evict_kv(prob, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, weights, weights_out, budget,
