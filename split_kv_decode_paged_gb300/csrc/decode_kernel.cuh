@@ -1601,10 +1601,6 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 p.part_d[row * p.S + m_s] = Ls;
             }
         }
-        if constexpr (MODE == kScores) {
-            // the padding columns of the scores count for nothing
-            if (tid >= G && tid < QROWS) scr_lse[tid] = scr_inv[tid] = 0.f;
-        }
         named_bar_sync(1, NC * 32);
         // The warps' states of the row in slot h combined, outputs d .. d + 3.
         auto combined = [&](int h, int d) {

@@ -22,7 +22,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid_constant__ WeightParams p, int chunks) {
     grid_dependency_wait();
-    extern __shared__ float lse2[];  // the rows' lse in log2 units, then ones (padding: zeros)
+    extern __shared__ float lse2[];  // the rows' lse in log2 units, then ones
     const int stride = score_stride(p.R);
     const long long bh = blockIdx.x / chunks;
     const int chunk = (int)(blockIdx.x % chunks);
@@ -42,7 +42,6 @@ __global__ void __launch_bounds__(kWeightThreads) fd_weights_kernel(const __grid
         lse2[r] = l == -INFINITY ? 0.f : l * kLog2e;
         lse2[stride + r] = 1.f;
     }
-    for (int r = p.R + threadIdx.x; r < stride; r += kWeightThreads) lse2[r] = lse2[stride + r] = 0.f;
     __syncthreads();
     const size_t at = (size_t)bh * p.weights_stride;
     sum_weights<kWeightThreads, kWeightFly>(p.scores + (size_t)bh * p.cap * stride, p.R, lse2, lse2 + stride,

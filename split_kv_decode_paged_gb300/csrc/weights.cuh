@@ -7,16 +7,16 @@
 namespace fd {
 
 // Floats a token's R scores take: whole 16-byte groups from 3 on (the padding
-// columns hold the scores of absent query rows, which count for nothing).
+// columns hold the scores of absent query rows, NaN over an infinite key, and
+// are not read).
 __host__ __device__ constexpr int score_stride(int R) { return R <= 2 ? R : (R + 3) / 4 * 4; }
 
 // out[t] = in[t] + sum over r < R of 2^(sc[t][r] - row_max[r]) * row_inv[r] for
 // t in [t0, t1), by THREADS threads (tid).  FLY tokens a thread are in flight:
 // the loop is a chain of L2 (in: DRAM) round trips otherwise.  A token's scores
 // are score_stride(R) apart, read 16 bytes at a time where that is a multiple
-// of 4 (sc 16-byte aligned; row_max and row_inv hold score_stride(R) entries,
-// 0 for the padding).  A row that sees nothing has all scores -inf and a finite
-// row_max: it adds 0.
+// of 4 (sc 16-byte aligned), the last R % 4 by themselves.  A row that sees
+// nothing has all scores -inf and a finite row_max: it adds 0.
 template <int THREADS, int FLY>
 __device__ __forceinline__ void sum_weights(const float *sc, int R, const float *row_max, const float *row_inv,
                                             const float *in, float *out, int t0, int t1, int tid) {
@@ -29,8 +29,9 @@ __device__ __forceinline__ void sum_weights(const float *sc, int R, const float 
             sum[k] = 0.f;
             old[k] = (in && t < t1) ? in[t] : 0.f;
         }
+        int r = 0;
         if ((stride & 3) == 0) {
-            for (int r = 0; r < stride; r += 4) {
+            for (; r + 4 <= R; r += 4) {
                 float4 s[FLY];
 #pragma unroll
                 for (int k = 0; k < FLY; ++k) {
@@ -46,17 +47,16 @@ __device__ __forceinline__ void sum_weights(const float *sc, int R, const float 
                     sum[k] = fmaf(ex2(s[k].w - row_max[r + 3]), row_inv[r + 3], sum[k]);
                 }
             }
-        } else {
-            for (int r = 0; r < R; ++r) {
-                float s[FLY];
+        }
+        for (; r < R; ++r) {
+            float s[FLY];
 #pragma unroll
-                for (int k = 0; k < FLY; ++k) {
-                    const int t = tb + k * THREADS;
-                    s[k] = t < t1 ? __ldcg(sc + (size_t)t * stride + r) : -INFINITY;
-                }
-#pragma unroll
-                for (int k = 0; k < FLY; ++k) sum[k] = fmaf(ex2(s[k] - row_max[r]), row_inv[r], sum[k]);
+            for (int k = 0; k < FLY; ++k) {
+                const int t = tb + k * THREADS;
+                s[k] = t < t1 ? __ldcg(sc + (size_t)t * stride + r) : -INFINITY;
             }
+#pragma unroll
+            for (int k = 0; k < FLY; ++k) sum[k] = fmaf(ex2(s[k] - row_max[r]), row_inv[r], sum[k]);
         }
 #pragma unroll
         for (int k = 0; k < FLY; ++k) {
