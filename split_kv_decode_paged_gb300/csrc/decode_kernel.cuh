@@ -569,6 +569,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     // the second the [0 | q2] rows of the item's 8 heads, so each tile needs
     // half of the K Q^T products and fragments; with one, rows lie in order.
     constexpr bool kMapTiles = MODE == kDiff && NT == 2;
+    // With one, the halves of K are summed apart (the two accumulator chains
+    // of K Q^T) and each column takes its own map's: the other half's zeros
+    // would turn an infinite key element there into NaN.
+    constexpr bool kMapChains = MODE == kDiff && NT == 1;
     // Column slot (8 n + column of tile n) of query row h of the item, and back.
     auto slot_of = [](int h) { return kMapTiles ? (h & 1) * 8 + (h >> 1) : h; };
     auto row_of = [](int slot) { return kMapTiles ? (slot & 7) * 2 + (slot >> 3) : slot; };
@@ -1171,7 +1175,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
             const uint32_t hstride = (uint32_t)(p.boxr * SUBROW);
             // ---------------------------------------------------------- S = K Q^T
             // Two independent accumulator chains per sub-tile (even / odd
-            // k-steps) halve the dependent MMA latency of the dot products.
+            // k-steps, or the halves of K in turn) halve the dependent MMA
+            // latency of the dot products.
 #pragma unroll
             for (int sub = 0; sub < SUBT; ++sub) {
                 const int r0 = (sub * NC + warp) * kTokensPerWarp;
@@ -1185,7 +1190,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 if (nl[sub] > ll[sub]) {
                     if constexpr (!FP8) {
 #pragma unroll
-                        for (int kk = 0; kk < KT; ++kk) {
+                        for (int step = 0; step < KT; ++step) {
+                            const int kk = kMapChains ? (step & 1) * (KT / 2) + step / 2 : step;
                             const int byte = kk * 32;
                             const int h = byte / SUBROW;
                             const int chunk = (byte % SUBROW) / 16 + (lane >> 4);
@@ -1194,7 +1200,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 if (kMapTiles && (kk < KT / 2) != (n == 0)) continue;  // the other map's half
-                                float *acc = (kk & 1) ? s2[n] : sv[sub][n];
+                                float *acc = (step & 1) ? s2[n] : sv[sub][n];
                                 if constexpr (KV == KV_BF16)
                                     mma_bf16(acc, a0, a1, a2, a3, qf[kk][n][0], qf[kk][n][1]);
                                 else
@@ -1203,7 +1209,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                         }
                     } else {
 #pragma unroll
-                        for (int jg = 0; jg < D / 32; ++jg) {
+                        for (int step = 0; step < D / 32; ++step) {
+                            const int jg = kMapChains ? (step & 1) * (D / 64) + step / 2 : step;
                             const int byte = jg * 32;
                             const int h = byte / SUBROW;
                             const int chunk = (byte % SUBROW) / 16 + (lane >> 4);
@@ -1220,8 +1227,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 if (kMapTiles && (2 * jg < KT / 2) != (n == 0)) continue;  // the other map's half
-                                mma_f16(sv[sub][n], a00, a01, a02, a03, qf[2 * jg][n][0], qf[2 * jg][n][1]);
-                                mma_f16(s2[n], a10, a11, a12, a13, qf[2 * jg + 1][n][0], qf[2 * jg + 1][n][1]);
+                                float *acc0 = kMapChains && (step & 1) ? s2[n] : sv[sub][n];
+                                float *acc1 = kMapChains && !(step & 1) ? sv[sub][n] : s2[n];
+                                mma_f16(acc0, a00, a01, a02, a03, qf[2 * jg][n][0], qf[2 * jg][n][1]);
+                                mma_f16(acc1, a10, a11, a12, a13, qf[2 * jg + 1][n][0], qf[2 * jg + 1][n][1]);
                             }
                         }
                     }
@@ -1257,10 +1266,14 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                             v11 = v11 && ta + 8 < l1;
                         }
                     }
-                    sv[sub][n][0] = v00 ? (sv[sub][n][0] + s2[n][0]) * sc0 : -INFINITY;
-                    sv[sub][n][1] = v01 ? (sv[sub][n][1] + s2[n][1]) * sc1 : -INFINITY;
-                    sv[sub][n][2] = v10 ? (sv[sub][n][2] + s2[n][2]) * sc0 : -INFINITY;
-                    sv[sub][n][3] = v11 ? (sv[sub][n][3] + s2[n][3]) * sc1 : -INFINITY;
+                    // columns 2c and 2c + 1: of maps 1 and 2 with kMapChains
+                    auto whole = [&](int r) {
+                        return kMapChains ? ((r & 1) ? s2[n][r] : sv[sub][n][r]) : sv[sub][n][r] + s2[n][r];
+                    };
+                    sv[sub][n][0] = v00 ? whole(0) * sc0 : -INFINITY;
+                    sv[sub][n][1] = v01 ? whole(1) * sc1 : -INFINITY;
+                    sv[sub][n][2] = v10 ? whole(2) * sc0 : -INFINITY;
+                    sv[sub][n][3] = v11 ? whole(3) * sc1 : -INFINITY;
                 }
             }
 
