@@ -62,9 +62,28 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile every CUDA source for sm_103a and link libfd.so, and the torch
     binding beside it; returns the library's path."""
     newest = max(os.path.getmtime(f) for f in _deps())
-    if not force and not verbose_ptxas and all(os.path.exists(f) and os.path.getmtime(f) >= newest
-                                               for f in (LIB, BINDING)):
-        return LIB
+    fresh = [os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)]
+    if force or verbose_ptxas:
+        fresh = [False, False]
+    if not fresh[0]:
+        _build_lib(verbose_ptxas, binding=not fresh[1])
+    elif not fresh[1]:
+        _try_binding()
+    return LIB
+
+
+def _try_binding() -> None:
+    try:
+        build_binding()
+    except (RuntimeError, OSError) as e:
+        # the calls it serves then go the Python way, which takes longer; an
+        # older binding may have other structures than the library
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        print(f"warning: no native torch binding: {e}", file=sys.stderr)
+
+
+def _build_lib(verbose_ptxas: bool, binding: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     common = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -81,13 +100,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(build_binding)
+        native = ex.submit(_try_binding) if binding else None
         results = list(ex.map(compile_one, SOURCES))
-        try:
-            binding.result()
-        except RuntimeError as e:
-            # the calls it serves then go the Python way, which takes longer
-            print(f"warning: no native torch binding: {e}", file=sys.stderr)
+        if native:
+            native.result()
     if verbose_ptxas:
         for _, log in results:
             sys.stderr.write(log)
@@ -97,7 +113,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
