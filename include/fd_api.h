@@ -91,7 +91,8 @@ typedef struct {
 typedef struct {
     int num_splits;     /* 0 = cost model [P2 进阶突破, P3 §6.3]; >0 forces the
                            number of contiguous chunks of the longest sequence   */
-    int num_sms;        /* 0 = query the device; >0 overrides (planning only)   */
+    int num_sms;        /* 0 = query the device; >0 overrides (planning only),
+                           at most 65536                                    */
     int fuse_merge;     /* 1 = the CTA that finishes the last chunk of a (b, kvh)
                            merges in place (default); 0 = a separate merge kernel */
     int max_seq_len;    /* 0 = max of seq_lens_host; otherwise the capacity the

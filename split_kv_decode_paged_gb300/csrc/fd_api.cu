@@ -96,6 +96,7 @@ constexpr int kMaxStages = 8;
 constexpr int kPlanPlain = 0;
 constexpr int kPlanDiff = 1;  // fd_plan_diff
 constexpr int kMaxHeads = 1 << 20;
+constexpr int kMaxSms = 1 << 16;  // a planner's option; the cost model queues every CTA
 constexpr int kMaxQLen = 64;  // query tokens per sequence (multi-token mode)
 constexpr int kMinStages = 2;
 constexpr int kSmallGridItemTokens = 1024;  // small grids: two CTAs per SM for items up to this long
@@ -351,7 +352,7 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
     if (st != FD_OK) return st;
     fd_plan_options opt = {0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (options) opt = *options;
-    if (opt.num_splits < 0 || opt.num_sms < 0 || opt.max_seq_len < 0 || opt.ctas_per_sm < 0 || opt.ctas_per_sm > 8 ||
+    if (opt.num_splits < 0 || opt.num_sms < 0 || opt.num_sms > kMaxSms || opt.max_seq_len < 0 || opt.ctas_per_sm < 0 || opt.ctas_per_sm > 8 ||
         opt.split_margin_pct < 0 || opt.split_margin_pct > 100 ||
         (opt.tile_tokens != 0 && opt.tile_tokens != 64 && opt.tile_tokens != 128 && opt.tile_tokens != 256) ||
         !hooks_valid(opt.timeout_us, opt.debug_stall_us, opt.debug_stall_role) || opt.q_len < 0 ||
