@@ -130,8 +130,9 @@ typedef struct {
                            tokens' K/V were appended ("Inference Cookbook"
                            §3.2-3.3, causal=True; [P1] §3.1, the append mode).
                            q and out are [B, q_len, Hq, D], lse [B, q_len, Hq];
-                           problem->B counts sequences; not with shared_kv or
-                           the fd_decode_extras indirections               */
+                           problem->B counts sequences; a sequence shorter
+                           than q_len sets FD_DEV_CAPACITY; not with shared_kv
+                           or the fd_decode_extras indirections            */
 } fd_plan_options;
 
 /* A plan: plain data in host memory, owned by the caller, reusable for any

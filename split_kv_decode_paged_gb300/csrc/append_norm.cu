@@ -11,7 +11,8 @@
 // and the norm weights stay in its registers over all the token's heads.
 // Where the rotary part turns in halves its lanes hold four elements of each
 // half instead of eight neighbours: their pairs are their own, no lane exchange,
-// and they need four cosines and sines, not eight (89 -> 70 us below).
+// and they need four cosines and sines, not eight (half of D turning, the tokens
+// below: 89 -> 72 us).
 //
 // One pass: every input is read and every output written once.  Many tokens
 // are bound by instruction issue (63% of the slots) about as much as by DRAM:
@@ -19,7 +20,8 @@
 // 86% of the copy rate.  A loop per kind of row halved the instructions (no
 // selects between q, k and v): 105 -> 75 us.  Few tokens are a chain of
 // latencies (lengths, page id, cosines): 1 token 3.6 us, 256 tokens of 64 + 8 +
-// 8 heads into E4M3 6.2 us.
+// 8 heads into E4M3 6.5 us.  The many tokens into E4M3: 84 us of 55 for their
+// bytes, a division by the page's scale for every element of K and V.
 #include <algorithm>
 
 #include "fd_internal.h"

@@ -19,10 +19,10 @@
 // Measured: 64 sequences x 8 heads of 512-8192 tokens to at most 4096, bf16, D =
 // 128, into other pages 274 us (1.72 GB, 6.3 TB/s, 93% of the copy rate): the
 // copy 249, the selection 25.  Four E4M3 sequences x 8 heads of 60000-65536
-// tokens halved 115 us: the copy 88 (floor 79), the selection 26.  A digit of
+// tokens halved 114 us: the copy 89 (floor 79), the selection 25.  A digit of
 // the radix select costs 1.2 us in one CTA; through the cluster 6 with every
 // CTA reading all the others' bins, 3 with their sums read first.  In
-// place 247 and 347 us: few rows leave few slices to work on at once.
+// place 238 and 331 us: few rows leave few slices to work on at once.
 #include <algorithm>
 
 #include "fd_internal.h"

@@ -4,8 +4,9 @@
 // exp(s_r(t) - lse_r).  The decode kernel that ran before left the scores
 // s_r(t) in log2 units (-inf where row r does not see t), R of them a token,
 // and lse.  A weight cannot be formed before the row's lse is known, and the
-// scores are 4 R bytes a token and KV head where K's row, to be read again
-// otherwise, is up to 256.
+// scores are 4 R bytes a token and KV head, out and back, where K's row, to be
+// read again otherwise, is 64 to 256: less for few rows, more for many (25 rows
+// over E4M3 take 9 times the time of their bytes).
 //
 // Only rows that the decode kernel split (or whose query rows take several
 // work items) come here; it finishes the others itself, from scores that are
