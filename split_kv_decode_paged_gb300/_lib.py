@@ -4,8 +4,8 @@ Each function keeps the name of the C entry point it calls (fd_plan,
 fd_decode_paged, fd_decode_paged_ex, fd_decode_paged_host, fd_host_copy_in,
 fd_decode_paged_staged, fd_host_copy_out, fd_merge_states,
 fd_merge_two, fd_append_kv, fd_append_kv_rotary, fd_append_kv_norm,
-fd_plan_weights, fd_decode_paged_weights, fd_evict_kv, fd_plan_diff, fd_decode_paged_diff, ...).  Tensors are passed by
-data_ptr(); the stream is torch's current CUDA stream unless given.  No
+fd_plan_weights, fd_decode_paged_weights, fd_evict_kv, fd_plan_diff,
+fd_decode_paged_diff, ...).  Tensors are passed by data_ptr(); the stream is torch's current CUDA stream unless given.  No
 computation happens here and there is no fallback: if libfd.so is missing or
 fails to load, every call raises.
 

@@ -68,9 +68,10 @@ def evict_kv(k_pages, v_pages, block_table, seq_lens, weights, budget, sinks=0, 
 
     In place (dst_table None) or into the pages of dst_table, which
     block_table must not name.  E4M3 codes that move to a page with another
-    scale are rescaled, rounded and saturated at 448 each time they do.  weights_out (weights for in place; None: not
-    kept) receives the kept weights.  Returns (new_lens int32 [B], kept int32
-    [B, Hkv, budget], the old indices, -1 past a row's new length)."""
+    scale are rescaled, rounded and saturated at 448 each time they do.
+    weights_out (weights for in place; None: not kept) receives the kept
+    weights.  Returns (new_lens int32 [B], kept int32 [B, Hkv, budget], the old
+    indices, -1 past a row's new length)."""
     if stream is None and (fast := _lib.fast()):
         done = fast.evict_kv(k_pages, v_pages, block_table, seq_lens, weights, budget, sinks, recent, dst_table,
                              weights_out, k_scale, v_scale, status)

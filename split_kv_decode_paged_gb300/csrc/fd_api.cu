@@ -352,8 +352,8 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
     if (st != FD_OK) return st;
     fd_plan_options opt = {0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (options) opt = *options;
-    if (opt.num_splits < 0 || opt.num_sms < 0 || opt.num_sms > kMaxSms || opt.max_seq_len < 0 || opt.ctas_per_sm < 0 || opt.ctas_per_sm > 8 ||
-        opt.split_margin_pct < 0 || opt.split_margin_pct > 100 ||
+    if (opt.num_splits < 0 || opt.num_sms < 0 || opt.num_sms > kMaxSms || opt.max_seq_len < 0 ||
+        opt.ctas_per_sm < 0 || opt.ctas_per_sm > 8 || opt.split_margin_pct < 0 || opt.split_margin_pct > 100 ||
         (opt.tile_tokens != 0 && opt.tile_tokens != 64 && opt.tile_tokens != 128 && opt.tile_tokens != 256) ||
         !hooks_valid(opt.timeout_us, opt.debug_stall_us, opt.debug_stall_role) || opt.q_len < 0 ||
         opt.q_len > kMaxQLen)
@@ -501,7 +501,7 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
     // registers, so at most 168 per thread.  Without a device, the instances
     // compiled within it: one 8-head tile, or two at D = 64 for 16-bit K/V; over
     // E4M3 no score-writing ones (175 to 254) and of the differential ones
-    // those of one tile at D = 64 (D = 128: 173 to 182).  256 E4M3 sequences of
+    // those of one tile at D = 64 (D = 128: 176 to 182).  256 E4M3 sequences of
     // 1024 tokens, 32/8 heads, D = 128, 64-token pages, two CTAs planned of which
     // one is resident against one: differential 167 and 116 us, totals 181 and 137.
     auto two_fit = [&](const Shape &s2) {
@@ -758,7 +758,8 @@ fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages,
     dp.qn = q_len;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = kInstances[mode.instances].of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas, (size_t)plan->smem_bytes, s);
+    cudaError_t e = kInstances[mode.instances].of(p.kv_dtype)(p, ks, dp, tmk, tmv, plan->grid_ctas,
+                                                              (size_t)plan->smem_bytes, s);
     if (e != cudaSuccess) return FD_ERR_CUDA;
     if (!plan->fuse_merge && plan->num_splits > 1) {
         MergeParams mp;
@@ -1015,9 +1016,9 @@ namespace {
 // rows where a KV head's query rows take several items), each CTA's scores.
 struct WeightsLayout {
     size_t scores, cta_scores, bytes;
-    bool fused;     // rows that are not split are finished by the decode kernel
-    bool separate;  // some rows are not
-    bool launchable;  // the kernel that finishes those can be launched for their sizes (else no bytes are given)
+    bool fused;       // rows that are not split are finished by the decode kernel
+    bool separate;    // some rows are not
+    bool launchable;  // nothing speaks against the kernel that finishes those (else no bytes are given)
 };
 
 bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
@@ -1034,7 +1035,8 @@ bool weights_layout(const fd_plan_t *plan, WeightsLayout *l) {
         l->launchable = false;
         return true;
     }
-    const size_t chunk = (size_t)plan->chunk_tokens * score_stride((int)rows) * sizeof(float);  // a KV head's scores of one
+    // one chunk's scores of a KV head
+    const size_t chunk = (size_t)plan->chunk_tokens * score_stride((int)rows) * sizeof(float);
     l->scores = align256((size_t)p.B * p.Hq * sizeof(float));
     l->cta_scores = l->scores + (l->separate ? align256((size_t)plan->kv_rows * p.Hkv * plan->num_splits * chunk) : 0);
     l->bytes = l->cta_scores + (l->fused ? align256((size_t)plan->grid_ctas * chunk) : 0);
