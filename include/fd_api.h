@@ -131,7 +131,9 @@ typedef struct {
                            §3.2-3.3, causal=True; [P1] §3.1, the append mode).
                            q and out are [B, q_len, Hq, D], lse [B, q_len, Hq];
                            problem->B counts sequences; a sequence shorter
-                           than q_len sets FD_DEV_CAPACITY; not with shared_kv
+                           than q_len sets FD_DEV_CAPACITY.  V of the query
+                           tokens has to be finite: a hidden token's weight is
+                           0, and 0 times infinity is NaN.  Not with shared_kv
                            or the fd_decode_extras indirections            */
 } fd_plan_options;
 
