@@ -560,6 +560,149 @@ fd_status fd_decode_paged_diff(const fd_plan_t *plan, const void *q, const void 
                                float *lse, void *workspace, size_t workspace_bytes,
                                int32_t *status_dev, void *stream);
 
+/* Attention of many query rows over KV rows that all of them see.
+ *
+ * Cross attention: B = kv_rows * beams sequences of up to T query tokens each
+ * attend an encoder's states, cached in the paged pools like any others
+ * (written by fd_append_kv_norm or fd_append_kv):
+ *   out[b][t][h] = sum_i softmax_i(q[b][t][h] . K[r][i][h / G] / sqrt(D)) V[r][i][h / G]
+ * over all i in [0, kv_lens[r]) of KV row r = b / beams; nothing is causal.
+ * The beams of a KV row (the hypotheses of a beam search) read its states
+ * together, once. */
+typedef struct {
+    int tokens;         /* T: query tokens per sequence, 0 or 1 = one             */
+    int beams;          /* sequences per KV row, 0 or 1 = one                     */
+    int num_splits;     /* 0 = cost model; > 0 forces the number of chunks of the
+                           longest KV row (at most 64 chunks)                     */
+    int num_sms;        /* 0 = query the device; > 0 overrides (planning only), at
+                           most 65536                                             */
+    int max_kv_len;     /* 0 = max of kv_lens_host; otherwise the capacity the
+                           plan must cover when it is reused as lengths grow      */
+    int timeout_us;     /* limit of every device-side wait, as in fd_plan_options */
+    int debug_stall_us; /* TEST HOOK, 0 = off: the loads of every CTA start this
+                           late, so that the waits for them run out; <= 1 s       */
+} fd_cross_options;
+
+/* A plan: plain data in host memory, reusable for any number of calls while
+ * 0 <= kv_lens[r] <= capacity_tokens on the device. */
+typedef struct {
+    fd_problem problem;   /* problem.B: KV rows (cross), sequences (prefix)       */
+    int kv_rows;          /* rows of block_table and kv_lens                      */
+    int seqs;             /* sequences: q is [seqs, tokens, Hq, D]                */
+    int tokens;
+    int beams;            /* sequences per KV row; 0: groups (fd_plan_prefix)     */
+    int num_splits;       /* partial-state slots per query row                    */
+    int chunk_tokens;     /* tokens per split                                     */
+    int capacity_tokens;
+    int tile_rows;        /* query rows of one work item                          */
+    int grid_ctas;
+    int num_sms;
+    int smem_bytes;       /* dynamic shared memory per CTA                        */
+    int timeout_us;
+    int debug_stall_us;
+    size_t workspace_bytes;
+    size_t ws_partial_o;  /* byte offsets inside the workspace                    */
+    size_t ws_partial_md;
+    size_t ws_counters;
+    int reserved[4];      /* 0                                                    */
+} fd_cross_plan_t;
+
+/* Plan a cross-attention call.
+ *   problem       B = KV rows (at most 8192), Hq, Hkv, D, page_size,
+ *                 max_blocks_per_seq, num_pages and the types, as in fd_plan;
+ *                 out_dtype has to be q_dtype
+ *   kv_lens_host  HOST int32 [B]: the lengths the work is split for
+ *   options       may be NULL (one token, one beam)
+ * B * beams * T is at most 2^22, and times Hq at most 2^28. */
+fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
+                        const fd_cross_options *options, fd_cross_plan_t *plan);
+
+/*   q            device [B * beams, T, Hq, D] in q_dtype, 16-byte aligned; heads
+ *                are contiguous, tokens (b, t) -> b*T + t lie q_stride elements
+ *                apart (a multiple of 8, at least Hq * D), e.g. a slice of a fused
+ *                projection
+ *   q_lens       device int32 [B * beams]: the sequence's query tokens in this
+ *                call, 0..T (a padded batch), or NULL: T each.  Tokens beyond are
+ *                not read, their out and lse not written; a count outside [0, T]
+ *                sets FD_DEV_CAPACITY and the sequence is skipped
+ *   block_table  device int32 [B, max_blocks_per_seq]
+ *   kv_lens      device int32 [B].  0 gives out = 0 and lse = -inf (and so does a
+ *                row of scores that are all -inf); a length below 0 or beyond the
+ *                plan's capacity sets FD_DEV_CAPACITY and is cut to it
+ *   out          device [B * beams, T, Hq, D] in q_dtype, 16-byte aligned, dense
+ *   lse          device fp32 [B * beams, T, Hq] (natural log), or NULL
+ *   workspace    device, 256-byte aligned, >= plan->workspace_bytes, zero-filled
+ *                before its first use and after a call that reported an FD_DEV_*
+ *                error; one per call in flight
+ *   the pools, their scales, status_dev and stream as in fd_decode_paged.
+ * K and V behind a row's length are not used, whatever they hold.  The weights
+ * enter P.V rounded to the type of the product: q_dtype, and for an E4M3 pool
+ * pairs of bf16 (f16 q) or bf16. */
+fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q_stride,
+                         const int32_t *q_lens, const void *k_pages, const void *v_pages,
+                         const float *k_scale, const float *v_scale, const int32_t *block_table,
+                         const int32_t *kv_lens, void *out, float *lse, void *workspace,
+                         size_t workspace_bytes, int32_t *status_dev, void *stream);
+
+/* Decode of sequences that share long prefixes: sequence b attends its group's
+ * prefix, all of it, and then its own tokens as in fd_decode_paged (causal among
+ * q_len query tokens).  Every prefix is attended once for all of its group's
+ * query rows, 256 rows to a pass over its keys and values. */
+typedef struct {
+    fd_plan_t own;           /* the pass over each sequence's own tokens          */
+    fd_cross_plan_t shared;  /* the pass over the prefixes, and the merge         */
+    int prefixes;
+    size_t ws_own_out;       /* byte offsets inside the workspace                 */
+    size_t ws_own_lse;
+    size_t ws_own;
+    size_t ws_shared;
+    size_t workspace_bytes;
+} fd_prefix_plan_t;
+
+/* Plan it.
+ *   problem            B sequences; max_blocks_per_seq of their own tokens'
+ *                      block table; out_dtype q_dtype
+ *   seq_lens_host      HOST int32 [B]: the sequences' own lengths
+ *   prefixes           P >= 1, at most 8192
+ *   prefix_max_blocks  columns of the prefixes' block table
+ *   prefix_lens_host   HOST int32 [P]
+ *   offsets_host       HOST int32 [P + 1]: 0 = offsets[0] <= ... <= offsets[P] <= B
+ *                      (see fd_decode_paged_prefix)
+ *   options            of the own pass, may be NULL: q_len, num_sms, max_seq_len,
+ *                      timeout_us, debug_stall_us and debug_stall_role apply (no
+ *                      shared_kv); num_sms and timeout_us to both passes
+ *   prefix_options     may be NULL: num_splits, max_kv_len and debug_stall_us of
+ *                      the pass over the prefixes (its other fields are not used) */
+fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host, int prefixes,
+                         int prefix_max_blocks, const int32_t *prefix_lens_host,
+                         const int32_t *offsets_host, const fd_plan_options *options,
+                         const fd_cross_options *prefix_options, fd_prefix_plan_t *plan);
+
+/*   q             device [B, (q_len,) Hq, D], as in fd_decode_paged
+ *   prefix_table  device int32 [P, prefix_max_blocks]; prefixes need not end at a
+ *                 page's end
+ *   prefix_lens   device int32 [P]; 0 is a group without a prefix
+ *   members       device int32 [B]: every sequence once, ordered by group: prefix
+ *                 p's are members[offsets[p] .. offsets[p + 1]), and those from
+ *                 offsets[P] on have no prefix.  An entry outside [0, B) sets
+ *                 FD_DEV_BAD_PAGE and is skipped; the outputs of a sequence that
+ *                 is missing are not written
+ *   offsets       device int32 [P + 1].  Another grouping than the planned one is
+ *                 served too; offsets that fall or leave [0, B] set
+ *                 FD_DEV_BAD_PAGE and are cut to the nearest that do not
+ *   block_table, seq_lens  the sequences' own tokens, as in fd_decode_paged
+ *   out, lse      as in fd_decode_paged (out in q_dtype)
+ *   workspace     device, 256-byte aligned, >= plan->workspace_bytes, zero-filled
+ *                 before its first use and after an FD_DEV_* error
+ *   other arguments as in fd_decode_paged.  One call in flight per workspace. */
+fd_status fd_decode_paged_prefix(const fd_prefix_plan_t *plan, const void *q, const void *k_pages,
+                                 const void *v_pages, const float *k_scale, const float *v_scale,
+                                 const int32_t *prefix_table, const int32_t *prefix_lens,
+                                 const int32_t *members, const int32_t *offsets,
+                                 const int32_t *block_table, const int32_t *seq_lens, void *out,
+                                 float *lse, void *workspace, size_t workspace_bytes,
+                                 int32_t *status_dev, void *stream);
+
 /* Map a device status word to a status code (FD_OK when zero). */
 fd_status fd_status_from_device(int32_t status_word);
 

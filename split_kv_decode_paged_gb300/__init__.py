@@ -18,10 +18,11 @@ from ._lib import (FD_BF16, FD_E4M3, FD_F16, FD_F32, FdError, fd_append_kv, fd_d
                    fd_plan, fd_status_from_device, fd_status_string, make_problem)
 from .cache_ops import append_kv_norm, evict_kv
 from .diff import DiffDecoder
+from .shared import CrossDecoder, PrefixDecoder
 
 __all__ = ["PagedDecoder", "HostStep", "HostPipeline", "fd_plan", "fd_decode_paged", "fd_merge_states", "fd_append_kv", "fd_status_string",
            "fd_status_from_device", "make_problem", "FdError", "append_kv", "merge_states", "append_kv_norm", "evict_kv",
-           "DiffDecoder"]
+           "DiffDecoder", "CrossDecoder", "PrefixDecoder"]
 
 
 class PagedDecoder:

@@ -5,7 +5,8 @@ fd_decode_paged, fd_decode_paged_ex, fd_decode_paged_host, fd_host_copy_in,
 fd_decode_paged_staged, fd_host_copy_out, fd_merge_states,
 fd_merge_two, fd_append_kv, fd_append_kv_rotary, fd_append_kv_norm,
 fd_plan_weights, fd_decode_paged_weights, fd_evict_kv, fd_plan_diff,
-fd_decode_paged_diff, ...).  Tensors are passed by data_ptr(); the stream is torch's current CUDA stream unless given.  No
+fd_decode_paged_diff, fd_plan_cross, fd_cross_paged, fd_plan_prefix,
+fd_decode_paged_prefix, ...).  Tensors are passed by data_ptr(); the stream is torch's current CUDA stream unless given.  No
 computation happens here and there is no fallback: if libfd.so is missing or
 fails to load, every call raises.
 
@@ -91,6 +92,25 @@ class FdNormAppend(ctypes.Structure):
                 ("positions", ctypes.c_void_p), ("new_lens", ctypes.c_void_p)]
 
 
+class FdCrossOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("tokens", "beams", "num_splits", "num_sms", "max_kv_len", "timeout_us",
+                                            "debug_stall_us")]
+
+
+class FdCrossPlan(ctypes.Structure):
+    _fields_ = ([("problem", FdProblem)] +
+                [(n, ctypes.c_int) for n in ("kv_rows", "seqs", "tokens", "beams", "num_splits", "chunk_tokens",
+                                             "capacity_tokens", "tile_rows", "grid_ctas", "num_sms", "smem_bytes",
+                                             "timeout_us", "debug_stall_us")] +
+                [(n, ctypes.c_size_t) for n in ("workspace_bytes", "ws_partial_o", "ws_partial_md", "ws_counters")] +
+                [("reserved", ctypes.c_int * 4)])
+
+
+class FdPrefixPlan(ctypes.Structure):
+    _fields_ = ([("own", FdPlan), ("shared", FdCrossPlan), ("prefixes", ctypes.c_int)] +
+                [(n, ctypes.c_size_t) for n in ("ws_own_out", "ws_own_lse", "ws_own", "ws_shared", "workspace_bytes")])
+
+
 class FdHostIoLayout(ctypes.Structure):
     _fields_ = [("q_offset", ctypes.c_size_t), ("block_table_offset", ctypes.c_size_t),
                 ("seq_lens_offset", ctypes.c_size_t), ("in_bytes", ctypes.c_size_t),
@@ -149,6 +169,15 @@ def load(path: str = LIB_PATH):
     L.fd_decode_paged_diff.restype = I
     L.fd_decode_paged_diff.argtypes = [ctypes.POINTER(FdPlan), P, P, P, P, P, P, P, P, P, I, ctypes.c_float,
                                        ctypes.c_float, P, P, P, S, P, P]
+    L.fd_plan_cross.restype = I
+    L.fd_plan_cross.argtypes = [ctypes.POINTER(FdProblem), P, ctypes.POINTER(FdCrossOptions), ctypes.POINTER(FdCrossPlan)]
+    L.fd_cross_paged.restype = I
+    L.fd_cross_paged.argtypes = [ctypes.POINTER(FdCrossPlan), P, ctypes.c_longlong, P, P, P, P, P, P, P, P, P, P, S, P, P]
+    L.fd_plan_prefix.restype = I
+    L.fd_plan_prefix.argtypes = [ctypes.POINTER(FdProblem), P, I, I, P, P, ctypes.POINTER(FdPlanOptions),
+                                 ctypes.POINTER(FdCrossOptions), ctypes.POINTER(FdPrefixPlan)]
+    L.fd_decode_paged_prefix.restype = I
+    L.fd_decode_paged_prefix.argtypes = [ctypes.POINTER(FdPrefixPlan), P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P, P]
     L.fd_status_string.restype = ctypes.c_char_p
     L.fd_status_string.argtypes = [I]
     L.fd_status_from_device.restype = I
@@ -737,3 +766,106 @@ def fd_decode_paged_diff(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale, bl
             _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(lam),
             _ptr(norm_weight), wt, eps, out_scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.nbytes,
             _ptr(status))
+
+
+def _host_i32(entry, name, x, n):
+    """Host int32 entries x (a tensor or sequence of n whole numbers)."""
+    t = torch.as_tensor(x)
+    if t.dim() != 1 or t.numel() != n or t.dtype.is_floating_point or t.dtype == torch.bool or t.dtype.is_complex:
+        raise ValueError(f"{entry}: {name} must be {n} whole numbers")
+    t = t.cpu().to(torch.int64)
+    if n and (int(t.min()) < -(1 << 31) or int(t.max()) >= 1 << 31):
+        raise ValueError(f"{entry}: {name} must be whole numbers of at most 31 bits")
+    return t.to(torch.int32).contiguous()
+
+
+def fd_plan_cross(problem: FdProblem, kv_lens_host, tokens=1, beams=1, num_splits=0, num_sms=0, max_kv_len=0,
+                  timeout_us=0, debug_stall_us=0) -> FdCrossPlan:
+    """Plan cross attention of problem.B KV rows times beams sequences of
+    tokens query tokens each; kv_lens_host are the rows' lengths."""
+    a = _Args("fd_plan_cross")
+    lens = _host_i32("fd_plan_cross", "kv_lens_host", kv_lens_host, problem.B)
+    opts = FdCrossOptions(*(a.whole(n, v) for n, v in (
+        ("tokens", tokens), ("beams", beams), ("num_splits", num_splits), ("num_sms", num_sms),
+        ("max_kv_len", max_kv_len), ("timeout_us", timeout_us), ("debug_stall_us", debug_stall_us))))
+    plan = FdCrossPlan()
+    rc = load().fd_plan_cross(ctypes.byref(problem), lens.data_ptr(), ctypes.byref(opts), ctypes.byref(plan))
+    if rc != FD_OK:
+        raise FdError(rc, "fd_plan_cross")
+    return plan
+
+
+def fd_cross_paged(plan: FdCrossPlan, q, k_pages, v_pages, k_scale, v_scale, block_table, kv_lens, out, lse, workspace,
+                   q_lens=None, status=None, stream=None):
+    """q [seqs, T, Hq, D] or [seqs, Hq, D] (T = 1), tokens at one stride (see
+    _Args.rows); out and lse the same without gaps."""
+    p = plan.problem
+    a = _Args("fd_cross_paged")
+    act = FD_TO_TORCH[p.q_dtype]
+    lead = (plan.seqs, plan.tokens)
+    if plan.tokens == 1 and isinstance(q, torch.Tensor) and q.dim() == 3:
+        lead = (plan.seqs,)
+    stride = a.rows("q", q, act, lead, p.Hq, p.D)
+    a.tensor("q_lens", q_lens, torch.int32, (plan.seqs,), optional=True)
+    _check_pools(a, p, FD_TO_TORCH[p.kv_dtype], k_pages, v_pages, k_scale, v_scale)
+    a.tensor("block_table", block_table, torch.int32, (plan.kv_rows, p.max_blocks_per_seq))
+    a.tensor("kv_lens", kv_lens, torch.int32, (plan.kv_rows,))
+    a.tensor("out", out, act, lead + (p.Hq, p.D))
+    a.tensor("lse", lse, torch.float32, lead + (p.Hq,), optional=True)
+    a.tensor("workspace", workspace, None, None, min_bytes=int(plan.workspace_bytes))
+    a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)
+    _launch("fd_cross_paged", a.done(), stream, load().fd_cross_paged, ctypes.byref(plan), _ptr(q), stride, _ptr(q_lens),
+            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(kv_lens), _ptr(out),
+            _ptr(lse), _ptr(workspace), workspace.nbytes, _ptr(status))
+
+
+def fd_plan_prefix(problem: FdProblem, seq_lens_host, prefix_max_blocks, prefix_lens_host, offsets_host, num_splits=0,
+                   max_prefix_len=0, prefix_stall_us=0, **own) -> FdPrefixPlan:
+    """Plan decode behind shared prefixes: problem and seq_lens_host as
+    fd_plan for the sequences' own tokens, own its options (q_len, num_sms,
+    max_seq_len, timeout_us, ...); prefix_lens_host [P], offsets_host [P + 1]
+    as fd_decode_paged_prefix's; num_splits and max_prefix_len (capacity) of
+    the prefixes."""
+    a = _Args("fd_plan_prefix")
+    names = [n for n, _ in FdPlanOptions._fields_]
+    if set(own) - set(names):
+        raise TypeError(f"fd_plan_prefix: unknown options {sorted(set(own) - set(names))}")
+    opts = FdPlanOptions(**{n: a.whole(n, own.get(n, 1 if n == "fuse_merge" else 0)) for n in names})
+    P = len(prefix_lens_host)
+    lens = _host_i32("fd_plan_prefix", "seq_lens_host", seq_lens_host, problem.B)
+    plens = _host_i32("fd_plan_prefix", "prefix_lens_host", prefix_lens_host, P)
+    offs = _host_i32("fd_plan_prefix", "offsets_host", offsets_host, P + 1)
+    po = FdCrossOptions(num_splits=a.whole("num_splits", num_splits), max_kv_len=a.whole("max_prefix_len", max_prefix_len),
+                        debug_stall_us=a.whole("prefix_stall_us", prefix_stall_us))
+    plan = FdPrefixPlan()
+    rc = load().fd_plan_prefix(ctypes.byref(problem), lens.data_ptr(), P, a.whole("prefix_max_blocks", prefix_max_blocks),
+                               plens.data_ptr(), offs.data_ptr(), ctypes.byref(opts), ctypes.byref(po), ctypes.byref(plan))
+    if rc != FD_OK:
+        raise FdError(rc, "fd_plan_prefix")
+    return plan
+
+
+def fd_decode_paged_prefix(plan: FdPrefixPlan, q, k_pages, v_pages, k_scale, v_scale, prefix_table, prefix_lens, members,
+                           offsets, block_table, seq_lens, out, lse, workspace, status=None, stream=None):
+    """q, out [B, (q_len,) Hq, D], lse fp32 [B, (q_len,) Hq] or None; members
+    int32 [B], offsets int32 [P + 1]."""
+    sh = plan.shared
+    p = sh.problem  # its block table is the prefixes'
+    a = _Args("fd_decode_paged_prefix")
+    act, own = FD_TO_TORCH[p.q_dtype], plan.own
+    a.tensor("q", q, act, _rows_shape(own, q, (p.Hq, p.D)))
+    _check_pools(a, p, FD_TO_TORCH[p.kv_dtype], k_pages, v_pages, k_scale, v_scale)
+    a.tensor("prefix_table", prefix_table, torch.int32, (plan.prefixes, p.max_blocks_per_seq))
+    a.tensor("prefix_lens", prefix_lens, torch.int32, (plan.prefixes,))
+    a.tensor("members", members, torch.int32, (sh.seqs,))
+    a.tensor("offsets", offsets, torch.int32, (plan.prefixes + 1,))
+    a.tensor("block_table", block_table, torch.int32, (sh.seqs, own.problem.max_blocks_per_seq))
+    a.tensor("seq_lens", seq_lens, torch.int32, (sh.seqs,))
+    a.tensor("out", out, act, _rows_shape(own, out, (p.Hq, p.D)))
+    a.tensor("lse", lse, torch.float32, _rows_shape(own, lse, (p.Hq,)), optional=True)
+    a.tensor("workspace", workspace, None, None, min_bytes=int(plan.workspace_bytes))
+    a.tensor("status", status, torch.int32, None, min_bytes=4, optional=True)
+    _launch("fd_decode_paged_prefix", a.done(), stream, load().fd_decode_paged_prefix, ctypes.byref(plan), _ptr(q),
+            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table), _ptr(prefix_lens),
+            _ptr(members), _ptr(offsets), _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.nbytes, _ptr(status))

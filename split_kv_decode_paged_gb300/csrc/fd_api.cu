@@ -142,7 +142,9 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-fd_status validate_problem(const fd_problem *p) {
+}  // namespace
+
+fd_status fd::validate_problem(const fd_problem *p) {
     if (!p) return FD_ERR_INVALID_ARG;
     if (p->B < 1 || p->Hq < 1 || p->Hkv < 1 || p->D < 1 || p->page_size < 1 || p->max_blocks_per_seq < 1 ||
         p->num_pages < 1)
@@ -162,14 +164,7 @@ fd_status validate_problem(const fd_problem *p) {
     return FD_OK;
 }
 
-struct DeviceInfo {
-    int sms = 0;
-    int smem_optin = 0;     // per CTA (opt-in maximum)
-    int smem_per_sm = 0;    // per SM
-    int smem_reserved = 0;  // set aside per resident CTA
-};
-
-fd_status device_info(DeviceInfo &di) {
+fd_status fd::device_info(DeviceInfo &di) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FD_ERR_CUDA;
     static std::mutex mu;
@@ -188,6 +183,8 @@ fd_status device_info(DeviceInfo &di) {
     di = cache[dev];
     return FD_OK;
 }
+
+namespace {
 
 int round_up(long long x, int a) { return (int)(((x + a - 1) / a) * a); }
 
@@ -284,11 +281,13 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+}  // namespace
+
 // K or V pool viewed as 5-D (d within a swizzle span, slot, span index,
 // kvh, page): one box = `boxr` token rows x all of D for one KV head, landing
 // in shared memory as [span][row][span bytes] so each span is one swizzled
 // region (a span is 128 bytes, or the whole row when the row is shorter).
-bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr) {
+bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int e = elem_bytes(p.kv_dtype);
@@ -312,8 +311,6 @@ bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, in
                     l2p, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 extern "C" {
 

@@ -118,6 +118,34 @@ struct EvictParams {
     int weights_stride, budget, sinks, recent;
 };
 
+// Query rows over KV rows that all of them see (rows.cu).  Segment s: the query
+// tokens of the sequences i in [off(s), off(s + 1)) of the member order, which
+// read KV row s; the last segment of a grouped call reads none.
+struct RowsParams {
+    const void *q;             // [seqs, T, Hq, D]
+    long long q_stride;        // elements between tokens
+    const int32_t *q_lens;     // [seqs] or null (T each)
+    const int32_t *members;    // [seqs] sequences in group order, or null (in order)
+    const int32_t *offsets;    // [kv_rows + 1], or null (beams sequences a KV row)
+    const int32_t *block_table, *kv_lens;  // [kv_rows, max_blocks], [kv_rows]
+    const float *k_scale, *v_scale;        // [num_pages, Hkv] or null
+    const void *k_pages, *v_pages;
+    void *out;                 // [seqs, T, Hq, D]
+    float *lse;                // [seqs, T, Hq] or null
+    const float *own_out;      // [seqs, T, Hq, D] and [seqs, T, Hq]: a state over other
+    const float *own_lse;      // tokens that joins every row's, or null
+    float *part_o;             // [seqs * T * Hq, S, D]: unnormalised; m in log2 units
+    float *part_m, *part_d;    // [seqs * T * Hq, S]
+    int *counters;
+    int *status;
+    int kv_rows, seqs, T, beams, Hq, Hkv, G;
+    int page_size, max_blocks, num_pages;
+    int S, chunk, cap;
+    int q_bf16, kv_kind, D;
+    float scale_log2;          // log2(e) / sqrt(D)
+    uint64_t timeout_ns, stall_ns;
+};
+
 struct MergeParams {
     const float *part_o, *part_m, *part_d;
     void *out;
@@ -177,6 +205,20 @@ bool weights_launchable(int Bkv, int Hkv, long long cap, long long R);
 cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream);
 cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_rows(const RowsParams &p, cudaStream_t stream);
+
+// Checks and encodings that the entry points share (fd_api.cu).
+struct DeviceInfo {
+    int sms = 0;
+    int smem_optin = 0;     // per CTA (opt-in maximum)
+    int smem_per_sm = 0;    // per SM
+    int smem_reserved = 0;  // set aside per resident CTA
+};
+fd_status device_info(DeviceInfo &di);
+fd_status validate_problem(const fd_problem *p);
+// Tensor map of a K or V pool with boxes of boxr token rows of one KV head.
+bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr);
+
 cudaError_t launch_merge_two(const float *oa, const float *la, const float *ob, const float *lb, int rows, int D,
                              int out_dtype, void *out, float *lse, cudaStream_t stream);
 

@@ -1,0 +1,272 @@
+// rows_api.cu -- C entry points of cross attention and of decode behind shared
+// prefixes (declared in include/fd_api.h): checks, plans and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "fd_internal.h"
+
+using namespace fd;
+
+namespace {
+
+constexpr int kMaxBeams = 1 << 16;
+constexpr long long kMaxTokens = 1LL << 22;  // query tokens of a call
+constexpr long long kMaxRows = 1LL << 28;    // query tokens * heads
+constexpr int kMaxRowSms = 1 << 16;
+constexpr uint64_t kRowsTimeoutNs = 2000000000ull;  // 2 s limit on any device-side wait
+constexpr int kPlanCross = 2, kPlanPrefix = 3;      // fd_cross_plan_t::reserved[0]
+
+bool on(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Shared by both planners.  seqs_of(s): sequences of segment s (segment kv_rows:
+// those without a prefix).
+template <typename SeqsOf>
+fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int max_blocks, const int32_t *kv_lens,
+                    const fd_cross_options &opt, SeqsOf seqs_of, fd_cross_plan_t *plan) {
+    if (opt.num_splits < 0 || opt.num_sms < 0 || opt.num_sms > kMaxRowSms || opt.max_kv_len < 0 || opt.timeout_us < 0 ||
+        opt.debug_stall_us < 0 || opt.debug_stall_us > 1000000)
+        return FD_ERR_INVALID_ARG;
+    if (p.out_dtype != p.q_dtype) return FD_ERR_UNSUPPORTED;
+    if (kv_rows > kMaxBatch || (long long)seqs * tokens > kMaxTokens || (long long)seqs * tokens * p.Hq > kMaxRows)
+        return FD_ERR_UNSUPPORTED;
+    long long longest = std::max(1, opt.max_kv_len);
+    for (int s = 0; s < kv_rows; ++s) {
+        if (kv_lens[s] < 0) return FD_ERR_INVALID_ARG;
+        longest = std::max<long long>(longest, kv_lens[s]);
+    }
+    if (longest > (long long)p.page_size * max_blocks) return FD_ERR_INVALID_ARG;
+    int sms = opt.num_sms;
+    if (sms == 0) {
+        DeviceInfo di;
+        fd_status st = FD_ERR_CUDA;
+        try {
+            st = device_info(di);
+        } catch (...) {
+        }
+        if (st != FD_OK) return st;
+        sms = di.sms;
+    }
+    (void)seqs_of;
+    std::memset(plan, 0, sizeof(*plan));
+    plan->problem = p;
+    plan->problem.max_blocks_per_seq = max_blocks;
+    plan->kv_rows = kv_rows;
+    plan->seqs = seqs;
+    plan->tokens = tokens;
+    plan->num_splits = 1;
+    plan->chunk_tokens = (int)longest;
+    plan->capacity_tokens = (int)longest;
+    plan->tile_rows = 1;
+    plan->grid_ctas = 1;
+    plan->num_sms = sms;
+    plan->timeout_us = opt.timeout_us;
+    plan->debug_stall_us = opt.debug_stall_us;
+    plan->workspace_bytes = 256;
+    return FD_OK;
+}
+
+// The launch of a planned pass; pointers were checked.
+fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pages, const void *v_pages,
+                   uint8_t *workspace, void *stream) {
+    const fd_problem &p = plan.problem;
+    rp.k_pages = k_pages;
+    rp.v_pages = v_pages;
+    rp.kv_rows = plan.kv_rows;
+    rp.seqs = plan.seqs;
+    rp.T = plan.tokens;
+    rp.beams = plan.beams;
+    rp.Hq = p.Hq;
+    rp.Hkv = p.Hkv;
+    rp.G = p.Hq / p.Hkv;
+    rp.D = p.D;
+    rp.page_size = p.page_size;
+    rp.max_blocks = p.max_blocks_per_seq;
+    rp.num_pages = p.num_pages;
+    rp.S = plan.num_splits;
+    rp.chunk = plan.chunk_tokens;
+    rp.cap = plan.capacity_tokens;
+    rp.q_bf16 = p.q_dtype == FD_BF16;
+    rp.kv_kind = p.kv_dtype == FD_F16 ? KV_F16 : (p.kv_dtype == FD_BF16 ? KV_BF16 : KV_E4M3);
+    rp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.D));
+    rp.timeout_ns = plan.timeout_us > 0 ? (uint64_t)plan.timeout_us * 1000ull : kRowsTimeoutNs;
+    rp.stall_ns = (uint64_t)plan.debug_stall_us * 1000ull;
+    (void)workspace;
+    return launch_rows(rp, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+// What a plan handed in must satisfy for its launch to stay in bounds.
+bool plan_ok(const fd_cross_plan_t &plan, int kind) {
+    const fd_problem &p = plan.problem;
+    fd_problem one = p;  // problem.B counts sequences or KV rows: both are bounded below
+    one.B = 1;
+    if (validate_problem(&one) != FD_OK || plan.reserved[0] != kind) return false;
+    if (plan.kv_rows < 1 || plan.kv_rows > kMaxBatch || plan.seqs < 1 || plan.tokens < 1 || plan.num_splits < 1 ||
+        (long long)plan.seqs * plan.tokens > kMaxTokens || (long long)plan.seqs * plan.tokens * p.Hq > kMaxRows)
+        return false;
+    if (kind == kPlanCross && (plan.beams < 1 || (long long)plan.kv_rows * plan.beams != plan.seqs)) return false;
+    if (plan.capacity_tokens < 1 || plan.capacity_tokens > (long long)p.page_size * p.max_blocks_per_seq) return false;
+    return plan.timeout_us >= 0 && plan.debug_stall_us >= 0 && plan.debug_stall_us <= 1000000;
+}
+
+bool pools_ok(const fd_problem &p, const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale) {
+    const bool fp8 = p.kv_dtype == FD_E4M3;
+    if (!k_pages || !v_pages || fp8 != (k_scale != nullptr) || fp8 != (v_scale != nullptr)) return false;
+    return on(k_pages, 16) && on(v_pages, 16) && on(k_scale, 4) && on(v_scale, 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host, const fd_cross_options *options,
+                        fd_cross_plan_t *plan) {
+    if (!plan || !kv_lens_host) return FD_ERR_INVALID_ARG;
+    const fd_status st = validate_problem(problem);
+    if (st != FD_OK) return st;
+    fd_cross_options opt = {};
+    if (options) opt = *options;
+    if (opt.tokens < 0 || opt.beams < 0) return FD_ERR_INVALID_ARG;
+    opt.tokens = std::max(1, opt.tokens);
+    opt.beams = std::max(1, opt.beams);
+    if (opt.beams > kMaxBeams || opt.tokens > kMaxTokens) return FD_ERR_UNSUPPORTED;
+    if ((long long)problem->B * opt.beams > kMaxTokens) return FD_ERR_UNSUPPORTED;
+    const fd_status r = plan_rows(*problem, problem->B, problem->B * opt.beams, opt.tokens, problem->max_blocks_per_seq,
+                                  kv_lens_host, opt, [&](int) { return opt.beams; }, plan);
+    if (r != FD_OK) return r;
+    plan->beams = opt.beams;
+    plan->reserved[0] = kPlanCross;
+    return FD_OK;
+}
+
+fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q_stride, const int32_t *q_lens,
+                         const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                         const int32_t *block_table, const int32_t *kv_lens, void *out, float *lse, void *workspace,
+                         size_t workspace_bytes, int32_t *status_dev, void *stream) {
+    if (!plan || !plan_ok(*plan, kPlanCross)) return FD_ERR_INVALID_ARG;
+    const fd_problem &p = plan->problem;
+    if (!q || !block_table || !kv_lens || !out || !workspace || !pools_ok(p, k_pages, v_pages, k_scale, v_scale))
+        return FD_ERR_INVALID_ARG;
+    if (!on(q, 16) || !on(out, 16) || !on(lse, 4) || !on(q_lens, 4) || !on(block_table, 4) || !on(kv_lens, 4) ||
+        !on(workspace, 256) || !on(status_dev, 4))
+        return FD_ERR_INVALID_ARG;
+    if (q_stride < (long long)p.Hq * p.D || q_stride % 8) return FD_ERR_INVALID_ARG;
+    if (workspace_bytes < plan->workspace_bytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+    RowsParams rp;
+    std::memset(&rp, 0, sizeof(rp));
+    rp.q = q;
+    rp.q_stride = q_stride;
+    rp.q_lens = q_lens;
+    rp.block_table = block_table;
+    rp.kv_lens = kv_lens;
+    rp.k_scale = k_scale;
+    rp.v_scale = v_scale;
+    rp.out = out;
+    rp.lse = lse;
+    rp.status = status_dev;
+    return run_rows(*plan, rp, k_pages, v_pages, static_cast<uint8_t *>(workspace), stream);
+}
+
+fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host, int prefixes, int prefix_max_blocks,
+                         const int32_t *prefix_lens_host, const int32_t *offsets_host, const fd_plan_options *options,
+                         const fd_cross_options *prefix_options, fd_prefix_plan_t *plan) {
+    if (!plan || !seq_lens_host || !prefix_lens_host || !offsets_host) return FD_ERR_INVALID_ARG;
+    const fd_status st = validate_problem(problem);
+    if (st != FD_OK) return st;
+    const fd_problem &p = *problem;
+    if (prefixes < 1 || prefix_max_blocks < 1 || (long long)p.page_size * prefix_max_blocks > (1LL << 30))
+        return FD_ERR_INVALID_ARG;
+    if (prefixes > kMaxBatch) return FD_ERR_UNSUPPORTED;
+    if (offsets_host[0] != 0 || offsets_host[prefixes] > p.B) return FD_ERR_INVALID_ARG;
+    for (int s = 0; s < prefixes; ++s)
+        if (offsets_host[s + 1] < offsets_host[s]) return FD_ERR_INVALID_ARG;
+    if (p.out_dtype != p.q_dtype) return FD_ERR_UNSUPPORTED;
+    fd_plan_options own = {0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    if (options) own = *options;
+    if (own.shared_kv) return FD_ERR_UNSUPPORTED;
+    fd_cross_options opt = {};
+    if (prefix_options) opt = *prefix_options;
+    std::memset(plan, 0, sizeof(*plan));
+    fd_problem po = p;
+    po.out_dtype = FD_F32;  // a state that the other pass joins
+    fd_status r = FD_ERR_UNSUPPORTED;
+    try {
+        r = fd_plan(&po, seq_lens_host, &own, &plan->own);
+    } catch (...) {  // no memory for the lengths
+    }
+    if (r != FD_OK) return r;
+    opt.num_sms = own.num_sms;
+    opt.timeout_us = own.timeout_us;
+    const int T = std::max(1, own.q_len);
+    r = plan_rows(p, prefixes, p.B, T, prefix_max_blocks, prefix_lens_host, opt,
+                  [&](int s) { return (s < prefixes ? offsets_host[s + 1] : p.B) - offsets_host[s]; }, &plan->shared);
+    if (r != FD_OK) return r;
+    plan->shared.reserved[0] = kPlanPrefix;
+    plan->prefixes = prefixes;
+    const size_t rows = (size_t)p.B * T * p.Hq;
+    size_t at = 0;
+    plan->ws_own_out = at;
+    at += up256(rows * p.D * 4);
+    plan->ws_own_lse = at;
+    at += up256(rows * 4);
+    plan->ws_own = at;
+    at += up256(plan->own.workspace_bytes);
+    plan->ws_shared = at;
+    at += up256(plan->shared.workspace_bytes);
+    plan->workspace_bytes = at;
+    return FD_OK;
+}
+
+fd_status fd_decode_paged_prefix(const fd_prefix_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
+                                 const float *k_scale, const float *v_scale, const int32_t *prefix_table,
+                                 const int32_t *prefix_lens, const int32_t *members, const int32_t *offsets,
+                                 const int32_t *block_table, const int32_t *seq_lens, void *out, float *lse,
+                                 void *workspace, size_t workspace_bytes, int32_t *status_dev, void *stream) {
+    if (!plan || !plan_ok(plan->shared, kPlanPrefix)) return FD_ERR_INVALID_ARG;
+    const fd_cross_plan_t &sh = plan->shared;
+    const fd_problem &p = sh.problem;
+    if (plan->prefixes != sh.kv_rows || plan->own.kv_rows != sh.seqs || std::max(1, plan->own.q_len) != sh.tokens ||
+        plan->own.problem.Hq != p.Hq || plan->own.problem.Hkv != p.Hkv || plan->own.problem.D != p.D ||
+        plan->own.problem.out_dtype != FD_F32)
+        return FD_ERR_INVALID_ARG;
+    const size_t rows = (size_t)sh.seqs * sh.tokens * p.Hq;
+    if (plan->ws_own_lse < plan->ws_own_out || plan->ws_own_lse - plan->ws_own_out < rows * p.D * 4 ||
+        plan->ws_own < plan->ws_own_lse || plan->ws_own - plan->ws_own_lse < rows * 4 || plan->ws_shared < plan->ws_own ||
+        plan->ws_shared - plan->ws_own < plan->own.workspace_bytes || plan->workspace_bytes < plan->ws_shared ||
+        plan->workspace_bytes - plan->ws_shared < sh.workspace_bytes ||
+        (plan->ws_own_out | plan->ws_own_lse | plan->ws_own | plan->ws_shared) % 256)
+        return FD_ERR_INVALID_ARG;
+    if (!q || !prefix_table || !prefix_lens || !members || !offsets || !block_table || !seq_lens || !out || !workspace ||
+        !pools_ok(p, k_pages, v_pages, k_scale, v_scale))
+        return FD_ERR_INVALID_ARG;
+    if (!on(q, 16) || !on(out, 16) || !on(lse, 4) || !on(prefix_table, 4) || !on(prefix_lens, 4) || !on(members, 4) ||
+        !on(offsets, 4) || !on(block_table, 4) || !on(seq_lens, 4) || !on(workspace, 256) || !on(status_dev, 4))
+        return FD_ERR_INVALID_ARG;
+    if (workspace_bytes < plan->workspace_bytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    float *own_out = reinterpret_cast<float *>(ws + plan->ws_own_out);
+    float *own_lse = reinterpret_cast<float *>(ws + plan->ws_own_lse);
+    const fd_status st = fd_decode_paged(&plan->own, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                                         own_out, own_lse, ws + plan->ws_own, plan->own.workspace_bytes, status_dev,
+                                         stream);
+    if (st != FD_OK) return st;
+    RowsParams rp;
+    std::memset(&rp, 0, sizeof(rp));
+    rp.q = q;
+    rp.q_stride = (long long)p.Hq * p.D;
+    rp.members = members;
+    rp.offsets = offsets;
+    rp.block_table = prefix_table;
+    rp.kv_lens = prefix_lens;
+    rp.k_scale = k_scale;
+    rp.v_scale = v_scale;
+    rp.out = out;
+    rp.lse = lse;
+    rp.own_out = own_out;
+    rp.own_lse = own_lse;
+    rp.status = status_dev;
+    return run_rows(sh, rp, k_pages, v_pages, ws + plan->ws_shared, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,149 @@
+"""Cross attention (CrossDecoder, fd_cross_paged) against the float64
+definition, with NaN behind every length and in every unused page."""
+import pytest
+import torch
+
+import split_kv_decode_paged_gb300 as fd
+from split_kv_decode_paged_gb300 import _lib
+from tests.shared_ref import Cross
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, E4M3 = torch.float16, torch.bfloat16, torch.float8_e4m3fn
+KINDS = [(F16, F16), (BF16, BF16), (E4M3, BF16), (E4M3, F16)]
+IDS = ["f16", "bf16", "e4m3-bf16", "e4m3-f16"]
+
+
+def run(c, plan_lens=None, want_lse=True, fill=7.0, **opts):
+    d = c.device()
+    q_lens = d.pop("q_lens")
+    dec = fd.CrossDecoder.for_pools(d["q"], d["k_pages"], d["v_pages"], d["block_table"], plan_lens or c.kv_lens,
+                                    beams=c.beams, **opts)
+    out = torch.full_like(d["q"], fill)
+    lse = torch.full(d["q"].shape[:-1], fill, device="cuda") if want_lse else None
+    dec(**d, q_lens=q_lens, out=out, lse=lse, want_lse=want_lse)
+    dec.check()
+    return out, lse, dec
+
+
+@pytest.mark.parametrize("kv,q", KINDS, ids=IDS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_single_tokens(fdlib, kv, q, D):
+    """Lengths of zero, one, around pages and tiles; one token each."""
+    c = Cross(1, [0, 1, 15, 16, 17, 127, 128, 129, 300, 513], Hq=8, Hkv=2, D=D, kv=kv, q=q, ps=32)
+    out, lse, _ = run(c)
+    c.verify(out, lse, what="single tokens")
+
+
+@pytest.mark.parametrize("kv,q", KINDS, ids=IDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,T", [(2, 2, 130), (8, 2, 70), (5, 1, 27), (6, 2, 300), (12, 1, 33)])
+def test_prompts(fdlib, kv, q, D, Hq, Hkv, T):
+    """More query rows than a tile holds, groups that do not divide one."""
+    c = Cross(2, [77, 0, 260, 5], T=T, Hq=Hq, Hkv=Hkv, D=D, kv=kv, q=q)
+    out, lse, _ = run(c)
+    c.verify(out, lse, what="prompts")
+
+
+@pytest.mark.parametrize("ps", [16, 32, 48, 64, 128, 176, 256])
+@pytest.mark.parametrize("kv,q", KINDS[1:3], ids=IDS[1:3])
+def test_page_sizes(fdlib, kv, q, ps):
+    c = Cross(3, [401, 176, 129], T=9, Hq=4, Hkv=2, D=128, kv=kv, q=q, ps=ps)
+    out, lse, _ = run(c)
+    c.verify(out, lse, what=f"page size {ps}")
+
+
+@pytest.mark.parametrize("beams,T", [(1, 6), (3, 1), (5, 40), (70, 2)])
+@pytest.mark.parametrize("kv,q", KINDS, ids=IDS)
+def test_beams_and_padded_queries(fdlib, beams, T, kv, q):
+    """Rows past a sequence's query tokens stay as they were; a sequence may
+    have none."""
+    lens = [200, 33, 0]
+    counts = [(3 * i) % (T + 1) for i in range(len(lens) * beams)]
+    c = Cross(4, lens, beams=beams, T=T, Hq=4, Hkv=2, D=64, kv=kv, q=q, q_lens=counts)
+    out, lse, _ = run(c)
+    c.verify(out, lse, untouched=7.0, what="padded")
+
+
+@pytest.mark.parametrize("splits", [1, 2, 5, 16])
+@pytest.mark.parametrize("kv,q", KINDS, ids=IDS)
+@pytest.mark.parametrize("T", [1, 40])
+def test_splits(fdlib, splits, kv, q, T):
+    """KV rows cut into chunks and joined; short rows beside them are not."""
+    c = Cross(5, [2100, 900, 0, 130, 1], T=T, Hq=8, Hkv=2, D=128, kv=kv, q=q, ps=64)
+    out, lse, dec = run(c, num_splits=splits)
+    c.verify(out, lse, what=f"{splits} splits")
+
+
+def test_lengths_change_within_the_capacity(fdlib):
+    c = Cross(6, [50, 700, 300], T=3, Hq=4, Hkv=2, D=64, pad_cols=30)
+    out, lse, dec = run(c, plan_lens=[10, 20, 30], max_kv_len=1024)
+    c.verify(out, lse, what="grown lengths")
+
+
+def test_strided_queries_and_no_lse(fdlib):
+    c = Cross(7, [99, 200], T=5, Hq=4, Hkv=2, D=64)
+    d = c.device()
+    wide = torch.randn(2, 5, 3 * 4 * 64, device="cuda").to(torch.bfloat16)
+    q = wide[..., 256:512].unflatten(-1, (4, 64))
+    q.copy_(d["q"])
+    dec = fd.CrossDecoder.for_pools(q, d["k_pages"], d["v_pages"], d["block_table"], c.kv_lens)
+    out, lse = dec(q, d["k_pages"], d["v_pages"], d["block_table"], d["kv_lens"], want_lse=False)
+    dec.check()
+    assert lse is None
+    c.verify(out, None, what="strided")
+
+
+def test_large_scores(fdlib):
+    """Scores of some hundreds: the running maximum moves, nothing overflows."""
+    for kv in (F16, BF16):
+        c = Cross(8, [1000, 260], T=70, Hq=4, Hkv=2, D=128, kv=kv, q_mult=40.0)
+        out, lse, _ = run(c)
+        c.verify(out, lse, what="large scores")
+
+
+def test_rising_maximum(fdlib):
+    """Keys that grow along the row: every tile passes the reference maximum."""
+    c = Cross(9, [900], T=40, Hq=4, Hkv=2, D=64)
+    ramp = torch.linspace(0.1, 12.0, 900)
+    for j in range(57):
+        page = int(c.table[0, j])
+        n = min(16, 900 - 16 * j)
+        c.k[page, :n] = (c.k[page, :n].float() * ramp[16 * j:16 * j + n, None, None]).to(BF16)
+    out, lse, _ = run(c)
+    c.verify(out, lse, what="rising maximum")
+
+
+def test_device_errors_are_reported(fdlib):
+    """Lengths beyond the capacity, pages and query counts out of range: the
+    status says so, the other sequences are right, nothing else is touched."""
+    c = Cross(10, [100, 60, 90], T=4, Hq=4, Hkv=2, D=64)
+    d = c.device()
+    ql = d.pop("q_lens")
+    assert ql is None
+    dec = fd.CrossDecoder.for_pools(d["q"], d["k_pages"], d["v_pages"], d["block_table"], c.kv_lens)
+
+    def call(bit, good, **kw):
+        out = torch.full_like(d["q"], 7.0)
+        dec(**{**d, **kw}, out=out)
+        assert int(dec.status.item()) & bit  # a cut length may meet unused pages: their bit as well
+        with pytest.raises(fd.FdError):
+            dec.check()
+        ref, _ = dec(**d)
+        dec.check()
+        for b in good:
+            assert torch.equal(out[b], ref[b])
+        return out
+
+    long = d["kv_lens"].clone()
+    long[1] = 5000
+    call(_lib.FD_DEV_CAPACITY, [0, 2], kv_lens=long)
+    long[1] = -3
+    out = call(_lib.FD_DEV_CAPACITY, [0, 2], kv_lens=long)
+    assert bool((out[1] == 0).all())
+    table = d["block_table"].clone()
+    table[2, 1] = 1 << 20
+    call(_lib.FD_DEV_BAD_PAGE, [0, 1], block_table=table)
+    counts = torch.tensor([4, 9, -1], dtype=torch.int32, device="cuda")
+    out = call(_lib.FD_DEV_CAPACITY, [0], q_lens=counts)
+    assert bool((out[1:] == 7.0).all())
