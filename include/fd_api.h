@@ -594,10 +594,9 @@ typedef struct {
     int num_splits;       /* partial-state slots per query row                    */
     int chunk_tokens;     /* tokens per split                                     */
     int capacity_tokens;
-    int tile_rows;        /* query rows of one work item                          */
+    int tile_rows;        /* query rows of one work item, at most                 */
     int grid_ctas;
     int num_sms;
-    int smem_bytes;       /* dynamic shared memory per CTA                        */
     int timeout_us;
     int debug_stall_us;
     size_t workspace_bytes;

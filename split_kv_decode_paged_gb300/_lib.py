@@ -100,8 +100,8 @@ class FdCrossOptions(ctypes.Structure):
 class FdCrossPlan(ctypes.Structure):
     _fields_ = ([("problem", FdProblem)] +
                 [(n, ctypes.c_int) for n in ("kv_rows", "seqs", "tokens", "beams", "num_splits", "chunk_tokens",
-                                             "capacity_tokens", "tile_rows", "grid_ctas", "num_sms", "smem_bytes",
-                                             "timeout_us", "debug_stall_us")] +
+                                             "capacity_tokens", "tile_rows", "grid_ctas", "num_sms", "timeout_us",
+                                             "debug_stall_us")] +
                 [(n, ctypes.c_size_t) for n in ("workspace_bytes", "ws_partial_o", "ws_partial_md", "ws_counters")] +
                 [("reserved", ctypes.c_int * 4)])
 

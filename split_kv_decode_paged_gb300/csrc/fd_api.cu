@@ -287,7 +287,7 @@ EncodeTiledFn encode_fn() {
 // kvh, page): one box = `boxr` token rows x all of D for one KV head, landing
 // in shared memory as [span][row][span bytes] so each span is one swizzled
 // region (a span is 128 bytes, or the whole row when the row is shorter).
-bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr) {
+bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool one_span) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int e = elem_bytes(p.kv_dtype);
@@ -298,7 +298,7 @@ bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p
                           (cuuint64_t)p.num_pages};
     cuuint64_t strides[4] = {(cuuint64_t)rb * p.Hkv, (cuuint64_t)span, (cuuint64_t)rb,
                              (cuuint64_t)rb * p.Hkv * p.page_size};
-    cuuint32_t box[5] = {(cuuint32_t)(span / e), (cuuint32_t)boxr, (cuuint32_t)nspan, 1u, 1u};
+    cuuint32_t box[5] = {(cuuint32_t)(span / e), (cuuint32_t)boxr, (cuuint32_t)(one_span ? 1 : nspan), 1u, 1u};
     cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
     const CUtensorMapDataType dt = e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     const CUtensorMapSwizzle sw = span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;

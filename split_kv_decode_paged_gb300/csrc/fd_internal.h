@@ -136,11 +136,14 @@ struct RowsParams {
     const float *own_lse;      // tokens that joins every row's, or null
     float *part_o;             // [seqs * T * Hq, S, D]: unnormalised; m in log2 units
     float *part_m, *part_d;    // [seqs * T * Hq, S]
-    int *counters;
+    int *row_splits;           // [seqs * T * Hq] partial states to merge, 0: none (zeros between calls)
+    int *counters;             // 2, zeros between calls
     int *status;
     int kv_rows, seqs, T, beams, Hq, Hkv, G;
     int page_size, max_blocks, num_pages;
     int S, chunk, cap;
+    int boxr;                  // token rows per TMA box: gcd(page_size, tile)
+    int kv_once;               // K and V are read by one item only
     int q_bf16, kv_kind, D;
     float scale_log2;          // log2(e) / sqrt(D)
     uint64_t timeout_ns, stall_ns;
@@ -205,7 +208,9 @@ bool weights_launchable(int Bkv, int Hkv, long long cap, long long R);
 cudaError_t launch_weights(const WeightParams &wp, cudaStream_t stream);
 cudaError_t launch_append_norm(NormAppendParams p, int D, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
-cudaError_t launch_rows(const RowsParams &p, cudaStream_t stream);
+cudaError_t launch_rows(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream);
+// The merge of the rows that it left in partial states.
+cudaError_t launch_rows_merge(const RowsParams &p, cudaStream_t stream);
 
 // Checks and encodings that the entry points share (fd_api.cu).
 struct DeviceInfo {
@@ -216,8 +221,9 @@ struct DeviceInfo {
 };
 fd_status device_info(DeviceInfo &di);
 fd_status validate_problem(const fd_problem *p);
-// Tensor map of a K or V pool with boxes of boxr token rows of one KV head.
-bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr);
+// Tensor map of a K or V pool with boxes of boxr token rows of one KV head: all
+// 128-byte spans of a row, one after the other, or one of them.
+bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool one_span = false);
 
 cudaError_t launch_merge_two(const float *oa, const float *la, const float *ob, const float *lb, int rows, int D,
                              int out_dtype, void *out, float *lse, cudaStream_t stream);

@@ -75,6 +75,13 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     return pol;
 }
 
+// The ordinary policy, where a load takes one.
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
 // 5-D tiled tensor load into CTA shared memory with an L2 cache policy;
 // completion counted in bytes on an mbarrier.  Coordinates are element
 // indices, innermost first.

@@ -9,6 +9,7 @@
 
 #include "fd_internal.h"
 #include "ptx.cuh"
+#include "rows_kernel.cuh"
 
 namespace fd {
 
@@ -40,7 +41,7 @@ __device__ int group_end(const RowsParams &p, int s) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) fd_rows_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(128) fd_rows_plain_kernel(const RowsParams p) {
     constexpr int E = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * 4 + warp;
@@ -142,16 +143,109 @@ __global__ void __launch_bounds__(128) fd_rows_kernel(const RowsParams p) {
     if (lane == 0 && p.lse) p.lse[row] = lse;
 }
 
+// One warp a query row (sequence, token, head): the partial states of its chunks
+// and, where there is one, the state over its own tokens.  Rows that the main
+// kernel finished itself, or never had, have row_splits = 0.
+template <int D>
+__global__ void __launch_bounds__(128) fd_rows_merge_kernel(const RowsParams p) {
+    constexpr int E = D / 32;
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + warp;
+    if (row >= (long long)p.seqs * p.T * p.Hq) return;
+    const int n = __ldcg(p.row_splits + row);
+    if (n == 0) return;
+    __syncwarp();
+    if (lane == 0) p.row_splits[row] = 0;
+    const float *pm = p.part_m + row * p.S, *pd = p.part_d + row * p.S;
+    float mx = -INFINITY;
+    for (int s = lane; s < n; s += 32) mx = fmaxf(mx, __ldcg(pm + s));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, shfl_xor(mx, o));
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, y[E];
+#pragma unroll
+    for (int x = 0; x < E; ++x) y[x] = 0.f;
+    for (int s = 0; s < n; ++s) {
+        const float d = __ldcg(pd + s);
+        if (d == 0.f) continue;  // an empty state
+        const float a = ex2(__ldcg(pm + s) - base);
+        sum = fmaf(a, d, sum);
+        const float *po = p.part_o + (row * p.S + s) * D + lane * E;
+#pragma unroll
+        for (int x = 0; x < E; ++x) y[x] = fmaf(a, __ldcg(po + x), y[x]);
+    }
+    const bool empty = sum == 0.f;
+    float lse = empty ? -INFINITY : (mx + __log2f(sum)) * kLn2;
+    float mul = empty ? 0.f : 1.f / sum, own = 0.f;
+    if (p.own_out) {
+        const float lo = __ldcg(p.own_lse + row), m = fmaxf(lse, lo);
+        const float wa = lse == -INFINITY ? 0.f : __expf(lse - m), wb = lo == -INFINITY ? 0.f : __expf(lo - m);
+        const float inv = wa + wb > 0.f ? 1.f / (wa + wb) : 0.f;
+        mul *= wa * inv;
+        own = wb * inv;
+        lse = m == -INFINITY ? -INFINITY : m + logf(wa + wb);
+    }
+    if (lane == 0 && p.lse) p.lse[row] = lse;
+#pragma unroll
+    for (int x = 0; x < E; ++x) {
+        y[x] *= mul;
+        if (p.own_out) y[x] = fmaf(own, __ldcg(p.own_out + row * D + lane * E + x), y[x]);
+    }
+    uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(p.out) + row * D + lane * E);
+#pragma unroll
+    for (int x = 0; x < E; x += 2) dst[x / 2] = p.q_bf16 ? pack_bf16x2(y[x], y[x + 1]) : pack_f16x2(y[x], y[x + 1]);
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_after(Kernel kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
+    // Programmatic dependent launch: the prologue may run while the previous
+    // grid of the stream drains; the kernel waits before it reads anything.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int KV, int D>
+cudaError_t launch_rows_t(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream) {
+    using Sh = RowsShape<KV, D>;
+    auto kern = fd_rows_kernel<KV, D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_after(kern, (unsigned)grid, Sh::THREADS, Sh::SMEM, stream, p, tmk, tmv);
+}
+
 }  // namespace
 
-cudaError_t launch_rows(const RowsParams &p, cudaStream_t stream) {
+cudaError_t launch_rows(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream) {
+    if (p.kv_kind == KV_BF16)
+        return p.D == 128 ? launch_rows_t<KV_BF16, 128>(p, tmk, tmv, grid, stream)
+                          : launch_rows_t<KV_BF16, 64>(p, tmk, tmv, grid, stream);
+    if (p.kv_kind == KV_F16)
+        return p.D == 128 ? launch_rows_t<KV_F16, 128>(p, tmk, tmv, grid, stream)
+                          : launch_rows_t<KV_F16, 64>(p, tmk, tmv, grid, stream);
     const long long rows = (long long)p.seqs * p.T * p.Hq;
-    const unsigned grid = (unsigned)((rows + 3) / 4);
+    const unsigned blocks = (unsigned)((rows + 3) / 4);
     if (p.D == 128)
-        fd_rows_kernel<128><<<grid, 128, 0, stream>>>(p);
+        fd_rows_plain_kernel<128><<<blocks, 128, 0, stream>>>(p);
     else
-        fd_rows_kernel<64><<<grid, 128, 0, stream>>>(p);
+        fd_rows_plain_kernel<64><<<blocks, 128, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t launch_rows_merge(const RowsParams &p, cudaStream_t stream) {
+    const long long rows = (long long)p.seqs * p.T * p.Hq;
+    const unsigned blocks = (unsigned)((rows + 3) / 4);
+    return p.D == 128 ? launch_after(fd_rows_merge_kernel<128>, blocks, 128, 0, stream, p)
+                      : launch_after(fd_rows_merge_kernel<64>, blocks, 128, 0, stream, p);
 }
 
 }  // namespace fd

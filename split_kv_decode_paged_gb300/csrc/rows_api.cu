@@ -3,6 +3,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <numeric>
+#include <queue>
+#include <vector>
 
 #include "fd_internal.h"
 
@@ -20,50 +23,145 @@ constexpr int kPlanCross = 2, kPlanPrefix = 3;      // fd_cross_plan_t::reserved
 bool on(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Shared by both planners.  seqs_of(s): sequences of segment s (segment kv_rows:
-// those without a prefix).
-template <typename SeqsOf>
+// One work item: up to kItemRows query rows of a KV head over a chunk of a KV
+// row, in tiles of kTile tokens and kTile rows.
+constexpr int kTile = 128, kItemRows = 256;
+constexpr int kMaxRowSplits = 64;
+constexpr size_t kMaxPartialBytes = size_t(256) << 20;
+// Times of the cost model, in ns: what an item costs beside its tiles (query
+// rows, epilogue), what a split one costs more (its partial state), and the
+// second launch that merges.
+constexpr double kItemNs = 2500, kSplitNs = 1000, kMergeNs = 3000;
+
+// Time of one CTA for a tile of 128 tokens: the largest of its share of the
+// memory's rate, of the products of its row tiles and, for one row tile alone,
+// of the chain from scores through softmax to output.
+double tile_ns(const fd_problem &p, int row_tiles) {
+    const double bytes = 2.0 * kTile * p.D * (p.kv_dtype == FD_E4M3 ? 1 : 2) / 44.0;
+    const double flops = row_tiles * 4.0 * kTile * kTile * p.D / 11000.0;
+    return std::max(std::max(bytes, flops), p.D == 128 ? 1200.0 : 900.0);
+}
+
+// Shared by both planners.  tokens_of(s): query tokens of segment s (segment
+// kv_rows: those without a prefix).
+template <typename TokensOf>
 fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int max_blocks, const int32_t *kv_lens,
-                    const fd_cross_options &opt, SeqsOf seqs_of, fd_cross_plan_t *plan) {
+                    const fd_cross_options &opt, TokensOf tokens_of, fd_cross_plan_t *plan) {
     if (opt.num_splits < 0 || opt.num_sms < 0 || opt.num_sms > kMaxRowSms || opt.max_kv_len < 0 || opt.timeout_us < 0 ||
         opt.debug_stall_us < 0 || opt.debug_stall_us > 1000000)
         return FD_ERR_INVALID_ARG;
     if (p.out_dtype != p.q_dtype) return FD_ERR_UNSUPPORTED;
     if (kv_rows > kMaxBatch || (long long)seqs * tokens > kMaxTokens || (long long)seqs * tokens * p.Hq > kMaxRows)
         return FD_ERR_UNSUPPORTED;
-    long long longest = std::max(1, opt.max_kv_len);
+    int longest = 1, sms = opt.num_sms;
     for (int s = 0; s < kv_rows; ++s) {
         if (kv_lens[s] < 0) return FD_ERR_INVALID_ARG;
-        longest = std::max<long long>(longest, kv_lens[s]);
+        longest = std::max(longest, (int)kv_lens[s]);
     }
-    if (longest > (long long)p.page_size * max_blocks) return FD_ERR_INVALID_ARG;
-    int sms = opt.num_sms;
+    const int room = std::max(longest, opt.max_kv_len);
+    if (room > (long long)p.page_size * max_blocks) return FD_ERR_INVALID_ARG;
     if (sms == 0) {
         DeviceInfo di;
-        fd_status st = FD_ERR_CUDA;
-        try {
-            st = device_info(di);
-        } catch (...) {
-        }
+        const fd_status st = device_info(di);
         if (st != FD_OK) return st;
         sms = di.sms;
     }
-    (void)seqs_of;
+    // Chunks: the count that the cost model finds cheapest (fewest of equals).
+    const size_t rows = (size_t)seqs * tokens * p.Hq;
+    const int G = p.Hq / p.Hkv;
+    auto chunk_of = [&](int S) { return (int)(((long long)longest + S - 1) / S + kTile - 1) / kTile * kTile; };
+    auto fits = [&](int C) {
+        const long long S = ((long long)room + C - 1) / C;
+        return S == 1 || (S <= kMaxRowSplits && rows * S * (p.D + 2) * sizeof(float) <= kMaxPartialBytes);
+    };
+    // items of all KV heads with chunks of C tokens, and their time on sms CTAs
+    auto cost = [&](int C, long long *items_out) {
+        std::vector<std::pair<double, long long>> items;  // time, how many of it
+        double total = 0;
+        long long count = 0;
+        bool split = false;
+        auto add = [&](double ns, long long n) {
+            if (n < 1) return;
+            items.push_back({ns, n});
+            total += ns * n;
+            count += n;
+        };
+        for (int s = 0; s <= kv_rows; ++s) {
+            const long long r = (long long)tokens_of(s) * G;
+            const int L = s < kv_rows ? kv_lens[s] : 0;
+            const int ns = L == 0 ? 1 : (L + C - 1) / C;
+            split |= ns > 1;
+            const long long whole = r / kItemRows * p.Hkv;
+            const int rest = (int)(r % kItemRows);
+            const int last = L - (ns - 1) * C;  // tokens of the last chunk
+            const double more = kItemNs + (ns > 1 ? kSplitNs : 0);
+            for (int part = 0; part < 2; ++part) {
+                const double tiles = (part ? last : C) / (double)kTile;
+                const long long n = part ? 1 : ns - 1;
+                add(std::ceil(tiles) * tile_ns(p, 2) + more, n * whole);
+                if (rest) add(std::ceil(tiles) * tile_ns(p, rest > kTile ? 2 : 1) + more, n * p.Hkv);
+            }
+        }
+        if (items_out) *items_out = count;
+        double longest_item = 0;
+        for (const auto &it : items) longest_item = std::max(longest_item, it.first);
+        if (count > 64LL * sms)  // plenty: the tail is about half an item
+            return total / sms + 0.5 * longest_item + (split ? kMergeNs : 0);
+        std::priority_queue<double, std::vector<double>, std::greater<double>> q;
+        for (int i = 0; i < sms; ++i) q.push(0.0);
+        double worst = 0;
+        for (const auto &it : items)
+            for (long long k = 0; k < it.second; ++k) {
+                const double t = q.top() + it.first;
+                q.pop();
+                worst = std::max(worst, t);
+                q.push(t);
+            }
+        return worst + (split ? kMergeNs : 0);
+    };
+    int best = chunk_of(std::max(1, std::min(opt.num_splits, kMaxRowSplits)));
+    if (opt.num_splits == 0) {
+        double best_cost = -1;
+        int last = 0;
+        for (int S = 1; S <= kMaxRowSplits; ++S) {
+            const int C = chunk_of(S);
+            if (C == last || !fits(C)) continue;
+            last = C;
+            const double t = cost(C, nullptr);
+            if (best_cost < 0 || t < best_cost * 0.98) {
+                best_cost = t;
+                best = C;
+            }
+        }
+    }
+    while (!fits(best)) best = (best + best / 2 + kTile - 1) / kTile * kTile;
+    long long items = 0;
+    cost(best, &items);
+    // other lengths or groups than the planned ones may make more items
+    items = std::max(items, (long long)sms);
     std::memset(plan, 0, sizeof(*plan));
     plan->problem = p;
     plan->problem.max_blocks_per_seq = max_blocks;
     plan->kv_rows = kv_rows;
     plan->seqs = seqs;
     plan->tokens = tokens;
-    plan->num_splits = 1;
-    plan->chunk_tokens = (int)longest;
-    plan->capacity_tokens = (int)longest;
-    plan->tile_rows = 1;
-    plan->grid_ctas = 1;
+    plan->num_splits = (room + best - 1) / best;
+    plan->chunk_tokens = best;
+    plan->capacity_tokens = room;
+    plan->tile_rows = kItemRows;
+    plan->grid_ctas = (int)std::min<long long>(items, sms);
     plan->num_sms = sms;
     plan->timeout_us = opt.timeout_us;
     plan->debug_stall_us = opt.debug_stall_us;
-    plan->workspace_bytes = 256;
+    const size_t S = plan->num_splits > 1 ? (size_t)plan->num_splits : 0;
+    size_t at = 0;
+    plan->ws_partial_o = at;
+    at += up256(rows * S * p.D * sizeof(float));
+    plan->ws_partial_md = at;
+    at += up256(2 * rows * S * sizeof(float));
+    plan->ws_counters = at;
+    at += 256 + (S ? up256(rows * sizeof(int)) : 0);
+    plan->workspace_bytes = at;
     return FD_OK;
 }
 
@@ -92,8 +190,21 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     rp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.D));
     rp.timeout_ns = plan.timeout_us > 0 ? (uint64_t)plan.timeout_us * 1000ull : kRowsTimeoutNs;
     rp.stall_ns = (uint64_t)plan.debug_stall_us * 1000ull;
-    (void)workspace;
-    return launch_rows(rp, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+    const size_t rows = (size_t)plan.seqs * plan.tokens * p.Hq;
+    rp.part_o = reinterpret_cast<float *>(workspace + plan.ws_partial_o);
+    rp.part_m = reinterpret_cast<float *>(workspace + plan.ws_partial_md);
+    rp.part_d = rp.part_m + rows * plan.num_splits;
+    rp.counters = reinterpret_cast<int *>(workspace + plan.ws_counters);
+    rp.row_splits = rp.counters + 64;
+    rp.boxr = std::gcd(p.page_size, kTile);
+    rp.kv_once = 0;
+    CUtensorMap tmk, tmv;
+    if (!encode_pool_map(&tmk, k_pages, p, rp.boxr, true) || !encode_pool_map(&tmv, v_pages, p, rp.boxr, true))
+        return FD_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_rows(rp, tmk, tmv, plan.grid_ctas, s) != cudaSuccess) return FD_ERR_CUDA;
+    if (plan.num_splits > 1 && launch_rows_merge(rp, s) != cudaSuccess) return FD_ERR_CUDA;
+    return FD_OK;
 }
 
 // What a plan handed in must satisfy for its launch to stay in bounds.
@@ -106,6 +217,15 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
         (long long)plan.seqs * plan.tokens > kMaxTokens || (long long)plan.seqs * plan.tokens * p.Hq > kMaxRows)
         return false;
     if (kind == kPlanCross && (plan.beams < 1 || (long long)plan.kv_rows * plan.beams != plan.seqs)) return false;
+    if (plan.chunk_tokens < kTile || plan.chunk_tokens % kTile || plan.num_splits > kMaxRowSplits || plan.grid_ctas < 1 ||
+        plan.capacity_tokens > (long long)plan.num_splits * plan.chunk_tokens)
+        return false;
+    const size_t rows = (size_t)plan.seqs * plan.tokens * p.Hq, S = plan.num_splits > 1 ? (size_t)plan.num_splits : 0;
+    if ((plan.ws_partial_o | plan.ws_partial_md | plan.ws_counters) % 256 || plan.ws_partial_md < plan.ws_partial_o ||
+        plan.ws_partial_md - plan.ws_partial_o < rows * S * p.D * sizeof(float) || plan.ws_counters < plan.ws_partial_md ||
+        plan.ws_counters - plan.ws_partial_md < 2 * rows * S * sizeof(float) || plan.workspace_bytes < plan.ws_counters ||
+        plan.workspace_bytes - plan.ws_counters < 256 + (S ? rows * sizeof(int) : 0))
+        return false;
     if (plan.capacity_tokens < 1 || plan.capacity_tokens > (long long)p.page_size * p.max_blocks_per_seq) return false;
     return plan.timeout_us >= 0 && plan.debug_stall_us >= 0 && plan.debug_stall_us <= 1000000;
 }
@@ -132,8 +252,12 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host, 
     opt.beams = std::max(1, opt.beams);
     if (opt.beams > kMaxBeams || opt.tokens > kMaxTokens) return FD_ERR_UNSUPPORTED;
     if ((long long)problem->B * opt.beams > kMaxTokens) return FD_ERR_UNSUPPORTED;
-    const fd_status r = plan_rows(*problem, problem->B, problem->B * opt.beams, opt.tokens, problem->max_blocks_per_seq,
-                                  kv_lens_host, opt, [&](int) { return opt.beams; }, plan);
+    fd_status r = FD_ERR_UNSUPPORTED;
+    try {
+        r = plan_rows(*problem, problem->B, problem->B * opt.beams, opt.tokens, problem->max_blocks_per_seq, kv_lens_host,
+                      opt, [&](int s) { return s < problem->B ? (long long)opt.beams * opt.tokens : 0LL; }, plan);
+    } catch (...) {  // no memory for the items
+    }
     if (r != FD_OK) return r;
     plan->beams = opt.beams;
     plan->reserved[0] = kPlanCross;
@@ -199,8 +323,13 @@ fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host
     opt.num_sms = own.num_sms;
     opt.timeout_us = own.timeout_us;
     const int T = std::max(1, own.q_len);
-    r = plan_rows(p, prefixes, p.B, T, prefix_max_blocks, prefix_lens_host, opt,
-                  [&](int s) { return (s < prefixes ? offsets_host[s + 1] : p.B) - offsets_host[s]; }, &plan->shared);
+    r = FD_ERR_UNSUPPORTED;
+    try {
+        r = plan_rows(p, prefixes, p.B, T, prefix_max_blocks, prefix_lens_host, opt,
+                      [&](int s) { return (long long)T * ((s < prefixes ? offsets_host[s + 1] : p.B) - offsets_host[s]); },
+                      &plan->shared);
+    } catch (...) {  // no memory for the items
+    }
     if (r != FD_OK) return r;
     plan->shared.reserved[0] = kPlanPrefix;
     plan->prefixes = prefixes;

@@ -1,0 +1,739 @@
+// rows_kernel.cuh -- attention of many query rows over KV rows that all of them
+// see (cross attention, the pass over shared prefixes), on tcgen05.
+//
+// The mathematics.  For the query rows r of a KV head (its G query heads, times
+// the query tokens of every sequence that reads the KV row) and its n tokens:
+//   S = Q K^T,  P = exp2(S c - m_r),  l_r = sum P,  O = P V,  out = O / l_r,
+// c = log2(e) / sqrt(D), in one pass over K and V: m_r is a running reference
+// that moves only when a score passes it by more than kSlack, and then l_r and
+// O are scaled.  No row hides a token from another, so a tile of 128 rows is a
+// plain matrix product, whatever sequences, tokens and heads its rows are.
+//
+// A work item is (KV row, KV head, chunk of its tokens, up to 256 query rows):
+// two tiles of 128 rows, each with its own S / P and O in tensor memory, that
+// take the same K and V tiles of 128 tokens.  While the softmax of one tile
+// runs, the tensor cores work on the other's products.
+//
+// CTA (one an SM, persistent; items claimed from a counter):
+//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread has one row; reads its
+//                   128 scores, writes P over them (16 bits), scales O when the
+//                   reference moves, and finishes the item's rows
+//   warp 8          issues the products
+//   warp 9          claims items, loads K and V tiles by TMA into a ring
+//   warps 10-11     gather the query rows (any sequence, token and head order,
+//                   any token stride) into swizzled shared memory
+// Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
+// leaves the loop, which ends the others' waits the same way.
+#pragma once
+
+#include <math.h>
+
+#include "fd_internal.h"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace fd {
+
+constexpr int kTileTokens = 128;
+constexpr int kTileRows = 128;   // query rows of one tile; two tiles an item
+constexpr int kItemSlots = 2;
+constexpr float kRowsLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;    // log2 headroom of the softmax reference
+
+struct RowsItem {
+    int seg;      // KV row; kv_rows: none; -1: no more items
+    int kvh;
+    int row0;     // first query row of the item within (segment, KV head)
+    int nrows;    // 1 .. 256
+    int first;    // member place of the segment's first sequence
+    int tok0;     // first token of the chunk
+    int ntok;     // tokens of the chunk (0: an empty KV row)
+    int split;
+    int nsplit;
+    int pad[3];
+};
+
+template <int KV, int D>
+struct RowsShape {
+    static constexpr int HALVES = D / 64;                   // 128-byte spans of a row
+    static constexpr int TILE = kTileTokens * D * 2;        // bytes of a Q, K or V tile (16 bits)
+    static constexpr int SPAN = kTileTokens * 128;          // bytes of one half of it
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr int THREADS = 384;
+    // shared memory: control block, two Q tiles, the ring
+    static constexpr int CONTROL = 3072;
+    static constexpr int SMEM = CONTROL + 2 * TILE + STAGES * TILE;
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
+
+struct RowsControl {
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full[kItemSlots];
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t drain;
+    uint32_t tmem;
+    int pad;
+    RowsItem item[kItemSlots];
+    int tok[kItemSlots][2 * kTileRows];  // q token (sequence * T + token) of every row, -1 past the end
+};
+static_assert(sizeof(RowsControl) <= 3072, "the control block's room");
+
+// The segments of a call: query tokens and KV length of each, in the kernel's
+// dispatch order.  Lengths, counts and offsets that are out of range are cut.
+struct Segments {
+    const RowsParams &p;
+    __device__ int count() const { return p.kv_rows + (p.offsets ? 1 : 0); }
+    // offsets[s] before it is made to rise
+    __device__ int raw_offset(int s) const { return s > p.kv_rows ? p.seqs : (s == 0 ? 0 : __ldg(p.offsets + s)); }
+    __device__ int q_len(int b) const {
+        if (!p.q_lens) return p.T;
+        const int n = __ldg(p.q_lens + b);
+        return n < 0 || n > p.T ? 0 : n;
+    }
+    __device__ int kv_len(int s) const {
+        if (s >= p.kv_rows) return 0;
+        return min(max(__ldg(p.kv_lens + s), 0), p.cap);
+    }
+    // query tokens of sequences [first, end) of the member order
+    __device__ int tokens(int first, int end) const {
+        if (!p.q_lens) return (end - first) * p.T;
+        int n = 0;
+        for (int b = first; b < end; ++b) n += q_len(b);
+        return n;
+    }
+    // items of a segment with that many query tokens
+    __device__ int items(int tokens, int len) const {
+        const int mt = (tokens * p.G + 2 * kTileRows - 1) / (2 * kTileRows);
+        const int ns = len == 0 ? 1 : (len + p.chunk - 1) / p.chunk;
+        return mt * ns * p.Hkv;
+    }
+};
+
+__device__ __forceinline__ void rows_flag(int *status, int bit) {
+    if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool live) {
+    const int n = live ? 16 : 0;  // 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A whole warp's wait: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, uint64_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar), parity, limit));
+}
+
+template <int KV, int D>
+__global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
+    fd_rows_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap tmk,
+                   const __grid_constant__ CUtensorMap tmv) {
+    using Sh = RowsShape<KV, D>;
+    constexpr bool BF16 = KV == KV_BF16;
+    constexpr int HALVES = Sh::HALVES, NST = Sh::STAGES;
+    constexpr uint32_t TMEM_S = 0, TMEM_O = 256;  // columns: S (and P) of both tiles, then O
+    extern __shared__ __align__(1024) uint8_t smem[];
+    RowsControl &c = *reinterpret_cast<RowsControl *>(smem);
+    const uint32_t q_base = smem_u32(smem) + Sh::CONTROL, ring = q_base + 2 * Sh::TILE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t limit = p.timeout_ns;
+
+    if (smem_u32(smem) & 1023) {  // the swizzled tiles' alignment: the launch has no static shared memory
+        rows_flag(p.status, FD_DEV_TIMEOUT);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c.q_full[i]), 64);
+            mbar_init(smem_u32(&c.q_empty[i]), 1);
+            mbar_init(smem_u32(&c.s_full[i]), 1);
+            mbar_init(smem_u32(&c.p_full[i]), 4);
+            mbar_init(smem_u32(&c.pv_done[i]), 1);
+        }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(smem_u32(&c.item_full[i]), 1);
+            mbar_init(smem_u32(&c.item_empty[i]), 8 + 1 + 2);  // softmax warps, products, query loaders
+            mbar_init(smem_u32(&c.rows_full[i]), 64);
+        }
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(smem_u32(&c.kv_full[i]), 1);
+            mbar_init(smem_u32(&c.kv_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&c.drain), 1);
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(&c.tmem), 512);
+        tmem_relinquish();
+    }
+    if (warp == 9 && lane == 0) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = c.tmem;
+    // Only shared memory, tensor memory and parameters so far; what follows
+    // reads what the preceding grid may still be writing.
+    grid_dependency_wait();
+
+    // ---- Items of every segment, counted by all threads into the ring (not in
+    // use yet): the producer warp keeps their sums over 32 runs of segments.
+    const Segments seg{p};
+    const int nseg = seg.count();
+    int *scratch = reinterpret_cast<int *>(smem + Sh::CONTROL);  // offsets that rise, then items: nseg + 1 each
+    int *s_off = scratch, *s_items = scratch + nseg + 1;
+    if (p.offsets) {
+        // offsets made to rise within [0, seqs]: a running maximum, by one warp
+        if (warp == 0) {
+            int high = 0;
+            bool bad = __ldg(p.offsets) != 0;
+            for (int s0 = 0; s0 <= nseg; s0 += 32) {
+                const int s = s0 + lane;
+                const int raw = s <= nseg ? seg.raw_offset(s) : 0;
+                int v = min(max(raw, high), p.seqs);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v = max(v, t);
+                }
+                if (s <= nseg) {
+                    s_off[s] = v;
+                    bad |= v != raw;
+                }
+                high = __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (__any_sync(0xffffffffu, bad) && lane == 0) rows_flag(p.status, FD_DEV_BAD_PAGE);
+        }
+    } else {
+        for (int s = threadIdx.x; s <= nseg; s += Sh::THREADS) s_off[s] = s * p.beams;
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < nseg; s += Sh::THREADS) {
+        const int first = s_off[s], end = s_off[s + 1];
+        s_items[s] = seg.items(seg.tokens(first, end), seg.kv_len(s));
+        if (s < p.kv_rows) {
+            const int L = __ldg(p.kv_lens + s);
+            if (L < 0 || L > p.cap) rows_flag(p.status, FD_DEV_CAPACITY);
+        }
+        if (p.q_lens)
+            for (int b = first; b < end; ++b) {
+                const int n = __ldg(p.q_lens + b);
+                if (n < 0 || n > p.T) rows_flag(p.status, FD_DEV_CAPACITY);
+            }
+    }
+    __syncthreads();
+    // Run of segments of each lane of the producer warp: [lane * per, ...).
+    const int per = (nseg + 31) >> 5;
+    int run_items = 0, run_before = 0, run_off = 0, total = 0;
+    if (warp == 9) {
+        const int s0 = min(lane * per, nseg), s1 = min(s0 + per, nseg);
+        for (int s = s0; s < s1; ++s) run_items += s_items[s];
+        run_off = s_off[s0];
+        int incl = run_items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        run_before = incl - run_items;
+        total = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    fence_proxy_async_shared();
+    __syncthreads();  // the ring and Q tiles are free now
+
+    if (warp == 9) {
+        // ============================================================ producer
+        const int bsh = __ffs(p.boxr) - 1;  // boxr is a power of two
+        const int BPT = kTileTokens >> bsh;
+        const uint64_t policy = p.kv_once ? l2_policy_evict_first() : l2_policy_evict_normal();
+        uint32_t e = 0;        // ring entries issued
+        int n_item = 0;        // items published
+        bool ok = true;
+        int claim = (int)blockIdx.x;
+        if (p.stall_ns) {      // test hook: late loads
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < p.stall_ns) __nanosleep(1000);
+        }
+        while (true) {
+            const int slot = n_item % kItemSlots;
+            if (!warp_wait(c.item_empty[slot], ((n_item / kItemSlots) & 1) ^ 1, limit)) {
+                ok = false;
+                break;
+            }
+            RowsItem it;
+            it.seg = -1;
+            if (claim < total) {
+                // the lane's run that holds it, then the segment within the run
+                const unsigned has = __ballot_sync(0xffffffffu, run_before <= claim && claim < run_before + run_items);
+                const int src = __ffs(has) - 1;
+                int left = claim - __shfl_sync(0xffffffffu, run_before, src);
+                int high = __shfl_sync(0xffffffffu, run_off, src);
+                const int s_end = min((src + 1) * per, nseg);
+                for (int s0 = src * per;; s0 += 32) {
+                    const int s = s0 + lane;
+                    int first = 0, end = 0;
+                    if (p.offsets) {
+                        int v = s < s_end ? min(max(seg.raw_offset(s + 1), high), p.seqs) : 0;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int t = __shfl_up_sync(0xffffffffu, v, o);
+                            if (lane >= o) v = max(v, t);
+                        }
+                        end = v;
+                        const int before = __shfl_up_sync(0xffffffffu, v, 1);
+                        first = lane == 0 ? high : before;
+                        high = __shfl_sync(0xffffffffu, v, 31);
+                    } else {
+                        first = s * p.beams;
+                        end = first + p.beams;
+                    }
+                    const int len = s < s_end ? seg.kv_len(s) : 0;
+                    const int ntokens = s < s_end ? seg.tokens(first, end) : 0;
+                    const int n = s < s_end ? seg.items(ntokens, len) : 0;
+                    int incl = n;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += t;
+                    }
+                    const unsigned in = __ballot_sync(0xffffffffu, left < incl);
+                    if (!in && s0 + 32 < s_end) {
+                        left -= __shfl_sync(0xffffffffu, incl, 31);
+                        continue;
+                    }
+                    const int ln = in ? __ffs(in) - 1 : 31;
+                    // tile of rows fastest: the items that read the same K and V
+                    // run at the same time and meet them in L2
+                    const int L = __shfl_sync(0xffffffffu, len, ln);
+                    const int rows = __shfl_sync(0xffffffffu, ntokens, ln) * p.G;
+                    const int mt = max(1, (rows + 2 * kTileRows - 1) / (2 * kTileRows));
+                    int k = left - __shfl_sync(0xffffffffu, incl - n, ln);
+                    it.seg = s0 + ln;
+                    it.first = __shfl_sync(0xffffffffu, first, ln);
+                    it.row0 = (k % mt) * 2 * kTileRows;
+                    k /= mt;
+                    it.kvh = k % p.Hkv;
+                    it.split = k / p.Hkv;
+                    it.nsplit = L == 0 ? 1 : (L + p.chunk - 1) / p.chunk;
+                    it.nrows = min(2 * kTileRows, rows - it.row0);
+                    it.tok0 = it.split * p.chunk;
+                    it.ntok = min(L - it.tok0, p.chunk);
+                    break;
+                }
+            }
+            if (lane == 0) {
+                c.item[slot] = it;
+                mbar_arrive(smem_u32(&c.item_full[slot]));
+            }
+            __syncwarp();
+            ++n_item;
+            if (it.seg < 0) break;
+            int next = 0;
+            if (lane == 0) next = atomicAdd(p.counters, 1);
+            // K and V tiles in turn; page ids 32 boxes ahead
+            const int nbox = (it.ntok + p.boxr - 1) >> bsh;
+            const int *table = p.block_table + (size_t)it.seg * p.max_blocks;
+            auto page_of = [&](int k) -> int {
+                if (k >= nbox) return -1;
+                const int tok = it.tok0 + (k << bsh);
+                return __ldg(table + tok / p.page_size);
+            };
+            int pg_cur = it.ntok > 0 ? page_of(lane) : -1, pg_nxt = it.ntok > 0 ? page_of(32 + lane) : -1;
+            int batch = 0;
+            for (int k0 = 0; k0 < nbox && ok; k0 += BPT) {
+                if (k0 >= (batch + 1) * 32) {
+                    ++batch;
+                    pg_cur = pg_nxt;
+                    pg_nxt = page_of((batch + 1) * 32 + lane);
+                }
+                const int pg = __shfl_sync(0xffffffffu, pg_cur, (k0 + (lane & (BPT - 1))) & 31);
+                const bool live = lane < BPT && k0 + lane < nbox;
+                const bool good = live && pg >= 0 && pg < p.num_pages;
+                if (live && !good) rows_flag(p.status, FD_DEV_BAD_PAGE);
+                const unsigned mask = __ballot_sync(0xffffffffu, good);
+                const int at = (it.tok0 + ((k0 + lane) << bsh)) % p.page_size;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int st = e % NST;
+                    if (!warp_wait(c.kv_empty[st], ((e / NST) & 1) ^ 1, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&c.kv_full[st]);
+                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(mask) * p.boxr * D * 2);
+                    __syncwarp();
+                    if (good) {
+                        const uint32_t dst = ring + st * Sh::TILE + ((lane << bsh) * 128);
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_5d(dst + h * Sh::SPAN, kv ? &tmv : &tmk, fb, 0, at, h, it.kvh, pg, policy);
+                    }
+                    ++e;
+                }
+            }
+            claim = (int)gridDim.x + __shfl_sync(0xffffffffu, next, 0);
+            if (!ok) break;
+        }
+        grid_launch_dependents();
+        if (!ok && lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
+        // No copy may be in flight when the CTA ends: the latest entry of every stage.
+        for (uint32_t k = 1; k <= NST && k <= e; ++k)
+            if (!warp_wait(c.kv_full[(e - k) % NST], ((e - k) / NST) & 1, limit) && lane == 0)
+                rows_flag(p.status, FD_DEV_TIMEOUT);
+        // The last producer out resets the counters for the next launch.
+        if (lane == 0 && atom_add_acq_rel_gpu(p.counters + 1, 1) == (int)gridDim.x - 1) {
+            atomicExch(p.counters, 0);
+            atomicExch(p.counters + 1, 0);
+        }
+    } else if (warp >= 10) {
+        // ========================================================= query rows
+        const int t = threadIdx.x - 320;  // 0 .. 63
+        int n_item = 0;
+        uint32_t n_q[2] = {0, 0};         // tiles loaded
+        while (true) {
+            const int slot = n_item % kItemSlots;
+            if (!warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit)) {
+                rows_flag(p.status, FD_DEV_TIMEOUT);
+                break;
+            }
+            const RowsItem it = c.item[slot];
+            if (it.seg < 0) break;
+            int *tok = c.tok[slot];
+            for (int r = t; r < 2 * kTileRows; r += 64) {
+                int q = -1;
+                if (r < it.nrows) {
+                    int n = (it.row0 + r) / p.G;  // token of the segment
+                    if (p.q_lens) {
+                        int b = it.first;
+                        for (int len = seg.q_len(b); n >= len && b + 1 < p.seqs; len = seg.q_len(b)) {
+                            n -= len;
+                            ++b;
+                        }
+                        q = b * p.T + n;
+                    } else {
+                        const int i = it.first + n / p.T;
+                        const int b = p.members ? __ldg(p.members + i) : i;
+                        if (b >= 0 && b < p.seqs)
+                            q = b * p.T + n % p.T;
+                        else
+                            rows_flag(p.status, FD_DEV_BAD_PAGE);
+                    }
+                }
+                tok[r] = q;
+            }
+            mbar_arrive(smem_u32(&c.rows_full[slot]));
+            bool ok = warp_wait(c.rows_full[slot], (n_item / kItemSlots) & 1, limit);
+            if (!ok) rows_flag(p.status, FD_DEV_TIMEOUT);
+            for (int i = 0; i < 2 && ok; ++i) {
+                if (i * kTileRows >= it.nrows) break;
+                if (!warp_wait(c.q_empty[i], (n_q[i] & 1) ^ 1, limit)) {
+                    rows_flag(p.status, FD_DEV_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                if (it.ntok > 0) {
+                    constexpr int CH = D / 8;  // 16-byte pieces of a row
+                    const int ch = t % CH;
+                    const uint32_t dst = q_base + i * Sh::TILE + (ch / 8) * Sh::SPAN;
+#pragma unroll 8
+                    for (int r = t / CH; r < kTileRows; r += 64 / CH) {
+                        const int row = i * kTileRows + r, q = tok[row];
+                        const int h = it.kvh * p.G + (it.row0 + row) % p.G;
+                        const uint8_t *src = reinterpret_cast<const uint8_t *>(p.q) +
+                                             2 * (q < 0 ? 0 : (size_t)q * p.q_stride + (size_t)h * D + ch * 8);
+                        cp_async_16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, q >= 0);
+                    }
+                    cp_async_wait_all();
+                    fence_proxy_async_shared();
+                }
+                mbar_arrive(smem_u32(&c.q_full[i]));
+                ++n_q[i];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
+            ++n_item;
+            if (!ok) break;
+        }
+        cp_async_wait_all();
+    } else if (warp == 8) {
+        // ============================================================ products
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, BF16, false);
+            constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, BF16, true);
+            int n_item = 0;
+            uint32_t e = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint64_t &bar, uint32_t parity) {
+                if (ok && !mbar_wait_bounded(smem_u32(&bar), parity, limit)) {
+                    rows_flag(p.status, FD_DEV_TIMEOUT);
+                    ok = false;
+                }
+                return ok;
+            };
+            auto qk = [&](int i, uint32_t st) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * Sh::SPAN + (k % 4) * 32;
+                    mma_ss(tmem + TMEM_S + i * 128, smem_desc(q_base + i * Sh::TILE + off, 16, 1024),
+                           smem_desc(ring + st * Sh::TILE + off, 16, 1024), idesc_qk, k > 0);
+                }
+                mma_commit(smem_u32(&c.s_full[i]));
+            };
+            while (true) {
+                const int slot = n_item % kItemSlots;
+                if (!wait(c.item_full[slot], (n_item / kItemSlots) & 1)) break;
+                const int sg = c.item[slot].seg, nrows = c.item[slot].nrows, ntok = c.item[slot].ntok;
+                mbar_arrive(smem_u32(&c.item_empty[slot]));
+                ++n_item;
+                if (sg < 0) break;
+                const int tiles = nrows > kTileRows ? 2 : 1, nt = (ntok + kTileTokens - 1) / kTileTokens;
+                for (int i = 0; i < tiles; ++i) {
+                    if (!wait(c.q_full[i], n_q[i] & 1)) break;
+                    ++n_q[i];
+                    if (nt == 0) mbar_arrive(smem_u32(&c.q_empty[i]));
+                }
+                if (!ok) break;
+                if (nt == 0) continue;
+                if (!wait(c.kv_full[e % NST], (e / NST) & 1)) break;
+                tmem_fence_after();
+                for (int i = 0; i < tiles; ++i) qk(i, e % NST);
+                mma_commit(smem_u32(&c.kv_empty[e % NST]));
+                if (nt == 1)
+                    for (int i = 0; i < tiles; ++i) mma_commit(smem_u32(&c.q_empty[i]));
+                ++e;
+                for (int j = 0; j < nt && ok; ++j) {
+                    const uint32_t ev = e, ek = e + 1;
+                    const int steps = (min(kTileTokens, ntok - j * kTileTokens) + 15) / 16;
+                    if (!wait(c.kv_full[ev % NST], (ev / NST) & 1)) break;
+                    for (int i = 0; i < tiles; ++i) {
+                        if (!wait(c.p_full[i], n_p[i] & 1)) break;
+                        ++n_p[i];
+                        tmem_fence_after();
+                        const uint32_t vt = ring + (ev % NST) * Sh::TILE;
+                        for (int k = 0; k < steps; ++k)
+                            mma_ts(tmem + TMEM_O + i * 128, tmem + TMEM_S + i * 128 + k * 8,
+                                   smem_desc(vt + k * 2048, Sh::SPAN, 1024), idesc_pv, j > 0 || k > 0);
+                        mma_commit(smem_u32(&c.pv_done[i]));
+                        if (i == tiles - 1) mma_commit(smem_u32(&c.kv_empty[ev % NST]));
+                        if (j + 1 < nt) {
+                            if (i == 0 && !wait(c.kv_full[ek % NST], (ek / NST) & 1)) break;
+                            qk(i, ek % NST);
+                            if (i == tiles - 1) mma_commit(smem_u32(&c.kv_empty[ek % NST]));
+                            if (j + 2 == nt) mma_commit(smem_u32(&c.q_empty[i]));
+                        }
+                    }
+                    e += j + 1 < nt ? 2 : 1;
+                }
+                if (!ok) break;
+            }
+            // every product is complete before shared and tensor memory go
+            mma_commit(smem_u32(&c.drain));
+            ok = true;
+            wait(c.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ============================================================= softmax
+        const int i = warp >> 2;                           // tile
+        const int r = (warp & 3) * 32 + lane;              // row of the tile
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21; // first tensor-memory lane of the warp << 16
+        const uint32_t ts = tmem + lanes + TMEM_S + i * 128, to = tmem + lanes + TMEM_O + i * 128;
+        const float sc = p.scale_log2;
+        int n_item = 0;
+        uint32_t e = 0, n_s = 0;  // ring entries and score tiles so far
+        while (true) {
+            const int slot = n_item % kItemSlots;
+            if (!warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit)) {
+                rows_flag(p.status, FD_DEV_TIMEOUT);
+                break;
+            }
+            const RowsItem it = c.item[slot];
+            if (it.seg < 0) break;
+            const int nt = (it.ntok + kTileTokens - 1) / kTileTokens;
+            bool ok = true;
+            if (i * kTileRows < it.nrows) {
+                const bool warp_live = i * kTileRows + (warp & 3) * 32 < it.nrows;
+                float ref = -INFINITY, l = 0.f;
+                for (int j = 0; j < nt; ++j, ++n_s) {
+                    if (!warp_wait(c.s_full[i], n_s & 1, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const int nvalid = min(kTileTokens, it.ntok - j * kTileTokens);
+                    if (i == 0 && (nvalid & 15)) {
+                        // V rows behind the last token, up to the product's step of
+                        // 16: their weight is 0, but they may hold infinities or NaN.
+                        const uint32_t ev = e + 2 * j + 1;
+                        if (!warp_wait(c.kv_full[ev % NST], (ev / NST) & 1, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        const int z0 = nvalid, z1 = (nvalid + 15) & ~15;
+                        uint8_t *vt = smem + Sh::CONTROL + 2 * Sh::TILE + (ev % NST) * Sh::TILE;
+                        for (int x = r; x < (z1 - z0) * HALVES * 8; x += 128) {
+                            const int h = x / ((z1 - z0) * 8), y = x - h * (z1 - z0) * 8;
+                            *reinterpret_cast<uint4 *>(vt + h * Sh::SPAN + (z0 + y / 8) * 128 + (y % 8) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_shared();
+                    }
+                    if (warp_live) {
+                        tmem_fence_after();
+                        uint32_t s[128];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+                        if (nvalid < kTileTokens) {
+#pragma unroll
+                            for (int k = 0; k < 128; ++k)
+                                if (k >= nvalid) s[k] = 0xff800000u;  // -inf
+                        }
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                            const float now = fmaxf(ref, top);
+                            const float a = now == -INFINITY ? 1.f : ex2(ref - now);
+                            ref = now;
+                            l *= a;
+                            if (j > 0) {
+                                // O so far, once the product before this one is complete
+                                if (!warp_wait(c.pv_done[i], (n_s - 1) & 1, limit)) {
+                                    ok = false;
+                                } else {
+                                    tmem_fence_after();
+                                    for (int k = 0; k < D; k += 32) {
+                                        uint32_t o[32];
+                                        tmem_ld32(to + k, o);
+                                        tmem_wait_ld();
+                                        tmem_loaded32(o);
+#pragma unroll
+                                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
+                                        tmem_st32(to + k, o);
+                                    }
+                                    tmem_wait_st();
+                                }
+                            }
+                        }
+                        const float base = ref == -INFINITY ? 0.f : ref;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < 128; k += 2) {
+                            const float p0 = ex2(fmaf(__uint_as_float(s[k]), sc, -base));
+                            const float p1 = ex2(fmaf(__uint_as_float(s[k + 1]), sc, -base));
+                            sum[(k >> 1) & 3] += p0 + p1;
+                            s[k >> 1] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+                        }
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_st32(ts, s);
+                        tmem_st32(ts + 32, s + 32);
+                        tmem_wait_st();
+                    }
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&c.p_full[i]));
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                // ------------------------------------------------- the item's rows
+                if (ok && nt > 0) ok = warp_wait(c.pv_done[i], (n_s - 1) & 1, limit);
+                if (ok) ok = warp_wait(c.rows_full[slot], (n_item / kItemSlots) & 1, limit);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && warp_live) {
+                    tmem_fence_after();
+                    const int row = i * kTileRows + r;
+                    const int q = c.tok[slot][row];
+                    const int h = it.kvh * p.G + (it.row0 + row) % p.G;
+                    const size_t at = (size_t)(q < 0 ? 0 : q) * p.Hq + h;
+                    const bool empty = l == 0.f;  // no token, or every score -inf
+                    float mul = empty ? 0.f : 1.f / l, own = 0.f;
+                    if (it.nsplit > 1) {
+                        mul = 1.f;
+                        if (q >= 0) {
+                            p.part_m[at * p.S + it.split] = ref;
+                            p.part_d[at * p.S + it.split] = l;
+                            if (it.split == 0) p.row_splits[at] = it.nsplit;
+                        }
+                    } else if (q >= 0) {
+                        float lse = empty ? -INFINITY : (ref + __log2f(l)) * kRowsLn2;
+                        if (p.own_out) {
+                            const float lo = p.own_lse[at], m = fmaxf(lse, lo);
+                            const float wa = lse == -INFINITY ? 0.f : __expf(lse - m), wb = lo == -INFINITY ? 0.f : __expf(lo - m);
+                            const float inv = wa + wb > 0.f ? 1.f / (wa + wb) : 0.f;
+                            mul *= wa * inv;
+                            own = wb * inv;
+                            lse = m == -INFINITY ? -INFINITY : m + logf(wa + wb);
+                        }
+                        if (p.lse) p.lse[at] = lse;
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        if (nt > 0) {
+                            tmem_ld32(to + k, o);
+                            tmem_wait_ld();
+                            tmem_loaded32(o);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = 0u;
+                        }
+                        if (q >= 0 && it.nsplit > 1) {
+                            float *dst = p.part_o + (at * p.S + it.split) * D + k;
+#pragma unroll
+                            for (int x = 0; x < 32; x += 4)
+                                *reinterpret_cast<uint4 *>(dst + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                        } else if (q >= 0) {
+                            float y[32];
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) y[x] = empty ? 0.f : __uint_as_float(o[x]) * mul;
+                            if (p.own_out) {
+                                const float4 *src = reinterpret_cast<const float4 *>(p.own_out + at * D + k);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) {
+                                    const float4 f = __ldcg(src + x);
+                                    y[4 * x] = fmaf(f.x, own, y[4 * x]);
+                                    y[4 * x + 1] = fmaf(f.y, own, y[4 * x + 1]);
+                                    y[4 * x + 2] = fmaf(f.z, own, y[4 * x + 2]);
+                                    y[4 * x + 3] = fmaf(f.w, own, y[4 * x + 3]);
+                                }
+                            }
+                            uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + at * D + k;
+#pragma unroll
+                            for (int x = 0; x < 32; x += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    w[z] = BF16 ? pack_bf16x2(y[x + 2 * z], y[x + 2 * z + 1])
+                                                : pack_f16x2(y[x + 2 * z], y[x + 2 * z + 1]);
+                                *reinterpret_cast<uint4 *>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    tmem_fence_before();
+                }
+                if (!ok) {
+                    if (lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
+                    break;
+                }
+            }
+            e += 2 * nt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
+            ++n_item;
+        }
+        tmem_fence_before();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace fd
