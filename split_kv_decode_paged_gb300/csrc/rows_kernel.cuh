@@ -60,6 +60,9 @@ struct RowsShape {
     static constexpr int SPAN = kTileTokens * 128;          // bytes of one half of it
     static constexpr int STAGES = D == 128 ? 5 : 10;
     static constexpr int THREADS = 384;
+    // 65536 registers / 384 threads: 168 each at launch, then dealt out anew
+    static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
+    static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 168, "the launch's registers");
     // shared memory: control block, two Q tiles, the ring
     static constexpr int CONTROL = 3072;
     static constexpr int SMEM = CONTROL + 2 * TILE + STAGES * TILE;
@@ -243,6 +246,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     fence_proxy_async_shared();
     __syncthreads();  // the ring and Q tiles are free now
 
+    if (warp >= 8) {
+    regs_down<Sh::REGS_OTHER>();
     if (warp == 9) {
         // ============================================================ producer
         const int bsh = __ffs(p.boxr) - 1;  // boxr is a power of two
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     constexpr int CH = D / 8;  // 16-byte pieces of a row
                     const int ch = t % CH;
                     const uint32_t dst = q_base + i * Sh::TILE + (ch / 8) * Sh::SPAN;
-#pragma unroll 8
+#pragma unroll 4
                     for (int r = t / CH; r < kTileRows; r += 64 / CH) {
                         const int row = i * kTileRows + r, q = tok[row];
                         const int h = it.kvh * p.G + (it.row0 + row) % p.G;
@@ -534,8 +539,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             wait(c.drain, 0);
         }
         __syncwarp();
+    }
     } else {
         // ============================================================= softmax
+        regs_up<Sh::REGS_SOFTMAX>();
         const int i = warp >> 2;                           // tile
         const int r = (warp & 3) * 32 + lane;              // row of the tile
         const uint32_t lanes = (uint32_t)(warp & 3) << 21; // first tensor-memory lane of the warp << 16
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) tmem_loaded32(s + 32 * k);
+                        for (int k = 0; k < 4; ++k) tmem_loaded<32>(s + 32 * k);
                         if (nvalid < kTileTokens) {
 #pragma unroll
                             for (int k = 0; k < 128; ++k)
@@ -594,7 +601,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         }
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
+                        for (int k = 0; k < 128; k += 2)
+                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
                             const float now = fmaxf(ref, top);
@@ -607,29 +615,35 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                     ok = false;
                                 } else {
                                     tmem_fence_after();
-                                    for (int k = 0; k < D; k += 32) {
-                                        uint32_t o[32];
-                                        tmem_ld32(to + k, o);
+#pragma unroll 1
+                                    for (int k = 0; k < D; k += 8) {
+                                        uint32_t o[8];
+                                        tmem_ld8(to + k, o);
                                         tmem_wait_ld();
-                                        tmem_loaded32(o);
+                                        tmem_loaded<8>(o);
 #pragma unroll
-                                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
-                                        tmem_st32(to + k, o);
+                                        for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
+                                        tmem_st8(to + k, o);
                                     }
                                     tmem_wait_st();
                                 }
                             }
                         }
                         const float base = ref == -INFINITY ? 0.f : ref;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        const uint64_t sc2 = pair(sc, sc), base2 = pair(-base, -base);
+                        uint64_t sum[2] = {0, 0};
 #pragma unroll
                         for (int k = 0; k < 128; k += 2) {
-                            const float p0 = ex2(fmaf(__uint_as_float(s[k]), sc, -base));
-                            const float p1 = ex2(fmaf(__uint_as_float(s[k + 1]), sc, -base));
-                            sum[(k >> 1) & 3] += p0 + p1;
-                            s[k >> 1] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+                            float x0, x1;
+                            unpair(fma2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, base2), x0, x1);
+                            x0 = ex2(x0);
+                            x1 = ex2(x1);
+                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(x0, x1));
+                            s[k >> 1] = BF16 ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        float l0, l1;
+                        unpair(add2(sum[0], sum[1]), l0, l1);
+                        l += l0 + l1;
                         tmem_st32(ts, s);
                         tmem_st32(ts + 32, s + 32);
                         tmem_wait_st();
@@ -679,7 +693,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         if (nt > 0) {
                             tmem_ld32(to + k, o);
                             tmem_wait_ld();
-                            tmem_loaded32(o);
+                            tmem_loaded<32>(o);
                         } else {
 #pragma unroll
                             for (int x = 0; x < 32; ++x) o[x] = 0u;
