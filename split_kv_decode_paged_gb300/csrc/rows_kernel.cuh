@@ -122,9 +122,18 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool 
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// A whole warp's wait: the same answer in every lane.
+// A whole warp's wait, for at most limit nanoseconds: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, uint64_t limit) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar), parity, limit));
+    const uint32_t at = smem_u32(&bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    bool late = false;
+#pragma unroll 1
+    while (!late) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+        late = __any_sync(0xffffffffu, global_timer_ns() - t0 > limit);
+    }
+    return false;
 }
 
 template <int KV, int D>
@@ -464,81 +473,120 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         cp_async_wait_all();
     } else if (warp == 8) {
         // ============================================================ products
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, BF16, false);
-            constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, BF16, true);
-            int n_item = 0;
-            uint32_t e = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-            bool ok = true;
-            auto wait = [&](uint64_t &bar, uint32_t parity) {
-                if (ok && !mbar_wait_bounded(smem_u32(&bar), parity, limit)) {
-                    rows_flag(p.status, FD_DEV_TIMEOUT);
-                    ok = false;
-                }
-                return ok;
-            };
-            auto qk = [&](int i, uint32_t st) {
+        // The whole warp goes round, so that descriptors and addresses stay in
+        // uniform registers; one lane issues.
+        constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, BF16, false);
+        constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, BF16, true);
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t q_desc = smem_desc(q_base, 16, 1024), k_desc = smem_desc(ring, 16, 1024);
+        const uint64_t v_desc = smem_desc(ring, Sh::SPAN, 1024);
+        int n_item = 0;
+        uint32_t st = 0, par = 0;  // ring stage and parity of the next entry
+        uint32_t n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0;
+        bool ok = true;
+        auto next = [&]() {
+            if (++st == NST) {
+                st = 0;
+                par ^= 1;
+            }
+        };
+        auto qk = [&](int i, uint32_t stage) {
+            const uint64_t a0 = q_desc + (uint64_t)(i * (Sh::TILE >> 4)), b0 = k_desc + (uint64_t)(stage * (Sh::TILE >> 4));
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * Sh::SPAN + (k % 4) * 32;
-                    mma_ss(tmem + TMEM_S + i * 128, smem_desc(q_base + i * Sh::TILE + off, 16, 1024),
-                           smem_desc(ring + st * Sh::TILE + off, 16, 1024), idesc_qk, k > 0);
+                    const uint32_t off = ((k / 4) * Sh::SPAN + (k % 4) * 32) >> 4;
+                    mma_ss(tm + TMEM_S + i * 128, a0 + off, b0 + off, idesc_qk, k > 0);
                 }
                 mma_commit(smem_u32(&c.s_full[i]));
-            };
-            while (true) {
-                const int slot = n_item % kItemSlots;
-                if (!wait(c.item_full[slot], (n_item / kItemSlots) & 1)) break;
-                const int sg = c.item[slot].seg, nrows = c.item[slot].nrows, ntok = c.item[slot].ntok;
-                mbar_arrive(smem_u32(&c.item_empty[slot]));
-                ++n_item;
-                if (sg < 0) break;
-                const int tiles = nrows > kTileRows ? 2 : 1, nt = (ntok + kTileTokens - 1) / kTileTokens;
-                for (int i = 0; i < tiles; ++i) {
-                    if (!wait(c.q_full[i], n_q[i] & 1)) break;
-                    ++n_q[i];
-                    if (nt == 0) mbar_arrive(smem_u32(&c.q_empty[i]));
-                }
-                if (!ok) break;
-                if (nt == 0) continue;
-                if (!wait(c.kv_full[e % NST], (e / NST) & 1)) break;
-                tmem_fence_after();
-                for (int i = 0; i < tiles; ++i) qk(i, e % NST);
-                mma_commit(smem_u32(&c.kv_empty[e % NST]));
-                if (nt == 1)
-                    for (int i = 0; i < tiles; ++i) mma_commit(smem_u32(&c.q_empty[i]));
-                ++e;
-                for (int j = 0; j < nt && ok; ++j) {
-                    const uint32_t ev = e, ek = e + 1;
-                    const int steps = (min(kTileTokens, ntok - j * kTileTokens) + 15) / 16;
-                    if (!wait(c.kv_full[ev % NST], (ev / NST) & 1)) break;
-                    for (int i = 0; i < tiles; ++i) {
-                        if (!wait(c.p_full[i], n_p[i] & 1)) break;
-                        ++n_p[i];
-                        tmem_fence_after();
-                        const uint32_t vt = ring + (ev % NST) * Sh::TILE;
-                        for (int k = 0; k < steps; ++k)
-                            mma_ts(tmem + TMEM_O + i * 128, tmem + TMEM_S + i * 128 + k * 8,
-                                   smem_desc(vt + k * 2048, Sh::SPAN, 1024), idesc_pv, j > 0 || k > 0);
-                        mma_commit(smem_u32(&c.pv_done[i]));
-                        if (i == tiles - 1) mma_commit(smem_u32(&c.kv_empty[ev % NST]));
-                        if (j + 1 < nt) {
-                            if (i == 0 && !wait(c.kv_full[ek % NST], (ek / NST) & 1)) break;
-                            qk(i, ek % NST);
-                            if (i == tiles - 1) mma_commit(smem_u32(&c.kv_empty[ek % NST]));
-                            if (j + 2 == nt) mma_commit(smem_u32(&c.q_empty[i]));
-                        }
-                    }
-                    e += j + 1 < nt ? 2 : 1;
-                }
-                if (!ok) break;
             }
-            // every product is complete before shared and tensor memory go
-            mma_commit(smem_u32(&c.drain));
-            ok = true;
-            wait(c.drain, 0);
+        };
+        auto pv = [&](int i, uint32_t stage, int steps, bool more) {
+            const uint64_t b0 = v_desc + (uint64_t)(stage * (Sh::TILE >> 4));
+            const uint32_t d = tm + TMEM_O + i * 128, a0 = tm + TMEM_S + i * 128;
+            if (leader) {
+                if (steps == kTileTokens / 16) {
+#pragma unroll
+                    for (int k = 0; k < kTileTokens / 16; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
+                } else {
+                    for (int k = 0; k < steps; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
+                }
+                mma_commit(smem_u32(&c.pv_done[i]));
+            }
+        };
+        auto release = [&](uint64_t &bar) {
+            if (leader) mma_commit(smem_u32(&bar));
+        };
+        while (ok) {
+            const int slot = n_item % kItemSlots;
+            if (!(ok = warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit))) break;
+            const int sg = __shfl_sync(0xffffffffu, c.item[slot].seg, 0);
+            const int nrows = __shfl_sync(0xffffffffu, c.item[slot].nrows, 0);
+            const int ntok = __shfl_sync(0xffffffffu, c.item[slot].ntok, 0);
+            if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
+            ++n_item;
+            if (sg < 0) break;
+            const bool two = nrows > kTileRows;
+            const int nt = (ntok + kTileTokens - 1) / kTileTokens;
+            if (!(ok = warp_wait(c.q_full[0], n_q0++ & 1, limit))) break;
+            if (two && !(ok = warp_wait(c.q_full[1], n_q1++ & 1, limit))) break;
+            if (nt == 0) {
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&c.q_empty[0]));
+                    if (two) mbar_arrive(smem_u32(&c.q_empty[1]));
+                }
+                __syncwarp();
+                continue;
+            }
+            if (!(ok = warp_wait(c.kv_full[st], par, limit))) break;
+            tmem_fence_after();
+            qk(0, st);
+            if (two) qk(1, st);
+            release(c.kv_empty[st]);
+            if (nt == 1) {
+                release(c.q_empty[0]);
+                if (two) release(c.q_empty[1]);
+            }
+            next();
+            for (int j = 0; j < nt; ++j) {
+                const uint32_t sv = st;
+                const bool more = j + 1 < nt;
+                if (!(ok = warp_wait(c.kv_full[sv], par, limit))) break;
+                next();
+                const uint32_t sk = st;
+                if (more) {
+                    if (!(ok = warp_wait(c.kv_full[sk], par, limit))) break;
+                    next();
+                }
+                const int steps = more ? kTileTokens / 16 : (ntok - j * kTileTokens + 15) / 16;
+                if (!(ok = warp_wait(c.p_full[0], n_p0++ & 1, limit))) break;
+                tmem_fence_after();
+                pv(0, sv, steps, j > 0);
+                if (more) qk(0, sk);
+                if (two) {
+                    if (!(ok = warp_wait(c.p_full[1], n_p1++ & 1, limit))) break;
+                    tmem_fence_after();
+                    pv(1, sv, steps, j > 0);
+                    release(c.kv_empty[sv]);
+                    if (more) {
+                        qk(1, sk);
+                        release(c.kv_empty[sk]);
+                    }
+                } else {
+                    release(c.kv_empty[sv]);
+                    if (more) release(c.kv_empty[sk]);
+                }
+                if (j + 2 == nt) {
+                    release(c.q_empty[0]);
+                    if (two) release(c.q_empty[1]);
+                }
+            }
         }
-        __syncwarp();
+        if (!ok && lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
+        // every product is complete before shared and tensor memory go
+        release(c.drain);
+        if (!warp_wait(c.drain, 0, limit) && lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
     }
     } else {
         // ============================================================= softmax
