@@ -37,6 +37,7 @@ namespace fd {
 constexpr int kTileTokens = 128;
 constexpr int kTileRows = 128;   // query rows of one tile; two tiles an item
 constexpr int kItemSlots = 2;
+constexpr int kPartTokens = 96;  // weights handed to the product with V before the rest
 constexpr float kRowsLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;    // log2 headroom of the softmax reference
 
@@ -70,7 +71,7 @@ struct RowsShape {
 };
 
 struct RowsControl {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], pv_done[2];
     uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full[kItemSlots];
     uint64_t kv_full[10], kv_empty[10];
     uint64_t drain;
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             mbar_init(smem_u32(&c.q_full[i]), 64);
             mbar_init(smem_u32(&c.q_empty[i]), 1);
             mbar_init(smem_u32(&c.s_full[i]), 1);
+            mbar_init(smem_u32(&c.p_part[i]), 4);
             mbar_init(smem_u32(&c.p_full[i]), 4);
             mbar_init(smem_u32(&c.pv_done[i]), 1);
         }
@@ -502,18 +504,29 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 mma_commit(smem_u32(&c.s_full[i]));
             }
         };
-        auto pv = [&](int i, uint32_t stage, int steps, bool more) {
+        auto pv = [&](int i, uint32_t stage, int k0, int k1, bool more) {
             const uint64_t b0 = v_desc + (uint64_t)(stage * (Sh::TILE >> 4));
             const uint32_t d = tm + TMEM_O + i * 128, a0 = tm + TMEM_S + i * 128;
             if (leader) {
-                if (steps == kTileTokens / 16) {
+                if (k1 - k0 == kPartTokens / 16) {
 #pragma unroll
-                    for (int k = 0; k < kTileTokens / 16; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
+                    for (int k = 0; k < kPartTokens / 16; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
                 } else {
-                    for (int k = 0; k < steps; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
+                    for (int k = k0; k < k1; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
                 }
-                mma_commit(smem_u32(&c.pv_done[i]));
             }
+        };
+        // O += P V of one tile: the first part of the weights, then the rest
+        auto output = [&](int i, uint32_t stage, int steps, bool more, uint32_t phase) {
+            constexpr int part = kPartTokens / 16;
+            if (!warp_wait(c.p_part[i], phase & 1, limit)) return false;
+            tmem_fence_after();
+            pv(i, stage, 0, min(steps, part), more);
+            if (!warp_wait(c.p_full[i], phase & 1, limit)) return false;
+            tmem_fence_after();
+            if (steps > part) pv(i, stage, part, steps, true);
+            if (leader) mma_commit(smem_u32(&c.pv_done[i]));
+            return true;
         };
         auto release = [&](uint64_t &bar) {
             if (leader) mma_commit(smem_u32(&bar));
@@ -549,25 +562,30 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 if (two) release(c.q_empty[1]);
             }
             next();
+            // V of a tile and K of the next one: looked for as the tile before
+            // them is issued, so that the look costs nothing.
+            bool v_here = false, k_here = false;
             for (int j = 0; j < nt; ++j) {
                 const uint32_t sv = st;
                 const bool more = j + 1 < nt;
-                if (!(ok = warp_wait(c.kv_full[sv], par, limit))) break;
+                if (!__all_sync(0xffffffffu, v_here) && !(ok = warp_wait(c.kv_full[sv], par, limit))) break;
                 next();
                 const uint32_t sk = st;
                 if (more) {
-                    if (!(ok = warp_wait(c.kv_full[sk], par, limit))) break;
+                    if (!__all_sync(0xffffffffu, k_here) && !(ok = warp_wait(c.kv_full[sk], par, limit))) break;
                     next();
                 }
                 const int steps = more ? kTileTokens / 16 : (ntok - j * kTileTokens + 15) / 16;
-                if (!(ok = warp_wait(c.p_full[0], n_p0++ & 1, limit))) break;
-                tmem_fence_after();
-                pv(0, sv, steps, j > 0);
+                if (!(ok = output(0, sv, steps, j > 0, n_p0++))) break;
                 if (more) qk(0, sk);
+                v_here = k_here = false;
+                if (more) {
+                    v_here = mbar_try_wait(smem_u32(&c.kv_full[st]), par);
+                    const uint32_t s2 = st + 1 == NST ? 0 : st + 1;
+                    if (j + 2 < nt) k_here = mbar_try_wait(smem_u32(&c.kv_full[s2]), s2 ? par : par ^ 1);
+                }
                 if (two) {
-                    if (!(ok = warp_wait(c.p_full[1], n_p1++ & 1, limit))) break;
-                    tmem_fence_after();
-                    pv(1, sv, steps, j > 0);
+                    if (!(ok = output(1, sv, steps, j > 0, n_p1++))) break;
                     release(c.kv_empty[sv]);
                     if (more) {
                         qk(1, sk);
@@ -637,20 +655,23 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     if (warp_live) {
                         tmem_fence_after();
                         uint32_t s[128];
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto highest = [&](int k0) {  // of 64 scores, masked behind the last token
+                            if (nvalid < kTileTokens) {
+#pragma unroll
+                                for (int k = k0; k < k0 + 64; ++k)
+                                    if (k >= nvalid) s[k] = 0xff800000u;  // -inf
+                            }
+#pragma unroll
+                            for (int k = k0; k < k0 + 64; k += 2)
+                                mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                        };
 #pragma unroll
                         for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
                         tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) tmem_loaded<32>(s + 32 * k);
-                        if (nvalid < kTileTokens) {
-#pragma unroll
-                            for (int k = 0; k < 128; ++k)
-                                if (k >= nvalid) s[k] = 0xff800000u;  // -inf
-                        }
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int k = 0; k < 128; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                        tmem_loaded<128>(s);
+                        highest(0);
+                        highest(64);
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
                             const float now = fmaxf(ref, top);
@@ -680,21 +701,34 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         const float base = ref == -INFINITY ? 0.f : ref;
                         const uint64_t sc2 = pair(sc, sc), base2 = pair(-base, -base);
                         uint64_t sum[2] = {0, 0};
+                        auto weights = [&](int k0, int k1) {
 #pragma unroll
-                        for (int k = 0; k < 128; k += 2) {
-                            float x0, x1;
-                            unpair(fma2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, base2), x0, x1);
-                            x0 = ex2(x0);
-                            x1 = ex2(x1);
-                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(x0, x1));
-                            s[k >> 1] = BF16 ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
-                        }
+                            for (int k = k0; k < k1; k += 2) {
+                                float x0, x1;
+                                unpair(fma2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, base2), x0, x1);
+                                x0 = ex2(x0);
+                                x1 = ex2(x1);
+                                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(x0, x1));
+                                s[k >> 1] = BF16 ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+                            }
+                        };
+                        // The product with V starts on the first part while the
+                        // rest is worked out.
+                        weights(0, kPartTokens);
+                        tmem_st32(ts, s);
+                        tmem_st16(ts + 32, s + 32);
+                        tmem_wait_st();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&c.p_part[i]));
+                        weights(kPartTokens, kTileTokens);
+                        tmem_st16(ts + 48, s + 48);
                         float l0, l1;
                         unpair(add2(sum[0], sum[1]), l0, l1);
                         l += l0 + l1;
-                        tmem_st32(ts, s);
-                        tmem_st32(ts + 32, s + 32);
                         tmem_wait_st();
+                    } else if (lane == 0) {
+                        mbar_arrive(smem_u32(&c.p_part[i]));
                     }
                     tmem_fence_before();
                     __syncwarp();
