@@ -301,7 +301,9 @@ bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p
     cuuint32_t box[5] = {(cuuint32_t)(span / e), (cuuint32_t)boxr, (cuuint32_t)(one_span ? 1 : nspan), 1u, 1u};
     cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
     const CUtensorMapDataType dt = e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    const CUtensorMapSwizzle sw = span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapSwizzle sw = one_span && e == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                  : span == 128      ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                     : CU_TENSOR_MAP_SWIZZLE_64B;
     // L2 promotion no wider than one row: a wider promotion also fetches the
     // neighbouring KV head's row, which another CTA reads at another time.
     const CUtensorMapL2promotion l2p = rb >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B

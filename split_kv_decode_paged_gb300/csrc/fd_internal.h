@@ -222,7 +222,8 @@ struct DeviceInfo {
 fd_status device_info(DeviceInfo &di);
 fd_status validate_problem(const fd_problem *p);
 // Tensor map of a K or V pool with boxes of boxr token rows of one KV head: all
-// 128-byte spans of a row, one after the other, or one of them.
+// 128-byte spans of a row, one after the other, or one of them (E4M3: its whole
+// row, unswizzled).
 bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool one_span = false);
 
 cudaError_t launch_merge_two(const float *oa, const float *la, const float *ob, const float *lb, int rows, int D,

@@ -22,6 +22,11 @@
 //   warp 9          claims items, loads K and V tiles by TMA into a ring
 //   warps 10-11     gather the query rows (any sequence, token and head order,
 //                   any token stride) into swizzled shared memory
+//   warps 12-15     (E4M3 pools) turn the loaded codes into 16-bit tiles
+// E4M3: codes of K become values of q's type and those of V bf16, exactly; K's
+// scale (one a page and KV head) multiplies the scores, V's the weights, before
+// their one rounding to bf16 (with f16 queries a pair of bf16, two products, so
+// that the output keeps f16's precision whatever the scales' range).
 // Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
 // leaves the loop, which ends the others' waits the same way.
 #pragma once
@@ -56,29 +61,39 @@ struct RowsItem {
 
 template <int KV, int D>
 struct RowsShape {
+    static constexpr bool FP8 = KV == KV_E4M3;
     static constexpr int HALVES = D / 64;                   // 128-byte spans of a row
     static constexpr int TILE = kTileTokens * D * 2;        // bytes of a Q, K or V tile (16 bits)
     static constexpr int SPAN = kTileTokens * 128;          // bytes of one half of it
-    static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr int THREADS = 384;
-    // 65536 registers / 384 threads: 168 each at launch, then dealt out anew
-    static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
-    static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 168, "the launch's registers");
-    // shared memory: control block, two Q tiles, the ring
+    static constexpr int RAW = FP8 ? kTileTokens * D : 0;   // bytes of a tile of codes
+    // stages of 16-bit K and V tiles, and of codes
+    static constexpr int STAGES = (FP8 ? 3 : 5) * (128 / D);
+    static constexpr int RAW_STAGES = FP8 ? 4 * (128 / D) : 0;
+    static constexpr int LOADS = FP8 ? RAW_STAGES : STAGES; // what TMA fills
+    static constexpr int THREADS = FP8 ? 512 : 384;
+    // 65536 registers dealt out evenly at launch, then anew
+    static constexpr int REGS_LAUNCH = FP8 ? 128 : 168;
+    static constexpr int REGS_SOFTMAX = FP8 ? 184 : 208, REGS_OTHER = FP8 ? 72 : 88;
+    static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
+    // shared memory: control block, two Q tiles, the rings
     static constexpr int CONTROL = 3072;
-    static constexpr int SMEM = CONTROL + 2 * TILE + STAGES * TILE;
+    static constexpr int RING = CONTROL + 2 * TILE, RAW_RING = RING + STAGES * TILE;
+    static constexpr int SMEM = RAW_RING + RAW_STAGES * RAW;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 struct RowsControl {
     uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], pv_done[2];
-    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full[kItemSlots];
-    uint64_t kv_full[10], kv_empty[10];
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full, rows_empty;
+    uint64_t kv_full[10], kv_empty[10];    // 16-bit tiles
+    uint64_t raw_full[8], raw_empty[8];    // tiles of codes
     uint64_t drain;
     uint32_t tmem;
     int pad;
     RowsItem item[kItemSlots];
-    int tok[kItemSlots][2 * kTileRows];  // q token (sequence * T + token) of every row, -1 past the end
+    int tok[2 * kTileRows];    // q token (sequence * T + token) of every row of the item, -1 past the end
+    float raw_scale[8][16];    // of a stage's groups of 16 tokens: K's, then V's
+    float scale[6][16];
 };
 static_assert(sizeof(RowsControl) <= 3072, "the control block's room");
 
@@ -137,17 +152,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, uint64
     return false;
 }
 
-template <int KV, int D>
+template <int KV, int D, bool QBF16>
 __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     fd_rows_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv) {
     using Sh = RowsShape<KV, D>;
-    constexpr bool BF16 = KV == KV_BF16;
+    constexpr bool FP8 = Sh::FP8;
+    constexpr bool P16 = KV == KV_F16;     // the product with V in f16 (else bf16)
+    constexpr bool PAIR = FP8 && !QBF16;   // weights as pairs of bf16
+    static_assert(FP8 || QBF16 == (KV == KV_BF16), "16-bit pools have q's type");
     constexpr int HALVES = Sh::HALVES, NST = Sh::STAGES;
     constexpr uint32_t TMEM_S = 0, TMEM_O = 256;  // columns: S (and P) of both tiles, then O
     extern __shared__ __align__(1024) uint8_t smem[];
     RowsControl &c = *reinterpret_cast<RowsControl *>(smem);
-    const uint32_t q_base = smem_u32(smem) + Sh::CONTROL, ring = q_base + 2 * Sh::TILE;
+    const uint32_t q_base = smem_u32(smem) + Sh::CONTROL, ring = smem_u32(smem) + Sh::RING;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.timeout_ns;
 
@@ -166,12 +184,17 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         }
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(smem_u32(&c.item_full[i]), 1);
-            mbar_init(smem_u32(&c.item_empty[i]), 8 + 1 + 2);  // softmax warps, products, query loaders
-            mbar_init(smem_u32(&c.rows_full[i]), 64);
+            mbar_init(smem_u32(&c.item_empty[i]), 8 + 1 + 2 + (FP8 ? 4 : 0));  // all warps but the producer's
         }
+        mbar_init(smem_u32(&c.rows_full), 64);
+        mbar_init(smem_u32(&c.rows_empty), 8);
         for (int i = 0; i < NST; ++i) {
-            mbar_init(smem_u32(&c.kv_full[i]), 1);
+            mbar_init(smem_u32(&c.kv_full[i]), FP8 ? 4 : 1);
             mbar_init(smem_u32(&c.kv_empty[i]), 1);
+        }
+        for (int i = 0; i < Sh::RAW_STAGES; ++i) {
+            mbar_init(smem_u32(&c.raw_full[i]), 1);
+            mbar_init(smem_u32(&c.raw_empty[i]), 4);
         }
         mbar_init(smem_u32(&c.drain), 1);
         fence_barrier_init();
@@ -370,21 +393,45 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 if (live && !good) rows_flag(p.status, FD_DEV_BAD_PAGE);
                 const unsigned mask = __ballot_sync(0xffffffffu, good);
                 const int at = (it.tok0 + ((k0 + lane) << bsh)) % p.page_size;
+                // the page of this lane's group of 16 tokens, for the scales
+                const int box = (lane & 7) >> (bsh - 4);
+                [[maybe_unused]] const int pg16 = __shfl_sync(0xffffffffu, good ? pg : -1, box);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int st = e % NST;
-                    if (!warp_wait(c.kv_empty[st], ((e / NST) & 1) ^ 1, limit)) {
+                    const int st = e % Sh::LOADS;
+                    uint64_t &full = FP8 ? c.raw_full[st] : c.kv_full[st];
+                    if (!warp_wait(FP8 ? c.raw_empty[st] : c.kv_empty[st], ((e / Sh::LOADS) & 1) ^ 1, limit)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = smem_u32(&c.kv_full[st]);
-                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(mask) * p.boxr * D * 2);
+                    const uint32_t fb = smem_u32(&full);
+                    if constexpr (FP8) {
+                        // both scales of every group with V's codes; the stage's
+                        // barrier also waits for them
+                        if (kv == 1 && lane < 8) {
+                            float *ks = &c.raw_scale[st][lane], *vs = ks + 8;
+                            if (pg16 >= 0) {
+                                cp_async_4(smem_u32(ks), p.k_scale + (size_t)pg16 * p.Hkv + it.kvh);
+                                cp_async_4(smem_u32(vs), p.v_scale + (size_t)pg16 * p.Hkv + it.kvh);
+                                cp_async_mbar_arrive(fb);
+                            } else {
+                                *ks = *vs = 1.f;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(mask) * p.boxr * D * (FP8 ? 1 : 2));
                     __syncwarp();
                     if (good) {
-                        const uint32_t dst = ring + st * Sh::TILE + ((lane << bsh) * 128);
+                        if constexpr (FP8) {
+                            const uint32_t dst = smem_u32(smem) + Sh::RAW_RING + st * Sh::RAW + (lane << bsh) * D;
+                            tma_load_5d(dst, kv ? &tmv : &tmk, fb, 0, at, 0, it.kvh, pg, policy);
+                        } else {
+                            const uint32_t dst = ring + st * Sh::TILE + ((lane << bsh) * 128);
 #pragma unroll
-                        for (int h = 0; h < HALVES; ++h)
-                            tma_load_5d(dst + h * Sh::SPAN, kv ? &tmv : &tmk, fb, 0, at, h, it.kvh, pg, policy);
+                            for (int h = 0; h < HALVES; ++h)
+                                tma_load_5d(dst + h * Sh::SPAN, kv ? &tmv : &tmk, fb, 0, at, h, it.kvh, pg, policy);
+                        }
                     }
                     ++e;
                 }
@@ -395,13 +442,78 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         grid_launch_dependents();
         if (!ok && lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
         // No copy may be in flight when the CTA ends: the latest entry of every stage.
-        for (uint32_t k = 1; k <= NST && k <= e; ++k)
-            if (!warp_wait(c.kv_full[(e - k) % NST], ((e - k) / NST) & 1, limit) && lane == 0)
+        for (uint32_t k = 1; k <= Sh::LOADS && k <= e; ++k) {
+            const uint32_t st = (e - k) % Sh::LOADS;
+            if (!warp_wait(FP8 ? c.raw_full[st] : c.kv_full[st], ((e - k) / Sh::LOADS) & 1, limit) && lane == 0)
                 rows_flag(p.status, FD_DEV_TIMEOUT);
+        }
         // The last producer out resets the counters for the next launch.
         if (lane == 0 && atom_add_acq_rel_gpu(p.counters + 1, 1) == (int)gridDim.x - 1) {
             atomicExch(p.counters, 0);
             atomicExch(p.counters + 1, 0);
+        }
+    } else if (FP8 && warp >= 12) {
+        if constexpr (FP8) {
+            // ================================================ codes to values
+            const int t = threadIdx.x - 384;  // 0 .. 127
+            constexpr int PIECES = D / 16;    // 16 codes of a row
+            const int ch = t % PIECES, r0 = t / PIECES;
+            int n_item = 0;
+            uint32_t e = 0;
+            bool ok = true;
+            while (ok) {
+                const int slot = n_item % kItemSlots;
+                if (!(ok = warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit))) break;
+                const int sg = c.item[slot].seg, ntok = c.item[slot].ntok;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
+                ++n_item;
+                if (sg < 0) break;
+                for (int x = 0; x < 2 * ((ntok + kTileTokens - 1) / kTileTokens); ++x, ++e) {
+                    const uint32_t rs = e % Sh::RAW_STAGES, st = e % NST;
+                    const bool is_v = x & 1;
+                    const int nvalid = ntok - (x >> 1) * kTileTokens;
+                    if (!(ok = warp_wait(c.raw_full[rs], (e / Sh::RAW_STAGES) & 1, limit))) break;
+                    if (!(ok = warp_wait(c.kv_empty[st], ((e / NST) & 1) ^ 1, limit))) break;
+                    const uint8_t *src = smem + Sh::RAW_RING + rs * Sh::RAW + ch * 16;
+                    uint8_t *dst = smem + Sh::RING + st * Sh::TILE + (ch / 4) * Sh::SPAN;
+                    const bool bf16 = QBF16 || is_v;
+#pragma unroll 2
+                    for (int r = r0; r < kTileTokens; r += 128 / PIECES) {
+                        uint4 w = *reinterpret_cast<const uint4 *>(src + r * D);
+                        if (is_v && r >= nvalid) w = make_uint4(0, 0, 0, 0);
+                        uint32_t o[8];
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            o[2 * k] = e4m3x2_to_f16x2((uint16_t)(in[k] & 0xffff));
+                            o[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(in[k] >> 16));
+                        }
+                        if (bf16) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&o[k]));
+                                o[k] = pack_bf16x2(f.x, f.y);
+                            }
+                        }
+                        // the two 16-byte pieces, in an order that keeps eight
+                        // neighbouring lanes on different banks
+                        const int c0 = (2 * ch) & 7, odd = (ch >> 2) & 1;
+                        uint8_t *row = dst + r * 128;
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4 *>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4 *>(row + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
+                    }
+                    if (is_v && t < 16) c.scale[st][t] = c.raw_scale[rs][t];
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&c.raw_empty[rs]));
+                        mbar_arrive(smem_u32(&c.kv_full[st]));
+                    }
+                }
+            }
+            if (!ok && lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
         }
     } else if (warp >= 10) {
         // ========================================================= query rows
@@ -416,7 +528,11 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             }
             const RowsItem it = c.item[slot];
             if (it.seg < 0) break;
-            int *tok = c.tok[slot];
+            if (!warp_wait(c.rows_empty, (n_item & 1) ^ 1, limit)) {
+                rows_flag(p.status, FD_DEV_TIMEOUT);
+                break;
+            }
+            int *tok = c.tok;
             for (int r = t; r < 2 * kTileRows; r += 64) {
                 int q = -1;
                 if (r < it.nrows) {
@@ -439,8 +555,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 }
                 tok[r] = q;
             }
-            mbar_arrive(smem_u32(&c.rows_full[slot]));
-            bool ok = warp_wait(c.rows_full[slot], (n_item / kItemSlots) & 1, limit);
+            mbar_arrive(smem_u32(&c.rows_full));
+            bool ok = warp_wait(c.rows_full, n_item & 1, limit);
             if (!ok) rows_flag(p.status, FD_DEV_TIMEOUT);
             for (int i = 0; i < 2 && ok; ++i) {
                 if (i * kTileRows >= it.nrows) break;
@@ -477,8 +593,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         // ============================================================ products
         // The whole warp goes round, so that descriptors and addresses stay in
         // uniform registers; one lane issues.
-        constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, BF16, false);
-        constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, BF16, true);
+        constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, QBF16, false);
+        constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, !P16, true);
         const bool leader = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t q_desc = smem_desc(q_base, 16, 1024), k_desc = smem_desc(ring, 16, 1024);
@@ -514,6 +630,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 } else {
                     for (int k = k0; k < k1; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
                 }
+                if constexpr (PAIR)  // the weights' low parts
+                    for (int k = k0; k < k1; ++k) mma_ts(d, a0 + 64 + k * 8, b0 + k * 128, idesc_pv, true);
             }
         };
         // O += P V of one tile: the first part of the weights, then the rest
@@ -625,8 +743,11 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             const RowsItem it = c.item[slot];
             if (it.seg < 0) break;
             const int nt = (it.ntok + kTileTokens - 1) / kTileTokens;
-            bool ok = true;
-            if (i * kTileRows < it.nrows) {
+            bool ok = warp_wait(c.rows_full, n_item & 1, limit);
+            const int q = c.tok[i * kTileRows + r];  // this thread's row
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.rows_empty));
+            if (ok && i * kTileRows < it.nrows) {
                 const bool warp_live = i * kTileRows + (warp & 3) * 32 < it.nrows;
                 float ref = -INFINITY, l = 0.f;
                 for (int j = 0; j < nt; ++j, ++n_s) {
@@ -635,7 +756,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         break;
                     }
                     const int nvalid = min(kTileTokens, it.ntok - j * kTileTokens);
-                    if (i == 0 && (nvalid & 15)) {
+                    [[maybe_unused]] const uint32_t es = (e + 2 * j + 1) % NST;  // V's stage
+                    if constexpr (FP8) {  // its scales
+                        if (!(ok = warp_wait(c.kv_full[es], ((e + 2 * j + 1) / NST) & 1, limit))) break;
+                    } else if (i == 0 && (nvalid & 15)) {
                         // V rows behind the last token, up to the product's step of
                         // 16: their weight is 0, but they may hold infinities or NaN.
                         const uint32_t ev = e + 2 * j + 1;
@@ -644,7 +768,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             break;
                         }
                         const int z0 = nvalid, z1 = (nvalid + 15) & ~15;
-                        uint8_t *vt = smem + Sh::CONTROL + 2 * Sh::TILE + (ev % NST) * Sh::TILE;
+                        uint8_t *vt = smem + Sh::RING + (ev % NST) * Sh::TILE;
                         for (int x = r; x < (z1 - z0) * HALVES * 8; x += 128) {
                             const int h = x / ((z1 - z0) * 8), y = x - h * (z1 - z0) * 8;
                             *reinterpret_cast<uint4 *>(vt + h * Sh::SPAN + (z0 + y / 8) * 128 + (y % 8) * 16) =
@@ -670,6 +794,16 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
                         tmem_wait_ld();
                         tmem_loaded<128>(s);
+                        if constexpr (FP8) {
+#pragma unroll
+                            for (int k = 0; k < 128; k += 2) {
+                                const float ks = c.scale[es][k >> 4];
+                                float x0, x1;
+                                unpair(mul2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), pair(ks, ks)), x0, x1);
+                                s[k] = __float_as_uint(x0);
+                                s[k + 1] = __float_as_uint(x1);
+                            }
+                        }
                         highest(0);
                         highest(64);
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
@@ -701,7 +835,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         const float base = ref == -INFINITY ? 0.f : ref;
                         const uint64_t sc2 = pair(sc, sc), base2 = pair(-base, -base);
                         uint64_t sum[2] = {0, 0};
+                        // Weights of tokens [k0, k1) in place of their scores (words
+                        // k0 / 2 ..), or straight to tensor memory where they are pairs.
                         auto weights = [&](int k0, int k1) {
+                            [[maybe_unused]] uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = k0; k < k1; k += 2) {
                                 float x0, x1;
@@ -709,20 +846,37 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                 x0 = ex2(x0);
                                 x1 = ex2(x1);
                                 sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(x0, x1));
-                                s[k >> 1] = BF16 ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+                                if constexpr (FP8) {
+                                    const float vs = c.scale[es][8 + (k >> 4)];
+                                    unpair(mul2(pair(x0, x1), pair(vs, vs)), x0, x1);
+                                }
+                                const uint32_t w = P16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+                                if constexpr (PAIR) {
+                                    const int n = (k & 31) >> 1;
+                                    hi[n] = w;
+                                    lo[n] = pack_bf16x2(x0 - __uint_as_float(w << 16), x1 - __uint_as_float(w & 0xffff0000u));
+                                    if (n == 15) {
+                                        tmem_st16(ts + (k >> 5) * 16, hi);
+                                        tmem_st16(ts + 64 + (k >> 5) * 16, lo);
+                                    }
+                                } else {
+                                    s[k >> 1] = w;
+                                }
                             }
                         };
                         // The product with V starts on the first part while the
                         // rest is worked out.
                         weights(0, kPartTokens);
-                        tmem_st32(ts, s);
-                        tmem_st16(ts + 32, s + 32);
+                        if constexpr (!PAIR) {
+                            tmem_st32(ts, s);
+                            tmem_st16(ts + 32, s + 32);
+                        }
                         tmem_wait_st();
                         tmem_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&c.p_part[i]));
                         weights(kPartTokens, kTileTokens);
-                        tmem_st16(ts + 48, s + 48);
+                        if constexpr (!PAIR) tmem_st16(ts + 48, s + 48);
                         float l0, l1;
                         unpair(add2(sum[0], sum[1]), l0, l1);
                         l += l0 + l1;
@@ -740,12 +894,9 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 }
                 // ------------------------------------------------- the item's rows
                 if (ok && nt > 0) ok = warp_wait(c.pv_done[i], (n_s - 1) & 1, limit);
-                if (ok) ok = warp_wait(c.rows_full[slot], (n_item / kItemSlots) & 1, limit);
-                ok = __all_sync(0xffffffffu, ok);
                 if (ok && warp_live) {
                     tmem_fence_after();
                     const int row = i * kTileRows + r;
-                    const int q = c.tok[slot][row];
                     const int h = it.kvh * p.G + (it.row0 + row) % p.G;
                     const size_t at = (size_t)(q < 0 ? 0 : q) * p.Hq + h;
                     const bool empty = l == 0.f;  // no token, or every score -inf
@@ -806,8 +957,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                 uint32_t w[4];
 #pragma unroll
                                 for (int z = 0; z < 4; ++z)
-                                    w[z] = BF16 ? pack_bf16x2(y[x + 2 * z], y[x + 2 * z + 1])
-                                                : pack_f16x2(y[x + 2 * z], y[x + 2 * z + 1]);
+                                    w[z] = QBF16 ? pack_bf16x2(y[x + 2 * z], y[x + 2 * z + 1])
+                                                 : pack_f16x2(y[x + 2 * z], y[x + 2 * z + 1]);
                                 *reinterpret_cast<uint4 *>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         }
@@ -815,10 +966,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     }
                     tmem_fence_before();
                 }
-                if (!ok) {
-                    if (lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
-                    break;
-                }
+            }
+            if (!ok) {
+                if (lane == 0) rows_flag(p.status, FD_DEV_TIMEOUT);
+                break;
             }
             e += 2 * nt;
             __syncwarp();
