@@ -25,22 +25,41 @@ __global__ void __launch_bounds__(128) fd_rows_merge_kernel(const RowsParams p) 
     __syncwarp();
     if (lane == 0) p.row_splits[row] = 0;
     const float *pm = p.part_m + row * p.S, *pd = p.part_d + row * p.S;
-    float mx = -INFINITY;
-    for (int s = lane; s < n; s += 32) mx = fmaxf(mx, __ldcg(pm + s));
+    // Lane s has chunk s's weight (and s + 32's); then the outputs with eight
+    // chunks' loads under way.
+    float m0 = lane < n ? __ldcg(pm + lane) : -INFINITY, m1 = lane + 32 < n ? __ldcg(pm + lane + 32) : -INFINITY;
+    const float d0 = lane < n ? __ldcg(pd + lane) : 0.f, d1 = lane + 32 < n ? __ldcg(pd + lane + 32) : 0.f;
+    float mx = fmaxf(m0, m1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, shfl_xor(mx, o));
     const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f, y[E];
+    const float a0 = d0 == 0.f ? 0.f : ex2(m0 - base), a1 = d1 == 0.f ? 0.f : ex2(m1 - base);  // 0: an empty state
+    float sum = a0 * d0 + a1 * d1, y[E];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += shfl_xor(sum, o);
 #pragma unroll
     for (int x = 0; x < E; ++x) y[x] = 0.f;
-    for (int s = 0; s < n; ++s) {
-        const float d = __ldcg(pd + s);
-        if (d == 0.f) continue;  // an empty state
-        const float a = ex2(__ldcg(pm + s) - base);
-        sum = fmaf(a, d, sum);
-        const float *po = p.part_o + (row * p.S + s) * D + lane * E;
+    const float *po = p.part_o + (size_t)row * p.S * D + lane * E;
+    for (int s0 = 0; s0 < n; s0 += 8) {
+        float v[8][E];
 #pragma unroll
-        for (int x = 0; x < E; ++x) y[x] = fmaf(a, __ldcg(po + x), y[x]);
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int x = 0; x < E; x += 2) {
+                const float2 f = s0 + k < n ? __ldcg(reinterpret_cast<const float2 *>(po + (size_t)(s0 + k) * D + x))
+                                            : make_float2(0.f, 0.f);
+                v[k][x] = f.x;
+                v[k][x + 1] = f.y;
+            }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int s = s0 + k;
+            const float a = __shfl_sync(0xffffffffu, s < 32 ? a0 : a1, s & 31);
+            const float d = __shfl_sync(0xffffffffu, s < 32 ? d0 : d1, s & 31);
+#pragma unroll
+            for (int x = 0; x < E; ++x)
+                if (s < n && d != 0.f) y[x] = fmaf(a, v[k][x], y[x]);
+        }
     }
     const bool empty = sum == 0.f;
     float lse = empty ? -INFINITY : (mx + __log2f(sum)) * kRowsLn2;

@@ -16,6 +16,7 @@ namespace {
 constexpr int kMaxBeams = 1 << 16;
 constexpr long long kMaxTokens = 1LL << 22;  // query tokens of a call
 constexpr long long kMaxRows = 1LL << 28;    // query tokens * heads
+constexpr int kMaxGroup = 1 << 15;           // query heads of a KV head
 constexpr int kMaxRowSms = 1 << 16;
 constexpr uint64_t kRowsTimeoutNs = 2000000000ull;  // 2 s limit on any device-side wait
 constexpr int kPlanCross = 2, kPlanPrefix = 3;      // fd_cross_plan_t::reserved[0]
@@ -51,6 +52,7 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
         opt.debug_stall_us < 0 || opt.debug_stall_us > 1000000)
         return FD_ERR_INVALID_ARG;
     if (p.out_dtype != p.q_dtype) return FD_ERR_UNSUPPORTED;
+    if (p.Hq / p.Hkv > kMaxGroup) return FD_ERR_UNSUPPORTED;
     if (kv_rows > kMaxBatch || (long long)seqs * tokens > kMaxTokens || (long long)seqs * tokens * p.Hq > kMaxRows)
         return FD_ERR_UNSUPPORTED;
     int longest = 1, sms = opt.num_sms;
@@ -197,6 +199,7 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     rp.counters = reinterpret_cast<int *>(workspace + plan.ws_counters);
     rp.row_splits = rp.counters + 64;
     rp.boxr = std::gcd(p.page_size, kTile);
+    rp.g_magic = rp.G > 1 ? (uint32_t)(((1ull << 32) + rp.G - 1) / rp.G) : 0;
     rp.kv_once = 0;
     CUtensorMap tmk, tmv;
     if (!encode_pool_map(&tmk, k_pages, p, rp.boxr, true) || !encode_pool_map(&tmv, v_pages, p, rp.boxr, true))
@@ -213,6 +216,7 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
     fd_problem one = p;  // problem.B counts sequences or KV rows: both are bounded below
     one.B = 1;
     if (validate_problem(&one) != FD_OK || plan.reserved[0] != kind) return false;
+    if (p.Hq / p.Hkv > kMaxGroup) return false;
     if (plan.kv_rows < 1 || plan.kv_rows > kMaxBatch || plan.seqs < 1 || plan.tokens < 1 || plan.num_splits < 1 ||
         (long long)plan.seqs * plan.tokens > kMaxTokens || (long long)plan.seqs * plan.tokens * p.Hq > kMaxRows)
         return false;

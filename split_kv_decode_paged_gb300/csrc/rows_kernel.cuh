@@ -33,6 +33,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "fd_internal.h"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
@@ -56,7 +58,8 @@ struct RowsItem {
     int ntok;     // tokens of the chunk (0: an empty KV row)
     int split;
     int nsplit;
-    int pad[3];
+    int n0, g0;   // row0's token of the segment and head of the group
+    int pad;
 };
 
 template <int KV, int D>
@@ -76,26 +79,26 @@ struct RowsShape {
     static constexpr int REGS_SOFTMAX = FP8 ? 184 : 208, REGS_OTHER = FP8 ? 72 : 88;
     static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "the launch's registers");
     // shared memory: control block, two Q tiles, the rings
-    static constexpr int CONTROL = 3072;
+    static constexpr int CONTROL = D == 128 ? 3072 : 4096;
     static constexpr int RING = CONTROL + 2 * TILE, RAW_RING = RING + STAGES * TILE;
     static constexpr int SMEM = RAW_RING + RAW_STAGES * RAW;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
+template <typename Sh>
 struct RowsControl {
     uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], pv_done[2];
-    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full, rows_empty;
-    uint64_t kv_full[10], kv_empty[10];    // 16-bit tiles
-    uint64_t raw_full[8], raw_empty[8];    // tiles of codes
-    uint64_t drain;
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full, rows_empty, join_full, join_empty, drain;
+    uint64_t kv_full[Sh::STAGES], kv_empty[Sh::STAGES];              // 16-bit tiles
+    uint64_t raw_full[Sh::RAW_STAGES + 1], raw_empty[Sh::RAW_STAGES + 1];  // tiles of codes
     uint32_t tmem;
-    int pad;
+    int held[kItemSlots];      // softmax warps that are done with the stage held for the item's epilogue
     RowsItem item[kItemSlots];
     int tok[2 * kTileRows];    // q token (sequence * T + token) of every row of the item, -1 past the end
-    float raw_scale[8][16];    // of a stage's groups of 16 tokens: K's, then V's
-    float scale[6][16];
+    float2 join[kTileRows];    // reference and denominator that tile 1's warps hand to tile 0's
+    float raw_scale[Sh::RAW_STAGES + 1][16];  // of a stage's groups of 16 tokens: K's, then V's
+    alignas(16) float scale[Sh::FP8 ? Sh::STAGES : 1][16];
 };
-static_assert(sizeof(RowsControl) <= 3072, "the control block's room");
 
 // The segments of a call: query tokens and KV length of each, in the kernel's
 // dispatch order.  Lengths, counts and offsets that are out of range are cut.
@@ -136,7 +139,23 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool 
     const int n = live ? 16 : 0;  // 0: zeros
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// n / G for n < G + 256, by the factor ceil(2^32 / G) (0: G = 1).  Exact while
+// n G < 2^32, and G is at most 2^15.
+__device__ __forceinline__ int small_div(int n, uint32_t magic) {
+    return magic ? (int)__umulhi((uint32_t)n, magic) : n;
+}
+
+// Four neighbouring outputs, rounded to nearest even.
+template <bool BF16>
+__device__ __forceinline__ void put4(void *out, size_t at, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(out) + at) =
+        BF16 ? make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d)) : make_uint2(pack_f16x2(a, b), pack_f16x2(c, d));
+}
 
 // A whole warp's wait, for at most limit nanoseconds: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, uint64_t limit) {
@@ -164,7 +183,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     constexpr int HALVES = Sh::HALVES, NST = Sh::STAGES;
     constexpr uint32_t TMEM_S = 0, TMEM_O = 256;  // columns: S (and P) of both tiles, then O
     extern __shared__ __align__(1024) uint8_t smem[];
-    RowsControl &c = *reinterpret_cast<RowsControl *>(smem);
+    static_assert(sizeof(RowsControl<Sh>) <= Sh::CONTROL, "the control block's room");
+    RowsControl<Sh> &c = *reinterpret_cast<RowsControl<Sh> *>(smem);
     const uint32_t q_base = smem_u32(smem) + Sh::CONTROL, ring = smem_u32(smem) + Sh::RING;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.timeout_ns;
@@ -188,6 +208,9 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         }
         mbar_init(smem_u32(&c.rows_full), 64);
         mbar_init(smem_u32(&c.rows_empty), 8);
+        mbar_init(smem_u32(&c.join_full), 4);
+        mbar_init(smem_u32(&c.join_empty), 4);
+        c.held[0] = c.held[1] = 0;
         for (int i = 0; i < NST; ++i) {
             mbar_init(smem_u32(&c.kv_full[i]), FP8 ? 4 : 1);
             mbar_init(smem_u32(&c.kv_empty[i]), 1);
@@ -212,8 +235,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     tmem_fence_after();
     const uint32_t tmem = c.tmem;
     // Only shared memory, tensor memory and parameters so far; what follows
-    // reads what the preceding grid may still be writing.
-    grid_dependency_wait();
+    // reads what the preceding grid may still be writing.  Behind the pass over
+    // the sequences' own tokens only that pass's results may: they are waited
+    // for where they are joined (its launch waited for everything before it).
+    if (!p.own_out) grid_dependency_wait();
 
     // ---- Items of every segment, counted by all threads into the ring (not in
     // use yet): the producer warp keeps their sums over 32 runs of segments.
@@ -263,11 +288,16 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     __syncthreads();
     // Run of segments of each lane of the producer warp: [lane * per, ...).
     const int per = (nseg + 31) >> 5;
-    int run_items = 0, run_before = 0, run_off = 0, total = 0;
+    int run_items = 0, run_before = 0, run_off = 0, run_end = 0, run_len = 0, run_tokens = 0, total = 0;
     if (warp == 9) {
         const int s0 = min(lane * per, nseg), s1 = min(s0 + per, nseg);
         for (int s = s0; s < s1; ++s) run_items += s_items[s];
         run_off = s_off[s0];
+        run_end = s_off[s1];
+        if (per == 1 && s1 > s0) {
+            run_len = seg.kv_len(s0);
+            run_tokens = seg.tokens(run_off, run_end);
+        }
         int incl = run_items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -307,13 +337,17 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 // the lane's run that holds it, then the segment within the run
                 const unsigned has = __ballot_sync(0xffffffffu, run_before <= claim && claim < run_before + run_items);
                 const int src = __ffs(has) - 1;
-                int left = claim - __shfl_sync(0xffffffffu, run_before, src);
+                // its items before this one (one segment a run: of all runs)
+                int left = per == 1 ? claim : claim - __shfl_sync(0xffffffffu, run_before, src);
                 int high = __shfl_sync(0xffffffffu, run_off, src);
-                const int s_end = min((src + 1) * per, nseg);
-                for (int s0 = src * per;; s0 += 32) {
+                const int s_end = per == 1 ? nseg : min((src + 1) * per, nseg);
+                for (int s0 = per == 1 ? 0 : src * per;; s0 += 32) {
                     const int s = s0 + lane;
                     int first = 0, end = 0;
-                    if (p.offsets) {
+                    if (per == 1) {  // a lane's run is one segment: its first and last place are here
+                        first = run_off;
+                        end = run_end;
+                    } else if (p.offsets) {
                         int v = s < s_end ? min(max(seg.raw_offset(s + 1), high), p.seqs) : 0;
 #pragma unroll
                         for (int o = 1; o < 32; o <<= 1) {
@@ -328,9 +362,9 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         first = s * p.beams;
                         end = first + p.beams;
                     }
-                    const int len = s < s_end ? seg.kv_len(s) : 0;
-                    const int ntokens = s < s_end ? seg.tokens(first, end) : 0;
-                    const int n = s < s_end ? seg.items(ntokens, len) : 0;
+                    const int len = per == 1 ? run_len : (s < s_end ? seg.kv_len(s) : 0);
+                    const int ntokens = per == 1 ? run_tokens : (s < s_end ? seg.tokens(first, end) : 0);
+                    const int n = per == 1 ? run_items : (s < s_end ? seg.items(ntokens, len) : 0);
                     int incl = n;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -357,6 +391,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     it.split = k / p.Hkv;
                     it.nsplit = L == 0 ? 1 : (L + p.chunk - 1) / p.chunk;
                     it.nrows = min(2 * kTileRows, rows - it.row0);
+                    it.n0 = it.row0 / p.G;
+                    it.g0 = it.row0 - it.n0 * p.G;
                     it.tok0 = it.split * p.chunk;
                     it.ntok = min(L - it.tok0, p.chunk);
                     break;
@@ -455,9 +491,15 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     } else if (FP8 && warp >= 12) {
         if constexpr (FP8) {
             // ================================================ codes to values
+            // A thread turns 16 codes of a row at a time into two 16-byte pieces.
+            // Eight neighbouring lanes have four pieces of a 64-code half of one
+            // row and of the other half of the next row (D = 64: of two rows):
+            // their loads and stores meet no bank twice.
             const int t = threadIdx.x - 384;  // 0 .. 127
-            constexpr int PIECES = D / 16;    // 16 codes of a row
-            const int ch = t % PIECES, r0 = t / PIECES;
+            constexpr int ROWS = D == 128 ? 16 : 32;  // rows a pass over the 128 threads
+            const int pr = (t >> 2) & 1;              // row of the pair
+            const int r0 = D == 128 ? (t >> 4) * 2 + pr : t >> 2;
+            const int half = D == 128 ? ((t >> 3) & 1) ^ pr : 0, ch = t & 3;
             int n_item = 0;
             uint32_t e = 0;
             bool ok = true;
@@ -475,34 +517,43 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     const int nvalid = ntok - (x >> 1) * kTileTokens;
                     if (!(ok = warp_wait(c.raw_full[rs], (e / Sh::RAW_STAGES) & 1, limit))) break;
                     if (!(ok = warp_wait(c.kv_empty[st], ((e / NST) & 1) ^ 1, limit))) break;
-                    const uint8_t *src = smem + Sh::RAW_RING + rs * Sh::RAW + ch * 16;
-                    uint8_t *dst = smem + Sh::RING + st * Sh::TILE + (ch / 4) * Sh::SPAN;
-                    const bool bf16 = QBF16 || is_v;
-#pragma unroll 2
-                    for (int r = r0; r < kTileTokens; r += 128 / PIECES) {
-                        uint4 w = *reinterpret_cast<const uint4 *>(src + r * D);
-                        if (is_v && r >= nvalid) w = make_uint4(0, 0, 0, 0);
-                        uint32_t o[8];
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                    const uint8_t *src = smem + Sh::RAW_RING + rs * Sh::RAW + r0 * D + half * 64 + ch * 16;
+                    uint8_t *dst = smem + Sh::RING + st * Sh::TILE + half * Sh::SPAN + r0 * 128;
+                    // r & 7 is the same in every pass (ROWS is a multiple of 8)
+                    const int c0 = ((2 * ch) ^ (r0 & 7)) << 4, c1 = ((2 * ch + 1) ^ (r0 & 7)) << 4;
+                    auto convert = [&](auto wide) {
+                        constexpr bool BF16 = decltype(wide)::value;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            o[2 * k] = e4m3x2_to_f16x2((uint16_t)(in[k] & 0xffff));
-                            o[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(in[k] >> 16));
-                        }
-                        if (bf16) {
+                        for (int r = 0; r < kTileTokens / ROWS; ++r) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src + r * ROWS * D);
+                            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                            uint32_t o[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&o[k]));
-                                o[k] = pack_bf16x2(f.x, f.y);
+                                o[k] = e4m3x2_to_f16x2((uint16_t)(in[k >> 1] >> (16 * (k & 1))));
+                                if constexpr (BF16) {
+                                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&o[k]));
+                                    o[k] = pack_bf16x2(f.x, f.y);
+                                }
                             }
+                            uint8_t *row = dst + r * ROWS * 128;
+                            *reinterpret_cast<uint4 *>(row + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(row + c1) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
-                        // the two 16-byte pieces, in an order that keeps eight
-                        // neighbouring lanes on different banks
-                        const int c0 = (2 * ch) & 7, odd = (ch >> 2) & 1;
-                        uint8_t *row = dst + r * 128;
-                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                        *reinterpret_cast<uint4 *>(row + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4 *>(row + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
+                    };
+                    if (QBF16 || is_v)
+                        convert(std::true_type());
+                    else
+                        convert(std::false_type());
+                    if (is_v && nvalid < kTileTokens) {
+                        // V behind the last token: zeros, whatever the codes were
+#pragma unroll 1
+                        for (int r = 0; r < kTileTokens / ROWS; ++r)
+                            if (r0 + r * ROWS >= nvalid) {
+                                uint8_t *row = dst + r * ROWS * 128;
+                                *reinterpret_cast<uint4 *>(row + c0) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(row + c1) = make_uint4(0, 0, 0, 0);
+                            }
                     }
                     if (is_v && t < 16) c.scale[st][t] = c.raw_scale[rs][t];
                     fence_proxy_async_shared();
@@ -533,10 +584,12 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 break;
             }
             int *tok = c.tok;
-            for (int r = t; r < 2 * kTileRows; r += 64) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int r = t + 64 * u;
                 int q = -1;
                 if (r < it.nrows) {
-                    int n = (it.row0 + r) / p.G;  // token of the segment
+                    int n = it.n0 + small_div(it.g0 + r, p.g_magic);  // token of the segment
                     if (p.q_lens) {
                         int b = it.first;
                         for (int len = seg.q_len(b); n >= len && b + 1 < p.seqs; len = seg.q_len(b)) {
@@ -545,10 +598,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         }
                         q = b * p.T + n;
                     } else {
-                        const int i = it.first + n / p.T;
+                        const int k = p.T == 1 ? n : n / p.T, i = it.first + k;
                         const int b = p.members ? __ldg(p.members + i) : i;
                         if (b >= 0 && b < p.seqs)
-                            q = b * p.T + n % p.T;
+                            q = b * p.T + (n - k * p.T);
                         else
                             rows_flag(p.status, FD_DEV_BAD_PAGE);
                     }
@@ -557,38 +610,41 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             }
             mbar_arrive(smem_u32(&c.rows_full));
             bool ok = warp_wait(c.rows_full, n_item & 1, limit);
-            if (!ok) rows_flag(p.status, FD_DEV_TIMEOUT);
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (i * kTileRows >= it.nrows) break;
-                if (!warp_wait(c.q_empty[i], (n_q[i] & 1) ^ 1, limit)) {
-                    rows_flag(p.status, FD_DEV_TIMEOUT);
-                    ok = false;
-                    break;
-                }
-                if (it.ntok > 0) {
+            const int tiles = it.nrows > kTileRows ? 2 : 1;
+            for (int i = 0; i < tiles && ok; ++i) {
+                ok = warp_wait(c.q_empty[i], (n_q[i] & 1) ^ 1, limit);
+                if (ok && it.ntok > 0) {
                     constexpr int CH = D / 8;  // 16-byte pieces of a row
                     const int ch = t % CH;
                     const uint32_t dst = q_base + i * Sh::TILE + (ch / 8) * Sh::SPAN;
-#pragma unroll 4
+                    const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (size_t)it.kvh * p.G * D + ch * 8;
+#pragma unroll 8
                     for (int r = t / CH; r < kTileRows; r += 64 / CH) {
                         const int row = i * kTileRows + r, q = tok[row];
-                        const int h = it.kvh * p.G + (it.row0 + row) % p.G;
-                        const uint8_t *src = reinterpret_cast<const uint8_t *>(p.q) +
-                                             2 * (q < 0 ? 0 : (size_t)q * p.q_stride + (size_t)h * D + ch * 8);
-                        cp_async_16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, q >= 0);
+                        const int g = it.g0 + row - small_div(it.g0 + row, p.g_magic) * p.G;
+                        cp_async_16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                                    src + (size_t)max(q, 0) * p.q_stride + g * D, q >= 0);
                     }
-                    cp_async_wait_all();
-                    fence_proxy_async_shared();
                 }
+                cp_async_commit();
+            }
+            // hand the tiles over as they land
+            for (int i = 0; i < tiles && ok; ++i) {
+                if (i + 1 < tiles)
+                    cp_async_wait<1>();
+                else
+                    cp_async_wait<0>();
+                fence_proxy_async_shared();
                 mbar_arrive(smem_u32(&c.q_full[i]));
                 ++n_q[i];
             }
+            if (!ok) rows_flag(p.status, FD_DEV_TIMEOUT);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
             ++n_item;
             if (!ok) break;
         }
-        cp_async_wait_all();
+        cp_async_wait<0>();
     } else if (warp == 8) {
         // ============================================================ products
         // The whole warp goes round, so that descriptors and addresses stay in
@@ -609,8 +665,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 par ^= 1;
             }
         };
-        auto qk = [&](int i, uint32_t stage) {
-            const uint64_t a0 = q_desc + (uint64_t)(i * (Sh::TILE >> 4)), b0 = k_desc + (uint64_t)(stage * (Sh::TILE >> 4));
+        auto qk = [&](int i, int tile, uint32_t stage) {  // scores i of that query tile
+            const uint64_t a0 = q_desc + (uint64_t)(tile * (Sh::TILE >> 4)), b0 = k_desc + (uint64_t)(stage * (Sh::TILE >> 4));
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -672,50 +728,90 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             }
             if (!(ok = warp_wait(c.kv_full[st], par, limit))) break;
             tmem_fence_after();
-            qk(0, st);
-            if (two) qk(1, st);
-            release(c.kv_empty[st]);
-            if (nt == 1) {
-                release(c.q_empty[0]);
-                if (two) release(c.q_empty[1]);
-            }
-            next();
-            // V of a tile and K of the next one: looked for as the tile before
-            // them is issued, so that the look costs nothing.
-            bool v_here = false, k_here = false;
-            for (int j = 0; j < nt; ++j) {
-                const uint32_t sv = st;
-                const bool more = j + 1 < nt;
-                if (!__all_sync(0xffffffffu, v_here) && !(ok = warp_wait(c.kv_full[sv], par, limit))) break;
+            if (two) {
+                qk(0, 0, st);
+                qk(1, 1, st);
+                if (nt > 1)  // the last K tile's stage is released by the softmax warps
+                    release(c.kv_empty[st]);
+                else {
+                    release(c.q_empty[0]);
+                    release(c.q_empty[1]);
+                }
                 next();
-                const uint32_t sk = st;
-                if (more) {
-                    if (!__all_sync(0xffffffffu, k_here) && !(ok = warp_wait(c.kv_full[sk], par, limit))) break;
+                // V of a tile and K of the next one: looked for as the tile before
+                // them is issued, so that the look costs nothing.
+                bool v_here = false, k_here = false;
+                for (int j = 0; j < nt; ++j) {
+                    const uint32_t sv = st;
+                    const bool more = j + 1 < nt;
+                    if (!__all_sync(0xffffffffu, v_here) && !(ok = warp_wait(c.kv_full[sv], par, limit))) break;
                     next();
-                }
-                const int steps = more ? kTileTokens / 16 : (ntok - j * kTileTokens + 15) / 16;
-                if (!(ok = output(0, sv, steps, j > 0, n_p0++))) break;
-                if (more) qk(0, sk);
-                v_here = k_here = false;
-                if (more) {
-                    v_here = mbar_try_wait(smem_u32(&c.kv_full[st]), par);
-                    const uint32_t s2 = st + 1 == NST ? 0 : st + 1;
-                    if (j + 2 < nt) k_here = mbar_try_wait(smem_u32(&c.kv_full[s2]), s2 ? par : par ^ 1);
-                }
-                if (two) {
+                    const uint32_t sk = st;
+                    if (more) {
+                        if (!__all_sync(0xffffffffu, k_here) && !(ok = warp_wait(c.kv_full[sk], par, limit))) break;
+                        next();
+                    }
+                    const int steps = more ? kTileTokens / 16 : (ntok - j * kTileTokens + 15) / 16;
+                    if (!(ok = output(0, sv, steps, j > 0, n_p0++))) break;
+                    if (more) qk(0, 0, sk);
+                    v_here = k_here = false;
+                    if (more) {
+                        v_here = mbar_try_wait(smem_u32(&c.kv_full[st]), par);
+                        const uint32_t s2 = st + 1 == NST ? 0 : st + 1;
+                        if (j + 2 < nt) k_here = mbar_try_wait(smem_u32(&c.kv_full[s2]), s2 ? par : par ^ 1);
+                    }
                     if (!(ok = output(1, sv, steps, j > 0, n_p1++))) break;
                     release(c.kv_empty[sv]);
                     if (more) {
-                        qk(1, sk);
-                        release(c.kv_empty[sk]);
+                        qk(1, 1, sk);
+                        if (j + 2 < nt)
+                            release(c.kv_empty[sk]);
+                        else {
+                            release(c.q_empty[0]);
+                            release(c.q_empty[1]);
+                        }
                     }
-                } else {
-                    release(c.kv_empty[sv]);
-                    if (more) release(c.kv_empty[sk]);
                 }
-                if (j + 2 == nt) {
+            } else {
+                // One row tile: its KV tiles in turn to the two halves of the
+                // softmax, two of them under way at a time.
+                qk(0, 0, st);
+                if (nt > 1)
+                    release(c.kv_empty[st]);
+                else
                     release(c.q_empty[0]);
-                    if (two) release(c.q_empty[1]);
+                next();
+                uint32_t sv = st, pv_par = par;  // V of tile 0
+                if (nt > 1) {
+                    next();                      // K of tile 1
+                    if (!(ok = warp_wait(c.kv_full[st], par, limit))) break;
+                    tmem_fence_after();
+                    qk(1, 0, st);
+                    if (nt > 2)
+                        release(c.kv_empty[st]);
+                    else
+                        release(c.q_empty[0]);
+                }
+                next();
+                for (int j = 0; j < nt; ++j) {
+                    const int steps = min(kTileTokens / 16, (ntok - j * kTileTokens + 15) / 16), i = j & 1;
+                    if (!(ok = warp_wait(c.kv_full[sv], pv_par, limit))) break;
+                    if (!(ok = output(i, sv, steps, j > 1, i ? n_p1++ : n_p0++))) break;
+                    release(c.kv_empty[sv]);
+                    // entries from here: V of tile j + 1 at st, K of tile j + 2 behind it
+                    sv = st;
+                    pv_par = par;
+                    if (j + 2 < nt) {
+                        next();
+                        if (!(ok = warp_wait(c.kv_full[st], par, limit))) break;
+                        tmem_fence_after();
+                        qk(i, 0, st);
+                        if (j + 3 < nt)
+                            release(c.kv_empty[st]);
+                        else
+                            release(c.q_empty[0]);
+                    }
+                    if (j + 1 < nt) next();
                 }
             }
         }
@@ -733,7 +829,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         const uint32_t ts = tmem + lanes + TMEM_S + i * 128, to = tmem + lanes + TMEM_O + i * 128;
         const float sc = p.scale_log2;
         int n_item = 0;
-        uint32_t e = 0, n_s = 0;  // ring entries and score tiles so far
+        uint32_t e = 0, n_s = 0, n_join = 0;  // ring entries, score tiles and joined items so far
+        bool handed = false;  // tile 1's state of a joined item may still be read
         while (true) {
             const int slot = n_item % kItemSlots;
             if (!warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit)) {
@@ -744,13 +841,17 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             if (it.seg < 0) break;
             const int nt = (it.ntok + kTileTokens - 1) / kTileTokens;
             bool ok = warp_wait(c.rows_full, n_item & 1, limit);
-            const int q = c.tok[i * kTileRows + r];  // this thread's row
+            // With one row tile both halves have its rows, and every other KV tile.
+            const bool solo = it.nrows <= kTileRows;
+            const int row0 = solo ? 0 : i * kTileRows, step = solo ? 2 : 1, j0 = solo ? i : 0;
+            const int q = c.tok[row0 + r];  // this thread's row
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c.rows_empty));
-            if (ok && i * kTileRows < it.nrows) {
-                const bool warp_live = i * kTileRows + (warp & 3) * 32 < it.nrows;
-                float ref = -INFINITY, l = 0.f;
-                for (int j = 0; j < nt; ++j, ++n_s) {
+            const bool warp_live = row0 + (warp & 3) * 32 < it.nrows;
+            const bool join = solo && nt > 1;
+            float ref = -INFINITY, l = 0.f;
+            if (ok) {
+                for (int j = j0; j < nt; j += step, ++n_s) {
                     if (!warp_wait(c.s_full[i], n_s & 1, limit)) {
                         ok = false;
                         break;
@@ -759,7 +860,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     [[maybe_unused]] const uint32_t es = (e + 2 * j + 1) % NST;  // V's stage
                     if constexpr (FP8) {  // its scales
                         if (!(ok = warp_wait(c.kv_full[es], ((e + 2 * j + 1) / NST) & 1, limit))) break;
-                    } else if (i == 0 && (nvalid & 15)) {
+                    } else if ((solo || i == 0) && (nvalid & 15)) {
                         // V rows behind the last token, up to the product's step of
                         // 16: their weight is 0, but they may hold infinities or NaN.
                         const uint32_t ev = e + 2 * j + 1;
@@ -776,43 +877,67 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         }
                         fence_proxy_async_shared();
                     }
+                    if (handed) {  // O of the joined item before this one has been read
+                        if (!(ok = warp_wait(c.join_empty, (n_join - 1) & 1, limit))) break;
+                        handed = false;
+                    }
                     if (warp_live) {
                         tmem_fence_after();
                         uint32_t s[128];
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        auto highest = [&](int k0) {  // of 64 scores, masked behind the last token
-                            if (nvalid < kTileTokens) {
-#pragma unroll
-                                for (int k = k0; k < k0 + 64; ++k)
-                                    if (k >= nvalid) s[k] = 0xff800000u;  // -inf
-                            }
-#pragma unroll
-                            for (int k = k0; k < k0 + 64; k += 2)
-                                mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                        };
 #pragma unroll
                         for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
                         tmem_wait_ld();
                         tmem_loaded<128>(s);
+                        // E4M3: a group's scale goes into its factor; one that is not
+                        // positive into the scores, before hidden ones are set to
+                        // -inf (the highest score would be the lowest product, or
+                        // -inf times 0).
+                        [[maybe_unused]] float fs[8], vs[8];
                         if constexpr (FP8) {
+                            const float4 *cs = reinterpret_cast<const float4 *>(c.scale[es]);
+                            const float4 k0 = cs[0], k1 = cs[1], v0 = cs[2], v1 = cs[3];
+                            fs[0] = k0.x; fs[1] = k0.y; fs[2] = k0.z; fs[3] = k0.w;
+                            fs[4] = k1.x; fs[5] = k1.y; fs[6] = k1.z; fs[7] = k1.w;
+                            vs[0] = v0.x; vs[1] = v0.y; vs[2] = v0.z; vs[3] = v0.w;
+                            vs[4] = v1.x; vs[5] = v1.y; vs[6] = v1.z; vs[7] = v1.w;
+                            bool odd = false;
 #pragma unroll
-                            for (int k = 0; k < 128; k += 2) {
-                                const float ks = c.scale[es][k >> 4];
-                                float x0, x1;
-                                unpair(mul2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), pair(ks, ks)), x0, x1);
-                                s[k] = __float_as_uint(x0);
-                                s[k + 1] = __float_as_uint(x1);
+                            for (int k = 0; k < 8; ++k) odd |= !(fs[k] > 0.f);
+                            if (odd) {
+#pragma unroll
+                                for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * fs[k >> 4]);
                             }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) fs[k] = odd ? sc : sc * fs[k];
                         }
-                        highest(0);
-                        highest(64);
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                        if (nvalid < kTileTokens) {
+#pragma unroll
+                            for (int k = 0; k < 128; ++k)
+                                if (k >= nvalid) s[k] = 0xff800000u;  // -inf
+                        }
+                        float top;
+                        if constexpr (FP8) {
+                            top = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 128; k += 16) {
+                                float m = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+#pragma unroll
+                                for (int x = 2; x < 16; x += 2) m = max3(m, __uint_as_float(s[k + x]), __uint_as_float(s[k + x + 1]));
+                                top = k < nvalid ? fmaxf(top, m * fs[k >> 4]) : top;
+                            }
+                        } else {
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int k = 0; k < 128; k += 2)
+                                mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                        }
                         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
                             const float now = fmaxf(ref, top);
                             const float a = now == -INFINITY ? 1.f : ex2(ref - now);
                             ref = now;
                             l *= a;
-                            if (j > 0) {
+                            if (j > j0) {
                                 // O so far, once the product before this one is complete
                                 if (!warp_wait(c.pv_done[i], (n_s - 1) & 1, limit)) {
                                     ok = false;
@@ -833,7 +958,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             }
                         }
                         const float base = ref == -INFINITY ? 0.f : ref;
-                        const uint64_t sc2 = pair(sc, sc), base2 = pair(-base, -base);
+                        const uint64_t base2 = pair(-base, -base);
                         uint64_t sum[2] = {0, 0};
                         // Weights of tokens [k0, k1) in place of their scores (words
                         // k0 / 2 ..), or straight to tensor memory where they are pairs.
@@ -842,13 +967,13 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
 #pragma unroll
                             for (int k = k0; k < k1; k += 2) {
                                 float x0, x1;
-                                unpair(fma2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, base2), x0, x1);
+                                const float f = FP8 ? fs[k >> 4] : sc;
+                                unpair(fma2(pair(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), pair(f, f), base2), x0, x1);
                                 x0 = ex2(x0);
                                 x1 = ex2(x1);
                                 sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(x0, x1));
                                 if constexpr (FP8) {
-                                    const float vs = c.scale[es][8 + (k >> 4)];
-                                    unpair(mul2(pair(x0, x1), pair(vs, vs)), x0, x1);
+                                    unpair(mul2(pair(x0, x1), pair(vs[k >> 4], vs[k >> 4])), x0, x1);
                                 }
                                 const uint32_t w = P16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
                                 if constexpr (PAIR) {
@@ -893,78 +1018,143 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     }
                 }
                 // ------------------------------------------------- the item's rows
-                if (ok && nt > 0) ok = warp_wait(c.pv_done[i], (n_s - 1) & 1, limit);
+                if (ok && j0 < nt) ok = warp_wait(c.pv_done[i], (n_s - 1) & 1, limit);
+            }
+            if (ok && join && i == 1) {
+                // this half's O stays where it is; the other half's warps, which
+                // read the same lanes of tensor memory, take it from there
+                c.join[r] = make_float2(ref, l);
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c.join_full));
+                ++n_join;
+                handed = true;
+            } else if (ok && !(solo && i == 1)) {
+                float a0 = 1.f, a1 = 0.f;
+                if (join) {
+                    ok = warp_wait(c.join_full, n_join & 1, limit);
+                    ++n_join;
+                    const float2 o = c.join[r];
+                    const float top = fmaxf(ref, o.x), base = top == -INFINITY ? 0.f : top;
+                    a0 = ex2(ref - base);
+                    a1 = ex2(o.x - base);
+                    l = a0 * l + a1 * o.y;
+                    ref = top;
+                }
                 if (ok && warp_live) {
                     tmem_fence_after();
-                    const int row = i * kTileRows + r;
-                    const int h = it.kvh * p.G + (it.row0 + row) % p.G;
-                    const size_t at = (size_t)(q < 0 ? 0 : q) * p.Hq + h;
-                    const bool empty = l == 0.f;  // no token, or every score -inf
+                    const int g = it.g0 + row0 + r;
+                    const int h = it.kvh * p.G + g - small_div(g, p.g_magic) * p.G;
+                    const int at = q < 0 ? -1 : q * p.Hq + h;  // row of out
+                    const bool empty = l == 0.f;               // no token, or every score -inf
                     float mul = empty ? 0.f : 1.f / l, own = 0.f;
-                    if (it.nsplit > 1) {
-                        mul = 1.f;
-                        if (q >= 0) {
-                            p.part_m[at * p.S + it.split] = ref;
-                            p.part_d[at * p.S + it.split] = l;
+                    const bool part = it.nsplit > 1;
+                    if (p.own_out && !part) grid_dependency_wait();
+                    if (at >= 0) {
+                        if (part) {
+                            mul = 1.f;
+                            p.part_m[(size_t)at * p.S + it.split] = ref;
+                            p.part_d[(size_t)at * p.S + it.split] = l;
                             if (it.split == 0) p.row_splits[at] = it.nsplit;
-                        }
-                    } else if (q >= 0) {
-                        float lse = empty ? -INFINITY : (ref + __log2f(l)) * kRowsLn2;
-                        if (p.own_out) {
-                            const float lo = p.own_lse[at], m = fmaxf(lse, lo);
-                            const float wa = lse == -INFINITY ? 0.f : __expf(lse - m), wb = lo == -INFINITY ? 0.f : __expf(lo - m);
-                            const float inv = wa + wb > 0.f ? 1.f / (wa + wb) : 0.f;
-                            mul *= wa * inv;
-                            own = wb * inv;
-                            lse = m == -INFINITY ? -INFINITY : m + logf(wa + wb);
-                        }
-                        if (p.lse) p.lse[at] = lse;
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        if (nt > 0) {
-                            tmem_ld32(to + k, o);
-                            tmem_wait_ld();
-                            tmem_loaded<32>(o);
                         } else {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] = 0u;
-                        }
-                        if (q >= 0 && it.nsplit > 1) {
-                            float *dst = p.part_o + (at * p.S + it.split) * D + k;
-#pragma unroll
-                            for (int x = 0; x < 32; x += 4)
-                                *reinterpret_cast<uint4 *>(dst + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-                        } else if (q >= 0) {
-                            float y[32];
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) y[x] = empty ? 0.f : __uint_as_float(o[x]) * mul;
+                            float lse = empty ? -INFINITY : (ref + __log2f(l)) * kRowsLn2;
                             if (p.own_out) {
-                                const float4 *src = reinterpret_cast<const float4 *>(p.own_out + at * D + k);
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) {
-                                    const float4 f = __ldcg(src + x);
-                                    y[4 * x] = fmaf(f.x, own, y[4 * x]);
-                                    y[4 * x + 1] = fmaf(f.y, own, y[4 * x + 1]);
-                                    y[4 * x + 2] = fmaf(f.z, own, y[4 * x + 2]);
-                                    y[4 * x + 3] = fmaf(f.w, own, y[4 * x + 3]);
-                                }
+                                const float lo = __ldcg(p.own_lse + at), m = fmaxf(lse, lo);
+                                const float wa = lse == -INFINITY ? 0.f : __expf(lse - m);
+                                const float wb = lo == -INFINITY ? 0.f : __expf(lo - m);
+                                const float inv = wa + wb > 0.f ? 1.f / (wa + wb) : 0.f;
+                                mul *= wa * inv;
+                                own = wb * inv;
+                                lse = m == -INFINITY ? -INFINITY : m + logf(wa + wb);
                             }
-                            uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + at * D + k;
+                            if (p.lse) p.lse[at] = lse;
+                        }
+                    }
+                    a0 *= mul;
+                    a1 *= mul;
+                    // O through shared memory, so that neighbouring lanes write
+                    // neighbouring bytes of a row: W columns at a time, in the
+                    // stage of the item's last K tile (all its products are
+                    // complete; the warps release it below).
+                    constexpr int W = D / 4, CH = W / 4, RPI = 32 / CH;  // columns, 16-byte pieces, rows a pass
+                    uint8_t *stage = smem + Sh::RING + ((e + 2 * max(nt - 1, 0)) % NST) * Sh::TILE + warp * (32 * W * 4);
+                    auto piece = [&](int row, int ch) {  // where piece ch of a row lies: eight lanes, eight banks' groups
+                        return stage + row * (W * 4) + ((ch ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 4);
+                    };
+#pragma unroll 1
+                    for (int k = 0; k < D; k += W) {
+                        uint32_t o[W];
+                        if (nt > 0) {
+                            tmem_ldw<W>(to + k, o);
+                            tmem_wait_ld();
+                            tmem_loaded<W>(o);
+                        }
 #pragma unroll
-                            for (int x = 0; x < 32; x += 8) {
-                                uint32_t w[4];
+                        for (int x = 0; x < W; ++x) o[x] = empty ? 0u : __float_as_uint(__uint_as_float(o[x]) * a0);
+                        if (join) {
+                            uint32_t o1[W];
+                            tmem_ldw<W>(to + 128 + k, o1);
+                            tmem_wait_ld();
+                            tmem_loaded<W>(o1);
 #pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    w[z] = QBF16 ? pack_bf16x2(y[x + 2 * z], y[x + 2 * z + 1])
-                                                 : pack_f16x2(y[x + 2 * z], y[x + 2 * z + 1]);
-                                *reinterpret_cast<uint4 *>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int x = 0; x < W; ++x)
+                                if (!empty) o[x] = __float_as_uint(fmaf(__uint_as_float(o1[x]), a1, __uint_as_float(o[x])));
+                        }
+                        if (nt == 0) {  // no tokens and no stage: zeros, joined with the own tokens' state
+#pragma unroll 1
+                            for (int x = 0; x < W; x += 4) {
+                                const float4 f = p.own_out && at >= 0 ? __ldcg(reinterpret_cast<const float4 *>(p.own_out + (size_t)at * D + k + x))
+                                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (at >= 0) put4<QBF16>(p.out, (size_t)at * D + k + x, f.x * own, f.y * own, f.z * own, f.w * own);
+                            }
+                            __syncwarp();
+                            continue;
+                        }
+#pragma unroll
+                        for (int x = 0; x < CH; ++x)
+                            *reinterpret_cast<uint4 *>(piece(lane, x)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        __syncwarp();
+#pragma unroll 4
+                        for (int x = 0; x < 32; x += RPI) {
+                            const int row = x + lane / CH, ch = lane % CH;
+                            const int to_row = __shfl_sync(0xffffffffu, at, row);
+                            const float w = __shfl_sync(0xffffffffu, own, row);
+                            float4 v = *reinterpret_cast<const float4 *>(piece(row, ch));
+                            if (to_row < 0) continue;
+                            if (part) {
+                                *reinterpret_cast<float4 *>(p.part_o + ((size_t)to_row * p.S + it.split) * D + k + 4 * ch) = v;
+                            } else {
+                                const size_t to_at = (size_t)to_row * D + k + 4 * ch;
+                                if (p.own_out) {
+                                    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.own_out + to_at));
+                                    v.x = fmaf(f.x, w, v.x);
+                                    v.y = fmaf(f.y, w, v.y);
+                                    v.z = fmaf(f.z, w, v.z);
+                                    v.w = fmaf(f.w, w, v.w);
+                                }
+                                put4<QBF16>(p.out, to_at, v.x, v.y, v.z, v.w);
                             }
                         }
                         __syncwarp();
                     }
+                }
+                if (join) {
                     tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&c.join_empty));
+                }
+                tmem_fence_before();
+            }
+            if (ok && nt > 0) {
+                // the last warp that is done with the held stage gives it back
+                // (counted by item: one half may be an item ahead of the other)
+                fence_proxy_async_shared();
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0 && atomicAdd(&c.held[slot], 1) == 7) {
+                    c.held[slot] = 0;
+                    __threadfence_block();
+                    mbar_arrive(smem_u32(&c.kv_empty[(e + 2 * (nt - 1)) % NST]));
                 }
             }
             if (!ok) {
@@ -978,6 +1168,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         }
         tmem_fence_before();
     }
+    // What waits for this grid may read the own tokens' state as well.
+    if (p.own_out) grid_dependency_wait();
     __syncthreads();
     tmem_fence_after();
     if (warp == 8) tmem_dealloc(tmem, 512);
