@@ -287,7 +287,7 @@ EncodeTiledFn encode_fn() {
 // kvh, page): one box = `boxr` token rows x all of D for one KV head, landing
 // in shared memory as [span][row][span bytes] so each span is one swizzled
 // region (a span is 128 bytes, or the whole row when the row is shorter).
-bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool one_span) {
+bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool plain) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int e = elem_bytes(p.kv_dtype);
@@ -298,12 +298,12 @@ bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p
                           (cuuint64_t)p.num_pages};
     cuuint64_t strides[4] = {(cuuint64_t)rb * p.Hkv, (cuuint64_t)span, (cuuint64_t)rb,
                              (cuuint64_t)rb * p.Hkv * p.page_size};
-    cuuint32_t box[5] = {(cuuint32_t)(span / e), (cuuint32_t)boxr, (cuuint32_t)(one_span ? 1 : nspan), 1u, 1u};
+    cuuint32_t box[5] = {(cuuint32_t)(span / e), (cuuint32_t)boxr, (cuuint32_t)nspan, 1u, 1u};
     cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
     const CUtensorMapDataType dt = e == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    const CUtensorMapSwizzle sw = one_span && e == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                  : span == 128      ? CU_TENSOR_MAP_SWIZZLE_128B
-                                                     : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapSwizzle sw = plain         ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                  : span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                : CU_TENSOR_MAP_SWIZZLE_64B;
     // L2 promotion no wider than one row: a wider promotion also fetches the
     // neighbouring KV head's row, which another CTA reads at another time.
     const CUtensorMapL2promotion l2p = rb >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
@@ -312,6 +312,25 @@ bool fd::encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p
     CUresult r = fn(map, dt, 5, const_cast<void *>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                     l2p, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+// A 16-bit pool as 4-D (d within a 128-byte span, row of eight tokens, span of
+// the token's heads, group of eight tokens of the pool): a box is boxr tokens of
+// one KV head, in shared memory [group][span][row][128 bytes], swizzled.  Groups
+// run through a page's slots and on to the next page; tokens of all heads do the
+// same with their spans.
+bool fd::encode_pool_map_grouped(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = (cuuint64_t)p.Hkv * p.D * 2, nspan = (cuuint64_t)p.D / 64;
+    cuuint64_t dims[4] = {64, 8, nspan * p.Hkv, (cuuint64_t)p.num_pages * p.page_size / 8};
+    cuuint64_t strides[3] = {row, 128, row * 8};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)nspan, (cuuint32_t)boxr / 8};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              p.D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 extern "C" {

@@ -222,10 +222,11 @@ struct DeviceInfo {
 };
 fd_status device_info(DeviceInfo &di);
 fd_status validate_problem(const fd_problem *p);
-// Tensor map of a K or V pool with boxes of boxr token rows of one KV head: all
-// 128-byte spans of a row, one after the other, or one of them (E4M3: its whole
-// row, unswizzled).
-bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool one_span = false);
+// Tensor map of a K or V pool with boxes of boxr token rows of one KV head, all
+// 128-byte spans of a row, one after the other, swizzled or plain.
+bool encode_pool_map(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr, bool plain = false);
+// The same of a 16-bit pool with a box's tokens in groups of eight.
+bool encode_pool_map_grouped(CUtensorMap *map, const void *pool, const fd_problem &p, int boxr);
 
 cudaError_t launch_merge_two(const float *oa, const float *la, const float *ob, const float *lb, int rows, int D,
                              int out_dtype, void *out, float *lse, cudaStream_t stream);

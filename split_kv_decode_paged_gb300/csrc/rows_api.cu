@@ -202,8 +202,10 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     rp.g_magic = rp.G > 1 ? (uint32_t)(((1ull << 32) + rp.G - 1) / rp.G) : 0;
     rp.kv_once = 0;
     CUtensorMap tmk, tmv;
-    if (!encode_pool_map(&tmk, k_pages, p, rp.boxr, true) || !encode_pool_map(&tmv, v_pages, p, rp.boxr, true))
-        return FD_ERR_CUDA;
+    const bool ok = p.kv_dtype == FD_E4M3
+                        ? encode_pool_map(&tmk, k_pages, p, rp.boxr, true) && encode_pool_map(&tmv, v_pages, p, rp.boxr, true)
+                        : encode_pool_map_grouped(&tmk, k_pages, p, rp.boxr) && encode_pool_map_grouped(&tmv, v_pages, p, rp.boxr);
+    if (!ok) return FD_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (launch_rows(rp, tmk, tmv, plan.grid_ctas, s) != cudaSuccess) return FD_ERR_CUDA;
     if (plan.num_splits > 1 && launch_rows_merge(rp, s) != cudaSuccess) return FD_ERR_CUDA;

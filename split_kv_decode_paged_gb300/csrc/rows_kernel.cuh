@@ -67,7 +67,10 @@ struct RowsShape {
     static constexpr bool FP8 = KV == KV_E4M3;
     static constexpr int HALVES = D / 64;                   // 128-byte spans of a row
     static constexpr int TILE = kTileTokens * D * 2;        // bytes of a Q, K or V tile (16 bits)
-    static constexpr int SPAN = kTileTokens * 128;          // bytes of one half of it
+    static constexpr int SPAN = kTileTokens * 128;          // bytes of one half of a Q tile
+    // K and V tiles: eight tokens' 128-byte spans, half after half, then the next
+    // eight tokens, so that one TMA box brings all of a page's tokens
+    static constexpr int GROUP = HALVES * 1024;
     static constexpr int RAW = FP8 ? kTileTokens * D : 0;   // bytes of a tile of codes
     // stages of 16-bit K and V tiles, and of codes
     static constexpr int STAGES = (FP8 ? 3 : 5) * (128 / D);
@@ -463,10 +466,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             const uint32_t dst = smem_u32(smem) + Sh::RAW_RING + st * Sh::RAW + (lane << bsh) * D;
                             tma_load_5d(dst, kv ? &tmv : &tmk, fb, 0, at, 0, it.kvh, pg, policy);
                         } else {
-                            const uint32_t dst = ring + st * Sh::TILE + ((lane << bsh) * 128);
-#pragma unroll
-                            for (int h = 0; h < HALVES; ++h)
-                                tma_load_5d(dst + h * Sh::SPAN, kv ? &tmv : &tmk, fb, 0, at, h, it.kvh, pg, policy);
+                            tma_load_4d(ring + st * Sh::TILE + (lane << bsh) * D * 2, kv ? &tmv : &tmk, fb, 0, 0, it.kvh * HALVES,
+                                        pg * (p.page_size >> 3) + (at >> 3), policy);
                         }
                     }
                     ++e;
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     if (!(ok = warp_wait(c.raw_full[rs], (e / Sh::RAW_STAGES) & 1, limit))) break;
                     if (!(ok = warp_wait(c.kv_empty[st], ((e / NST) & 1) ^ 1, limit))) break;
                     const uint8_t *src = smem + Sh::RAW_RING + rs * Sh::RAW + r0 * D + half * 64 + ch * 16;
-                    uint8_t *dst = smem + Sh::RING + st * Sh::TILE + half * Sh::SPAN + r0 * 128;
+                    uint8_t *dst = smem + Sh::RING + st * Sh::TILE + (r0 >> 3) * Sh::GROUP + half * 1024 + (r0 & 7) * 128;
                     // r & 7 is the same in every pass (ROWS is a multiple of 8)
                     const int c0 = ((2 * ch) ^ (r0 & 7)) << 4, c1 = ((2 * ch + 1) ^ (r0 & 7)) << 4;
                     auto convert = [&](auto wide) {
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                     o[k] = pack_bf16x2(f.x, f.y);
                                 }
                             }
-                            uint8_t *row = dst + r * ROWS * 128;
+                            uint8_t *row = dst + r * (ROWS / 8) * Sh::GROUP;
                             *reinterpret_cast<uint4 *>(row + c0) = make_uint4(o[0], o[1], o[2], o[3]);
                             *reinterpret_cast<uint4 *>(row + c1) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
 #pragma unroll 1
                         for (int r = 0; r < kTileTokens / ROWS; ++r)
                             if (r0 + r * ROWS >= nvalid) {
-                                uint8_t *row = dst + r * ROWS * 128;
+                                uint8_t *row = dst + r * (ROWS / 8) * Sh::GROUP;
                                 *reinterpret_cast<uint4 *>(row + c0) = make_uint4(0, 0, 0, 0);
                                 *reinterpret_cast<uint4 *>(row + c1) = make_uint4(0, 0, 0, 0);
                             }
@@ -653,8 +654,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, !P16, true);
         const bool leader = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t q_desc = smem_desc(q_base, 16, 1024), k_desc = smem_desc(ring, 16, 1024);
-        const uint64_t v_desc = smem_desc(ring, Sh::SPAN, 1024);
+        const uint64_t q_desc = smem_desc(q_base, 16, 1024), k_desc = smem_desc(ring, 16, Sh::GROUP);
+        const uint64_t v_desc = smem_desc(ring, 1024, Sh::GROUP);
         int n_item = 0;
         uint32_t st = 0, par = 0;  // ring stage and parity of the next entry
         uint32_t n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0;
@@ -670,8 +671,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k / 4) * Sh::SPAN + (k % 4) * 32) >> 4;
-                    mma_ss(tm + TMEM_S + i * 128, a0 + off, b0 + off, idesc_qk, k > 0);
+                    mma_ss(tm + TMEM_S + i * 128, a0 + (((k / 4) * Sh::SPAN + (k % 4) * 32) >> 4),
+                           b0 + (((k / 4) * 1024 + (k % 4) * 32) >> 4), idesc_qk, k > 0);
                 }
                 mma_commit(smem_u32(&c.s_full[i]));
             }
@@ -682,12 +683,12 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             if (leader) {
                 if (k1 - k0 == kPartTokens / 16) {
 #pragma unroll
-                    for (int k = 0; k < kPartTokens / 16; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
+                    for (int k = 0; k < kPartTokens / 16; ++k) mma_ts(d, a0 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, k > 0 || more);
                 } else {
-                    for (int k = k0; k < k1; ++k) mma_ts(d, a0 + k * 8, b0 + k * 128, idesc_pv, k > 0 || more);
+                    for (int k = k0; k < k1; ++k) mma_ts(d, a0 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, k > 0 || more);
                 }
                 if constexpr (PAIR)  // the weights' low parts
-                    for (int k = k0; k < k1; ++k) mma_ts(d, a0 + 64 + k * 8, b0 + k * 128, idesc_pv, true);
+                    for (int k = k0; k < k1; ++k) mma_ts(d, a0 + 64 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, true);
             }
         };
         // O += P V of one tile: the first part of the weights, then the rest
@@ -871,8 +872,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         const int z0 = nvalid, z1 = (nvalid + 15) & ~15;
                         uint8_t *vt = smem + Sh::RING + (ev % NST) * Sh::TILE;
                         for (int x = r; x < (z1 - z0) * HALVES * 8; x += 128) {
-                            const int h = x / ((z1 - z0) * 8), y = x - h * (z1 - z0) * 8;
-                            *reinterpret_cast<uint4 *>(vt + h * Sh::SPAN + (z0 + y / 8) * 128 + (y % 8) * 16) =
+                            const int z = z0 + x / (HALVES * 8), y = x % (HALVES * 8);
+                            *reinterpret_cast<uint4 *>(vt + (z >> 3) * Sh::GROUP + (y >> 3) * 1024 + (z & 7) * 128 + (y & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_shared();
@@ -1072,71 +1073,89 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     }
                     a0 *= mul;
                     a1 *= mul;
-                    // O through shared memory, so that neighbouring lanes write
-                    // neighbouring bytes of a row: W columns at a time, in the
-                    // stage of the item's last K tile (all its products are
-                    // complete; the warps release it below).
-                    constexpr int W = D / 4, CH = W / 4, RPI = 32 / CH;  // columns, 16-byte pieces, rows a pass
-                    uint8_t *stage = smem + Sh::RING + ((e + 2 * max(nt - 1, 0)) % NST) * Sh::TILE + warp * (32 * W * 4);
-                    auto piece = [&](int row, int ch) {  // where piece ch of a row lies: eight lanes, eight banks' groups
-                        return stage + row * (W * 4) + ((ch ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 4);
-                    };
+                    if (nt > 0) {
+                        // O through shared memory, so that neighbouring lanes write
+                        // neighbouring bytes of a row: W columns at a time, in the
+                        // stage of the item's last K tile (all its products are
+                        // complete; the warps release it below).
+                        constexpr int W = D / 4, CH = W / 4, RPI = 32 / CH;  // columns, 16-byte pieces, rows a pass
+                        uint8_t *stage = smem + Sh::RING + ((e + 2 * (nt - 1)) % NST) * Sh::TILE + warp * (32 * W * 4);
+                        // where piece ch of a row lies: eight lanes meet no bank twice
+                        auto piece = [&](int row, int ch) {
+                            return stage + row * (W * 4) + ((ch ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 4);
+                        };
+                        const int my_ch = lane % CH;
+                        int to_row[CH];  // this lane's rows of out, one a pass
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) to_row[x] = __shfl_sync(0xffffffffu, at, x * RPI + lane / CH);
 #pragma unroll 1
-                    for (int k = 0; k < D; k += W) {
-                        uint32_t o[W];
-                        if (nt > 0) {
+                        for (int k = 0; k < D; k += W) {
+                            uint32_t o[W];
                             tmem_ldw<W>(to + k, o);
-                            tmem_wait_ld();
-                            tmem_loaded<W>(o);
-                        }
+                            if (join) {
+                                uint32_t o1[W];
+                                tmem_ldw<W>(to + 128 + k, o1);
+                                tmem_wait_ld();
+                                tmem_loaded<W>(o);
+                                tmem_loaded<W>(o1);
 #pragma unroll
-                        for (int x = 0; x < W; ++x) o[x] = empty ? 0u : __float_as_uint(__uint_as_float(o[x]) * a0);
-                        if (join) {
-                            uint32_t o1[W];
-                            tmem_ldw<W>(to + 128 + k, o1);
-                            tmem_wait_ld();
-                            tmem_loaded<W>(o1);
+                                for (int x = 0; x < W; ++x)
+                                    o[x] = __float_as_uint(fmaf(__uint_as_float(o1[x]), a1, __uint_as_float(o[x]) * a0));
+                            } else {
+                                tmem_wait_ld();
+                                tmem_loaded<W>(o);
 #pragma unroll
-                            for (int x = 0; x < W; ++x)
-                                if (!empty) o[x] = __float_as_uint(fmaf(__uint_as_float(o1[x]), a1, __uint_as_float(o[x])));
-                        }
-                        if (nt == 0) {  // no tokens and no stage: zeros, joined with the own tokens' state
-#pragma unroll 1
-                            for (int x = 0; x < W; x += 4) {
-                                const float4 f = p.own_out && at >= 0 ? __ldcg(reinterpret_cast<const float4 *>(p.own_out + (size_t)at * D + k + x))
-                                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (at >= 0) put4<QBF16>(p.out, (size_t)at * D + k + x, f.x * own, f.y * own, f.z * own, f.w * own);
+                                for (int x = 0; x < W; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a0);
+                            }
+                            if (empty) {
+#pragma unroll
+                                for (int x = 0; x < W; ++x) o[x] = 0u;
+                            }
+#pragma unroll
+                            for (int x = 0; x < CH; ++x)
+                                *reinterpret_cast<uint4 *>(piece(lane, x)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                            __syncwarp();
+                            float4 v[CH];
+#pragma unroll
+                            for (int x = 0; x < CH; ++x) v[x] = *reinterpret_cast<const float4 *>(piece(x * RPI + lane / CH, my_ch));
+                            const int col = k + 4 * my_ch;
+                            if (part) {
+#pragma unroll
+                                for (int x = 0; x < CH; ++x)
+                                    if (to_row[x] >= 0)
+                                        *reinterpret_cast<float4 *>(p.part_o + ((size_t)to_row[x] * p.S + it.split) * D + col) = v[x];
+                            } else {
+                                if (p.own_out) {
+                                    float4 f[CH];
+#pragma unroll
+                                    for (int x = 0; x < CH; ++x)
+                                        f[x] = to_row[x] >= 0 ? __ldcg(reinterpret_cast<const float4 *>(p.own_out + (size_t)to_row[x] * D + col))
+                                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                    for (int x = 0; x < CH; ++x) {
+                                        const float w = __shfl_sync(0xffffffffu, own, x * RPI + lane / CH);
+                                        v[x].x = fmaf(f[x].x, w, v[x].x);
+                                        v[x].y = fmaf(f[x].y, w, v[x].y);
+                                        v[x].z = fmaf(f[x].z, w, v[x].z);
+                                        v[x].w = fmaf(f[x].w, w, v[x].w);
+                                    }
+                                }
+#pragma unroll
+                                for (int x = 0; x < CH; ++x)
+                                    if (to_row[x] >= 0) put4<QBF16>(p.out, (size_t)to_row[x] * D + col, v[x].x, v[x].y, v[x].z, v[x].w);
                             }
                             __syncwarp();
-                            continue;
                         }
-#pragma unroll
-                        for (int x = 0; x < CH; ++x)
-                            *reinterpret_cast<uint4 *>(piece(lane, x)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-                        __syncwarp();
-#pragma unroll 4
-                        for (int x = 0; x < 32; x += RPI) {
-                            const int row = x + lane / CH, ch = lane % CH;
-                            const int to_row = __shfl_sync(0xffffffffu, at, row);
-                            const float w = __shfl_sync(0xffffffffu, own, row);
-                            float4 v = *reinterpret_cast<const float4 *>(piece(row, ch));
-                            if (to_row < 0) continue;
-                            if (part) {
-                                *reinterpret_cast<float4 *>(p.part_o + ((size_t)to_row * p.S + it.split) * D + k + 4 * ch) = v;
-                            } else {
-                                const size_t to_at = (size_t)to_row * D + k + 4 * ch;
-                                if (p.own_out) {
-                                    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p.own_out + to_at));
-                                    v.x = fmaf(f.x, w, v.x);
-                                    v.y = fmaf(f.y, w, v.y);
-                                    v.z = fmaf(f.z, w, v.z);
-                                    v.w = fmaf(f.w, w, v.w);
-                                }
-                                put4<QBF16>(p.out, to_at, v.x, v.y, v.z, v.w);
-                            }
+                    } else if (at >= 0) {
+                        // no tokens: the own tokens' state, or zeros
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 4) {
+                            const float4 f = p.own_out ? __ldcg(reinterpret_cast<const float4 *>(p.own_out + (size_t)at * D + k))
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                            put4<QBF16>(p.out, (size_t)at * D + k, f.x * own, f.y * own, f.z * own, f.w * own);
                         }
-                        __syncwarp();
                     }
+                    __syncwarp();
                 }
                 if (join) {
                     tmem_fence_before();
