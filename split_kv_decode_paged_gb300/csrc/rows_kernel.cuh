@@ -757,9 +757,9 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     if (more) qk(0, 0, sk);
                     v_here = k_here = false;
                     if (more) {
-                        v_here = mbar_try_wait(smem_u32(&c.kv_full[st]), par);
+                        v_here = mbar_test_wait(smem_u32(&c.kv_full[st]), par);
                         const uint32_t s2 = st + 1 == NST ? 0 : st + 1;
-                        if (j + 2 < nt) k_here = mbar_try_wait(smem_u32(&c.kv_full[s2]), s2 ? par : par ^ 1);
+                        if (j + 2 < nt) k_here = mbar_test_wait(smem_u32(&c.kv_full[s2]), s2 ? par : par ^ 1);
                     }
                     if (!(ok = output(1, sv, steps, j > 0, n_p1++))) break;
                     release(c.kv_empty[sv]);
