@@ -23,10 +23,15 @@
 //   warps 10-11     gather the query rows (any sequence, token and head order,
 //                   any token stride) into swizzled shared memory
 //   warps 12-15     (E4M3 pools) turn the loaded codes into 16-bit tiles
-// E4M3: codes of K become values of q's type and those of V bf16, exactly; K's
-// scale (one a page and KV head) multiplies the scores, V's the weights, before
-// their one rounding to bf16 (with f16 queries a pair of bf16, two products, so
-// that the output keeps f16's precision whatever the scales' range).
+// E4M3: codes become f16 values, exactly, and all products are in f16.  K's scale
+// (one a page and KV head) multiplies the scores, V's the weights before their
+// one rounding, relative to a power of two R at or above the chunk's largest
+// scale (O is multiplied by it at the end).  Where a chunk's scales differ by more
+// than kScaleRange, small ones times R^-1 would leave f16's normal range: V and
+// the weights are bf16 there (with f16 queries the weights are pairs of bf16,
+// two products).  A bf16 query row enters times a power of two that brings its
+// largest element below 2^15 (elements down to 2^-31 of it are exact), undone on
+// the scores.
 // Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
 // leaves the loop, which ends the others' waits the same way.
 #pragma once
@@ -46,6 +51,7 @@ constexpr int kTileRows = 128;   // query rows of one tile; two tiles an item
 constexpr int kItemSlots = 2;
 constexpr int kPartTokens = 96;  // weights handed to the product with V before the rest
 constexpr float kRowsLn2 = 0.6931471805599453f;
+constexpr float kScaleRange = 8.f;  // E4M3: ratio of V's scales within a chunk up to which the product is in f16
 constexpr float kSlack = 8.f;    // log2 headroom of the softmax reference
 
 struct RowsItem {
@@ -59,7 +65,7 @@ struct RowsItem {
     int split;
     int nsplit;
     int n0, g0;   // row0's token of the segment and head of the group
-    int pad;
+    float v_unit; // E4M3: R, or 0 where V's scales differ by too much for it
 };
 
 template <int KV, int D>
@@ -91,13 +97,15 @@ struct RowsShape {
 template <typename Sh>
 struct RowsControl {
     uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], pv_done[2];
-    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full, rows_empty, join_full, join_empty, drain;
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots], rows_full, rows_empty, rows_read, join_full, join_empty, drain;
     uint64_t kv_full[Sh::STAGES], kv_empty[Sh::STAGES];              // 16-bit tiles
     uint64_t raw_full[Sh::RAW_STAGES + 1], raw_empty[Sh::RAW_STAGES + 1];  // tiles of codes
     uint32_t tmem;
     int held[kItemSlots];      // softmax warps that are done with the stage held for the item's epilogue
     RowsItem item[kItemSlots];
-    int tok[2 * kTileRows];    // q token (sequence * T + token) of every row of the item, -1 past the end
+    // q token (sequence * T + token) of every row of the item, -1 past the end; E4M3
+    // under bf16 queries: with 127 plus the exponent of the row's factor above 22 bits
+    int tok[2 * kTileRows];
     float2 join[kTileRows];    // reference and denominator that tile 1's warps hand to tile 0's
     float raw_scale[Sh::RAW_STAGES + 1][16];  // of a stage's groups of 16 tokens: K's, then V's
     alignas(16) float scale[Sh::FP8 ? Sh::STAGES : 1][16];
@@ -153,6 +161,38 @@ __device__ __forceinline__ int small_div(int n, uint32_t magic) {
     return magic ? (int)__umulhi((uint32_t)n, magic) : n;
 }
 
+// RowsItem::v_unit of a chunk, by a whole warp: the scales of its pages.
+__device__ __forceinline__ float scale_unit(const RowsParams &p, const RowsItem &it, int lane) {
+    const int pages = (it.ntok + it.tok0 % p.page_size + p.page_size - 1) / p.page_size;
+    const int *table = p.block_table + (size_t)it.seg * p.max_blocks + it.tok0 / p.page_size;
+    float lo = INFINITY, hi = 0.f;
+    bool fine = true;
+    for (int k0 = lane; k0 < pages; k0 += 8 * 32) {
+        int pg[8];
+        float s[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) pg[u] = k0 + 32 * u < pages ? __ldg(table + k0 + 32 * u) : -1;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            s[u] = pg[u] >= 0 && pg[u] < p.num_pages ? __ldg(p.v_scale + (size_t)pg[u] * p.Hkv + it.kvh) : -1.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (pg[u] < 0 || pg[u] >= p.num_pages) continue;  // not loaded either
+            fine = fine && s[u] > 0.f;                        // no NaN
+            lo = fminf(lo, s[u]);
+            hi = fmaxf(hi, s[u]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    fine = __all_sync(0xffffffffu, fine) && lo > 1e-30f && hi < 1e30f && hi <= kScaleRange * lo;
+    // the power of two at or above hi
+    return fine ? __uint_as_float((__float_as_uint(hi) + 0x7fffffu) & 0xff800000u) : 0.f;
+}
+
 // Four neighbouring outputs, rounded to nearest even.
 template <bool BF16>
 __device__ __forceinline__ void put4(void *out, size_t at, float a, float b, float c, float d) {
@@ -180,8 +220,9 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                    const __grid_constant__ CUtensorMap tmv) {
     using Sh = RowsShape<KV, D>;
     constexpr bool FP8 = Sh::FP8;
-    constexpr bool P16 = KV == KV_F16;     // the product with V in f16 (else bf16)
-    constexpr bool PAIR = FP8 && !QBF16;   // weights as pairs of bf16
+    constexpr bool B16 = KV == KV_BF16;    // products in bf16 (else f16)
+    constexpr bool PAIR = FP8 && !QBF16;   // bf16 weights of an E4M3 chunk of wide scales as pairs
+    constexpr bool QSCALE = FP8 && QBF16;  // query rows scaled into f16
     static_assert(FP8 || QBF16 == (KV == KV_BF16), "16-bit pools have q's type");
     constexpr int HALVES = Sh::HALVES, NST = Sh::STAGES;
     constexpr uint32_t TMEM_S = 0, TMEM_O = 256;  // columns: S (and P) of both tiles, then O
@@ -211,6 +252,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         }
         mbar_init(smem_u32(&c.rows_full), 64);
         mbar_init(smem_u32(&c.rows_empty), 8);
+        mbar_init(smem_u32(&c.rows_read), 64);
         mbar_init(smem_u32(&c.join_full), 4);
         mbar_init(smem_u32(&c.join_empty), 4);
         c.held[0] = c.held[1] = 0;
@@ -323,19 +365,23 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         uint32_t e = 0;        // ring entries issued
         int n_item = 0;        // items published
         bool ok = true;
-        int claim = (int)blockIdx.x;
         if (p.stall_ns) {      // test hook: late loads
             const uint64_t t0 = global_timer_ns();
             while (global_timer_ns() - t0 < p.stall_ns) __nanosleep(1000);
         }
-        while (true) {
-            const int slot = n_item % kItemSlots;
-            if (!warp_wait(c.item_empty[slot], ((n_item / kItemSlots) & 1) ^ 1, limit)) {
-                ok = false;
-                break;
-            }
+        // The item of a claim (seg -1: there are no more), and a page id for every
+        // lane of its first 64 boxes.
+        RowsItem nx;
+        int npg0 = -1, npg1 = -1;
+        auto page_of = [&](const RowsItem &it, int k) -> int {
+            const int at = k << bsh;
+            return at < it.ntok ? __ldg(p.block_table + (size_t)it.seg * p.max_blocks + (it.tok0 + at) / p.page_size) : -1;
+        };
+        auto look_up = [&](int claim) {
             RowsItem it;
             it.seg = -1;
+            it.ntok = 0;
+            it.v_unit = 0.f;
             if (claim < total) {
                 // the lane's run that holds it, then the segment within the run
                 const unsigned has = __ballot_sync(0xffffffffu, run_before <= claim && claim < run_before + run_items);
@@ -401,6 +447,23 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     break;
                 }
             }
+            if (it.seg >= 0) {
+                npg0 = page_of(it, lane);
+                npg1 = page_of(it, 32 + lane);
+            }
+            if constexpr (FP8) {
+                if (it.ntok > 0) it.v_unit = scale_unit(p, it, lane);
+            }
+            nx = it;
+        };
+        look_up((int)blockIdx.x);
+        while (true) {
+            const int slot = n_item % kItemSlots;
+            if (!warp_wait(c.item_empty[slot], ((n_item / kItemSlots) & 1) ^ 1, limit)) {
+                ok = false;
+                break;
+            }
+            const RowsItem it = nx;
             if (lane == 0) {
                 c.item[slot] = it;
                 mbar_arrive(smem_u32(&c.item_full[slot]));
@@ -410,21 +473,18 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             if (it.seg < 0) break;
             int next = 0;
             if (lane == 0) next = atomicAdd(p.counters, 1);
-            // K and V tiles in turn; page ids 32 boxes ahead
+            // K and V tiles in turn, page ids 32 boxes ahead; the next item is
+            // looked up two tiles before the end, while the ring is full.
             const int nbox = (it.ntok + p.boxr - 1) >> bsh;
-            const int *table = p.block_table + (size_t)it.seg * p.max_blocks;
-            auto page_of = [&](int k) -> int {
-                if (k >= nbox) return -1;
-                const int tok = it.tok0 + (k << bsh);
-                return __ldg(table + tok / p.page_size);
-            };
-            int pg_cur = it.ntok > 0 ? page_of(lane) : -1, pg_nxt = it.ntok > 0 ? page_of(32 + lane) : -1;
-            int batch = 0;
+            const int ahead = max(0, (it.ntok - 1) / kTileTokens - 1) * BPT;
+            int pg_cur = npg0, pg_nxt = npg1, batch = 0;
+            if (it.ntok == 0) look_up((int)gridDim.x + __shfl_sync(0xffffffffu, next, 0));
             for (int k0 = 0; k0 < nbox && ok; k0 += BPT) {
+                if (k0 == ahead) look_up((int)gridDim.x + __shfl_sync(0xffffffffu, next, 0));
                 if (k0 >= (batch + 1) * 32) {
                     ++batch;
                     pg_cur = pg_nxt;
-                    pg_nxt = page_of((batch + 1) * 32 + lane);
+                    pg_nxt = page_of(it, (batch + 1) * 32 + lane);
                 }
                 const int pg = __shfl_sync(0xffffffffu, pg_cur, (k0 + (lane & (BPT - 1))) & 31);
                 const bool live = lane < BPT && k0 + lane < nbox;
@@ -473,7 +533,6 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     ++e;
                 }
             }
-            claim = (int)gridDim.x + __shfl_sync(0xffffffffu, next, 0);
             if (!ok) break;
         }
         grid_launch_dependents();
@@ -502,28 +561,32 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             const int r0 = D == 128 ? (t >> 4) * 2 + pr : t >> 2;
             const int half = D == 128 ? ((t >> 3) & 1) ^ pr : 0, ch = t & 3;
             int n_item = 0;
-            uint32_t e = 0;
+            uint32_t rs = 0, rpar = 0, st = 0, par = 0;  // stages and parities of the next entry
+            bool here = false;                           // both were ready at a look ahead
             bool ok = true;
             while (ok) {
                 const int slot = n_item % kItemSlots;
                 if (!(ok = warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit))) break;
                 const int sg = c.item[slot].seg, ntok = c.item[slot].ntok;
+                const bool wide = c.item[slot].v_unit == 0.f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
                 ++n_item;
                 if (sg < 0) break;
-                for (int x = 0; x < 2 * ((ntok + kTileTokens - 1) / kTileTokens); ++x, ++e) {
-                    const uint32_t rs = e % Sh::RAW_STAGES, st = e % NST;
+                const int entries = 2 * ((ntok + kTileTokens - 1) / kTileTokens);
+                for (int x = 0; x < entries; ++x) {
                     const bool is_v = x & 1;
                     const int nvalid = ntok - (x >> 1) * kTileTokens;
-                    if (!(ok = warp_wait(c.raw_full[rs], (e / Sh::RAW_STAGES) & 1, limit))) break;
-                    if (!(ok = warp_wait(c.kv_empty[st], ((e / NST) & 1) ^ 1, limit))) break;
+                    if (!__all_sync(0xffffffffu, here)) {
+                        if (!(ok = warp_wait(c.raw_full[rs], rpar, limit))) break;
+                        if (!(ok = warp_wait(c.kv_empty[st], par ^ 1, limit))) break;
+                    }
                     const uint8_t *src = smem + Sh::RAW_RING + rs * Sh::RAW + r0 * D + half * 64 + ch * 16;
                     uint8_t *dst = smem + Sh::RING + st * Sh::TILE + (r0 >> 3) * Sh::GROUP + half * 1024 + (r0 & 7) * 128;
                     // r & 7 is the same in every pass (ROWS is a multiple of 8)
                     const int c0 = ((2 * ch) ^ (r0 & 7)) << 4, c1 = ((2 * ch + 1) ^ (r0 & 7)) << 4;
-                    auto convert = [&](auto wide) {
-                        constexpr bool BF16 = decltype(wide)::value;
+                    auto convert = [&](auto to_bf16) {
+                        constexpr bool BF16 = decltype(to_bf16)::value;
 #pragma unroll
                         for (int r = 0; r < kTileTokens / ROWS; ++r) {
                             const uint4 w = *reinterpret_cast<const uint4 *>(src + r * ROWS * D);
@@ -542,7 +605,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             *reinterpret_cast<uint4 *>(row + c1) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     };
-                    if (QBF16 || is_v)
+                    if (is_v && wide)
                         convert(std::true_type());
                     else
                         convert(std::false_type());
@@ -557,11 +620,21 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             }
                     }
                     if (is_v && t < 16) c.scale[st][t] = c.raw_scale[rs][t];
+                    const uint32_t raw_done = smem_u32(&c.raw_empty[rs]), kv_done = smem_u32(&c.kv_full[st]);
+                    if (++rs == Sh::RAW_STAGES) {
+                        rs = 0;
+                        rpar ^= 1;
+                    }
+                    if (++st == NST) {
+                        st = 0;
+                        par ^= 1;
+                    }
+                    here = mbar_test_wait(smem_u32(&c.raw_full[rs]), rpar) && mbar_test_wait(smem_u32(&c.kv_empty[st]), par ^ 1);
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(smem_u32(&c.raw_empty[rs]));
-                        mbar_arrive(smem_u32(&c.kv_full[st]));
+                        mbar_arrive(kv_done);
+                        mbar_arrive(raw_done);
                     }
                 }
             }
@@ -609,8 +682,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 }
                 tok[r] = q;
             }
-            mbar_arrive(smem_u32(&c.rows_full));
-            bool ok = warp_wait(c.rows_full, n_item & 1, limit);
+            // what the loaders need of each other's rows; the softmax warps get them
+            // now, or with the rows' factors
+            mbar_arrive(smem_u32(QSCALE ? &c.rows_read : &c.rows_full));
+            bool ok = warp_wait(QSCALE ? c.rows_read : c.rows_full, n_item & 1, limit);
             const int tiles = it.nrows > kTileRows ? 2 : 1;
             for (int i = 0; i < tiles && ok; ++i) {
                 ok = warp_wait(c.q_empty[i], (n_q[i] & 1) ^ 1, limit);
@@ -619,6 +694,41 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     const int ch = t % CH;
                     const uint32_t dst = q_base + i * Sh::TILE + (ch / 8) * Sh::SPAN;
                     const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (size_t)it.kvh * p.G * D + ch * 8;
+                    if constexpr (QSCALE) {
+#pragma unroll 1
+                        for (int r0 = t / CH; r0 < kTileRows; r0 += 8 * (64 / CH)) {
+                            uint4 w[8];
+                            int q[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const int row = i * kTileRows + r0 + u * (64 / CH);
+                                q[u] = tok[row];
+                                const int g = it.g0 + row - small_div(it.g0 + row, p.g_magic) * p.G;
+                                w[u] = q[u] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + (size_t)q[u] * p.q_stride + g * D))
+                                                 : make_uint4(0, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                const int r = r0 + u * (64 / CH);
+                                uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w}, o[4];
+                                // exponent of the row's largest element, as a bf16 pattern
+                                uint32_t top = 0;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) top = max(top, max(in[k] & 0x7fffu, (in[k] >> 16) & 0x7fffu));
+#pragma unroll
+                                for (int o2 = CH / 2; o2 > 0; o2 >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o2));
+                                const int f = top ? 127 + max(-126, min(126, 141 - (int)(top >> 7))) : 127;
+                                const float up = __uint_as_float((uint32_t)f << 23);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    o[k] = pack_f16x2(__uint_as_float(in[k] << 16) * up, __uint_as_float(in[k] & 0xffff0000u) * up);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                             : "memory");
+                                if (ch == 0 && q[u] >= 0) tok[i * kTileRows + r] = q[u] | (f << 22);
+                            }
+                        }
+                    } else
 #pragma unroll 8
                     for (int r = t / CH; r < kTileRows; r += 64 / CH) {
                         const int row = i * kTileRows + r, q = tok[row];
@@ -639,6 +749,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 mbar_arrive(smem_u32(&c.q_full[i]));
                 ++n_q[i];
             }
+            if (QSCALE) mbar_arrive(smem_u32(&c.rows_full));
             if (!ok) rows_flag(p.status, FD_DEV_TIMEOUT);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
@@ -650,8 +761,9 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         // ============================================================ products
         // The whole warp goes round, so that descriptors and addresses stay in
         // uniform registers; one lane issues.
-        constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, QBF16, false);
-        constexpr uint32_t idesc_pv = mma_idesc(kTileRows, D, !P16, true);
+        constexpr uint32_t idesc_qk = mma_idesc(kTileRows, kTileTokens, B16, false);
+        constexpr uint32_t idesc_f16 = mma_idesc(kTileRows, D, false, true), idesc_bf16 = mma_idesc(kTileRows, D, true, true);
+        uint32_t idesc_pv = B16 ? idesc_bf16 : idesc_f16;
         const bool leader = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t q_desc = smem_desc(q_base, 16, 1024), k_desc = smem_desc(ring, 16, Sh::GROUP);
@@ -687,7 +799,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 } else {
                     for (int k = k0; k < k1; ++k) mma_ts(d, a0 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, k > 0 || more);
                 }
-                if constexpr (PAIR)  // the weights' low parts
+                if (PAIR && idesc_pv == idesc_bf16)  // the weights' low parts
                     for (int k = k0; k < k1; ++k) mma_ts(d, a0 + 64 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, true);
             }
         };
@@ -712,6 +824,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             const int sg = __shfl_sync(0xffffffffu, c.item[slot].seg, 0);
             const int nrows = __shfl_sync(0xffffffffu, c.item[slot].nrows, 0);
             const int ntok = __shfl_sync(0xffffffffu, c.item[slot].ntok, 0);
+            if constexpr (FP8) idesc_pv = __shfl_sync(0xffffffffu, c.item[slot].v_unit, 0) == 0.f ? idesc_bf16 : idesc_f16;
             if (lane == 0) mbar_arrive(smem_u32(&c.item_empty[slot]));
             ++n_item;
             if (sg < 0) break;
@@ -845,7 +958,16 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             // With one row tile both halves have its rows, and every other KV tile.
             const bool solo = it.nrows <= kTileRows;
             const int row0 = solo ? 0 : i * kTileRows, step = solo ? 2 : 1, j0 = solo ? i : 0;
-            const int q = c.tok[row0 + r];  // this thread's row
+            int q = c.tok[row0 + r];  // this thread's row
+            float row_sc = sc;
+            if constexpr (QSCALE) {
+                if (q >= 0) {
+                    row_sc = sc * __uint_as_float((uint32_t)(254 - (q >> 22)) << 23);  // the row's factor undone
+                    q &= (1 << 22) - 1;
+                }
+            }
+            const bool wide = FP8 && it.v_unit == 0.f;
+            const float v_inv = wide || !FP8 ? 1.f : 1.f / it.v_unit;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c.rows_empty));
             const bool warp_live = row0 + (warp & 3) * 32 < it.nrows;
@@ -909,7 +1031,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                 for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * fs[k >> 4]);
                             }
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) fs[k] = odd ? sc : sc * fs[k];
+                            for (int k = 0; k < 8; ++k) {
+                                fs[k] = odd ? row_sc : row_sc * fs[k];
+                                vs[k] *= v_inv;
+                            }
                         }
                         if (nvalid < kTileTokens) {
 #pragma unroll
@@ -963,7 +1088,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         uint64_t sum[2] = {0, 0};
                         // Weights of tokens [k0, k1) in place of their scores (words
                         // k0 / 2 ..), or straight to tensor memory where they are pairs.
-                        auto weights = [&](int k0, int k1) {
+                        auto weights = [&](auto in_bf16, int k0, int k1) {
+                            constexpr bool to_bf16 = decltype(in_bf16)::value;
                             [[maybe_unused]] uint32_t hi[16], lo[16];
 #pragma unroll
                             for (int k = k0; k < k1; k += 2) {
@@ -976,8 +1102,10 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                 if constexpr (FP8) {
                                     unpair(mul2(pair(x0, x1), pair(vs[k >> 4], vs[k >> 4])), x0, x1);
                                 }
-                                const uint32_t w = P16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
-                                if constexpr (PAIR) {
+                                if (B16 || (!PAIR && to_bf16)) {
+                                    s[k >> 1] = pack_bf16x2(x0, x1);
+                                } else if (to_bf16) {
+                                    const uint32_t w = pack_bf16x2(x0, x1);
                                     const int n = (k & 31) >> 1;
                                     hi[n] = w;
                                     lo[n] = pack_bf16x2(x0 - __uint_as_float(w << 16), x1 - __uint_as_float(w & 0xffff0000u));
@@ -986,23 +1114,34 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                         tmem_st16(ts + 64 + (k >> 5) * 16, lo);
                                     }
                                 } else {
-                                    s[k >> 1] = w;
+                                    s[k >> 1] = pack_f16x2(x0, x1);
                                 }
                             }
                         };
                         // The product with V starts on the first part while the
                         // rest is worked out.
-                        weights(0, kPartTokens);
-                        if constexpr (!PAIR) {
-                            tmem_st32(ts, s);
-                            tmem_st16(ts + 32, s + 32);
+                        auto hand_over = [&](auto in_bf16) {
+                            constexpr bool stored = PAIR && decltype(in_bf16)::value;  // by weights() itself
+                            weights(in_bf16, 0, kPartTokens);
+                            if constexpr (!stored) {
+                                tmem_st32(ts, s);
+                                tmem_st16(ts + 32, s + 32);
+                            }
+                            tmem_wait_st();
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&c.p_part[i]));
+                            weights(in_bf16, kPartTokens, kTileTokens);
+                            if constexpr (!stored) tmem_st16(ts + 48, s + 48);
+                        };
+                        if constexpr (FP8) {
+                            if (wide)
+                                hand_over(std::true_type());
+                            else
+                                hand_over(std::false_type());
+                        } else {
+                            hand_over(std::bool_constant<B16>());
                         }
-                        tmem_wait_st();
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&c.p_part[i]));
-                        weights(kPartTokens, kTileTokens);
-                        if constexpr (!PAIR) tmem_st16(ts + 48, s + 48);
                         float l0, l1;
                         unpair(add2(sum[0], sum[1]), l0, l1);
                         l += l0 + l1;
@@ -1071,6 +1210,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             if (p.lse) p.lse[at] = lse;
                         }
                     }
+                    if (FP8 && !wide) mul *= it.v_unit;
                     a0 *= mul;
                     a1 *= mul;
                     if (nt > 0) {

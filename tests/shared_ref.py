@@ -7,11 +7,13 @@ pages): what is read of them shows.
 
 Bounds.  A score's error (attend in cache_ref): e_s.  A weight exp(s - m) is
 then off by e_s relative (both s and m: 2 e_s), by the exponential's own few
-2^-22, and by its rounding for the product with V: half a step of the
-product's type (bf16 2^-8, f16 2^-11; E4M3 pools: bf16, with f16 queries pairs
-of bf16, 2^-16).  The sums over n tokens in fp32 add at most n 2^-24 each, in
-numerator and denominator.  Together, relative to sum p |v|:
-    r_p + 4 e_s + n 2^-23 + 2^-18
+2^-22, and by its rounding r_p for the product with V: half a step of the
+product's type (bf16 2^-8, f16 2^-11).  E4M3 pools: f16, or where the scales of a
+chunk's pages differ by more than 8 bf16, under f16 queries pairs of bf16 (2^-16).
+f16 weights below 2^-14 are off by up to 2^-25 instead, relative to a unit of at
+most twice the largest |v| can be: n 2^-24 max |v| in all.  The sums over n tokens
+in fp32 add at most n 2^-24 each, in numerator and denominator.  Together
+    sum p |v| (r_p + 4 e_s + n 2^-23 + 2^-18) + n 2^-24 max |v|
 and then the output's own rounding.  The log-sum-exp: 2 e_s + n 2^-24 + 2^-18
 (1 + |lse|).  Decode behind prefixes joins a second pass over the own tokens,
 whose f16 weights are rounded in numerator and denominator: 2^-10 there in
@@ -24,14 +26,15 @@ from tests.cache_ref import HALF_STEP, make_table, rounding, seq_tokens, values
 NAN = float("nan")
 
 
-def r_p(q_dtype, kv_dtype):
+def r_p(q_dtype, kv_dtype, wide=False):
     if kv_dtype == torch.float8_e4m3fn:
-        return 2.0 ** -16 if q_dtype == torch.float16 else 2.0 ** -8
+        return 2.0 ** -8 if wide and q_dtype == torch.bfloat16 else 2.0 ** -11
     return HALF_STEP[kv_dtype]
 
 
-def pools(gen, lens_tables, pages, ps, H, D, kv):
-    """K and V pools (and scales) with NaN wherever no table's live slot lies."""
+def pools(gen, lens_tables, pages, ps, H, D, kv, wide=False):
+    """K and V pools (and scales) with NaN wherever no table's live slot lies;
+    wide: E4M3 scales of very different sizes."""
     live = torch.zeros(pages, ps, dtype=torch.bool)
     for lens, table in lens_tables:
         for b, L in enumerate(lens):
@@ -46,6 +49,8 @@ def pools(gen, lens_tables, pages, ps, H, D, kv):
             continue
         scale = x.abs().amax(dim=(1, 3)) / 448.0 * (1 + torch.rand((pages, H), generator=gen))
         codes = (x / scale[:, None, :, None]).to(kv)
+        if wide:
+            scale = scale * torch.exp2(torch.randint(-6, 7, scale.shape, generator=gen).float())
         codes.view(torch.uint8)[~live] = 0x7f
         scale[~live.any(dim=1)] = NAN
         out += [codes, scale]
@@ -75,10 +80,11 @@ def attend_many(q, k, v, n_seen=None):
     return out.reshape(m, Hq, D), size.reshape(m, Hq, D), lse.reshape(m, Hq), err
 
 
-def check(out, lse, ref, n, r, dtype, lse_extra=0.0, what=""):
-    """out [m, Hq, D] and lse [m, Hq] against ref = attend_many's result."""
+def check(out, lse, ref, n, r, dtype, lse_extra=0.0, what="", vmax=0.0):
+    """out [m, Hq, D] and lse [m, Hq] against ref = attend_many's result; vmax:
+    the largest |v| where weights are f16."""
     o, size, l, err = ref
-    bound = size * (r + 4 * err + n * 2.0 ** -23 + 2.0 ** -18)
+    bound = size * (r + 4 * err + n * 2.0 ** -23 + 2.0 ** -18) + n * 2.0 ** -24 * vmax
     bound = bound + rounding(o.abs() + bound, dtype)
     off = (out.double() - o).abs()
     assert bool((off <= bound).all()), f"{what}: out off by {float((off - bound).max())} beyond its bound"
@@ -95,13 +101,14 @@ class Cross:
     """A seeded case of cross attention (CPU tensors)."""
 
     def __init__(self, seed, kv_lens, beams=1, T=1, Hq=4, Hkv=2, D=64, ps=16, kv=torch.bfloat16, q=None, q_lens=None,
-                 pad_cols=0, q_mult=1.5):
+                 pad_cols=0, q_mult=1.5, wide=False):
         gen = torch.Generator().manual_seed(seed)
         self.q_dtype = q or (kv if kv != torch.float8_e4m3fn else torch.bfloat16)
         self.kv_lens, self.beams, self.T, self.ps, self.kv = list(kv_lens), beams, T, ps, kv
         B = len(self.kv_lens) * beams
         self.table, pages, _ = make_table(gen, self.kv_lens, ps, extra=2, pad_cols=pad_cols)
-        self.k, self.ks, self.v, self.vs = pools(gen, [(self.kv_lens, self.table)], pages, ps, Hkv, D, kv)
+        self.k, self.ks, self.v, self.vs = pools(gen, [(self.kv_lens, self.table)], pages, ps, Hkv, D, kv, wide)
+        self.wide = wide
         self.q = (q_mult * torch.randn((B, T, Hq, D), generator=gen)).to(self.q_dtype)
         self.q_lens = None if q_lens is None else list(q_lens)
 
@@ -122,8 +129,9 @@ class Cross:
                 n = self.T if self.q_lens is None else self.q_lens[b]
                 if n:
                     ref = attend_many(self.q[b, :n].double(), kk, vv)
-                    check(out[b, :n], None if lse is None else lse[b, :n], ref, L, r_p(self.q_dtype, self.kv),
-                          self.q_dtype, what=f"{what} sequence {b}, length {L}")
+                    check(out[b, :n], None if lse is None else lse[b, :n], ref, L,
+                          r_p(self.q_dtype, self.kv, self.wide), self.q_dtype, what=f"{what} sequence {b}, length {L}",
+                          vmax=float(vv.abs().max()) if L and self.kv != torch.bfloat16 else 0.0)
                 if untouched is not None and n < self.T:
                     assert bool((out[b, n:] == untouched).all()) and bool((lse[b, n:] == untouched).all()), (what, b)
 
@@ -167,4 +175,5 @@ class Prefix:
             seen = [kk.shape[0] - self.T + 1 + t for t in range(self.T)]
             ref = attend_many(self.q[b].double(), kk, vv, seen)
             check(out[b], None if lse is None else lse[b], ref, kk.shape[0], r, self.q_dtype,
-                  lse_extra=2.0 ** -11 if narrow else 0.0, what=f"{what} sequence {b}")
+                  lse_extra=2.0 ** -11 if narrow else 0.0, what=f"{what} sequence {b}",
+                  vmax=float(vv.abs().max()) if len(vv) and narrow else 0.0)

@@ -94,6 +94,51 @@ def test_strided_queries_and_no_lse(fdlib):
     c.verify(out, None, what="strided")
 
 
+@pytest.mark.parametrize("q", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("D,T", [(64, 40), (128, 3), (128, 90)])
+def test_scales_of_very_different_sizes(fdlib, q, D, T):
+    """E4M3 pages whose scales differ by up to 2^12, some rows all alike."""
+    c = Cross(11, [700, 16, 129, 1], T=T, Hq=6, Hkv=2, D=D, kv=E4M3, q=q, ps=32, wide=True, q_mult=0.1)
+    for splits in (1, 3):
+        out, lse, _ = run(c, num_splits=splits)
+        c.verify(out, lse, what="wide scales")
+
+
+def test_scales_that_are_not_positive(fdlib):
+    """A page of negative scales and one of zeros."""
+    c = Cross(12, [300, 90], T=70, Hq=4, Hkv=2, D=64, kv=E4M3, ps=32)
+    c.ks[int(c.table[0, 2])] *= -1
+    c.vs[int(c.table[0, 3])] *= -1
+    c.ks[int(c.table[1, 2])] = 0  # the page the second row ends in
+    c.vs[int(c.table[0, 5])] = 0
+    c.wide = True
+    out, lse, _ = run(c)
+    c.verify(out, lse, what="scales")
+
+
+@pytest.mark.parametrize("mult", [1e-30, 1e-6, 3e4, 1e20])
+def test_query_range_over_e4m3(fdlib, mult):
+    """bf16 queries far from f16's range over E4M3 keys of the opposite size."""
+    c = Cross(13, [200, 77], T=70, Hq=4, Hkv=2, D=64, kv=E4M3, ps=16)
+    c.q = (c.q.float() * mult).to(BF16)
+    c.ks /= mult
+    out, lse, _ = run(c)
+    c.verify(out, lse, what="query range")
+
+
+def test_nan_codes_stay_in_their_head(fdlib):
+    """A live NaN code reaches every row of its KV head and none of the others."""
+    c = Cross(14, [200, 77], T=3, Hq=4, Hkv=2, D=64, kv=E4M3, ps=16)
+    ref, _, _ = run(c)
+    c.v.view(torch.uint8)[int(c.table[0, 1]), 3, 1, 5] = 0x7f
+    c.k.view(torch.uint8)[int(c.table[1, 0]), 2, 0, 9] = 0xff
+    out, lse, _ = run(c)
+    assert bool(torch.isnan(out[0, :, 2:, 5]).all()) and bool(torch.isnan(out[1, :, :2]).all())
+    out[0, :, 2:, 5], ref[0, :, 2:, 5] = 0, 0
+    out[1, :, :2], ref[1, :, :2] = 0, 0
+    assert torch.equal(out, ref)
+
+
 def test_large_scores(fdlib):
     """Scores of some hundreds: the running maximum moves, nothing overflows."""
     for kv in (F16, BF16):
