@@ -603,7 +603,11 @@ typedef struct {
     size_t ws_partial_o;  /* byte offsets inside the workspace                    */
     size_t ws_partial_md;
     size_t ws_counters;
-    int reserved[4];      /* 0                                                    */
+    size_t ws_few;
+    fd_plan_t few;        /* of the decode kernel, which takes calls of up to 16
+                             query rows a KV head (see fd_plan_cross)             */
+    int has_few;          /* whether there is one                                 */
+    int reserved[3];      /* fd_plan_prefix marks its plans here                  */
 } fd_cross_plan_t;
 
 /* Plan a cross-attention call.
@@ -612,7 +616,10 @@ typedef struct {
  *                 out_dtype has to be q_dtype
  *   kv_lens_host  HOST int32 [B]: the lengths the work is split for
  *   options       may be NULL (one token, one beam)
- * B * beams * T is at most 2^22, and times Hq at most 2^28. */
+ * B * beams * T is at most 2^22, and times Hq at most 2^28; Hq / Hkv at most
+ * 2^15.  Where a KV head has at most 16 query rows (beams * T * Hq / Hkv; and B *
+ * beams * T at most 8192) the plan also holds one of the decode kernel, which
+ * then takes the calls without q_lens and with q dense. */
 fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
                         const fd_cross_options *options, fd_cross_plan_t *plan);
 

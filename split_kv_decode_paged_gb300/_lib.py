@@ -11,8 +11,8 @@ computation happens here and there is no fallback: if libfd.so is missing or
 fails to load, every call raises.
 
 The calls a serving loop makes once a layer and step (append_kv_norm,
-evict_kv, PagedDecoder.decode_weights, DiffDecoder) first try fast(), the same
-marshalling in C++; it hands back every call that is not the ordinary case,
+evict_kv, PagedDecoder.decode_weights, DiffDecoder, CrossDecoder,
+PrefixDecoder) first try fast(), the same marshalling in C++; it hands back every call that is not the ordinary case,
 and the functions here then check it, name what is wrong and raise.  A call whose
 launches failed is not made a second time: it raises FdError there.
 """
@@ -102,8 +102,9 @@ class FdCrossPlan(ctypes.Structure):
                 [(n, ctypes.c_int) for n in ("kv_rows", "seqs", "tokens", "beams", "num_splits", "chunk_tokens",
                                              "capacity_tokens", "tile_rows", "grid_ctas", "num_sms", "timeout_us",
                                              "debug_stall_us")] +
-                [(n, ctypes.c_size_t) for n in ("workspace_bytes", "ws_partial_o", "ws_partial_md", "ws_counters")] +
-                [("reserved", ctypes.c_int * 4)])
+                [(n, ctypes.c_size_t) for n in ("workspace_bytes", "ws_partial_o", "ws_partial_md", "ws_counters",
+                                                "ws_few")] +
+                [("few", FdPlan), ("has_few", ctypes.c_int), ("reserved", ctypes.c_int * 3)])
 
 
 class FdPrefixPlan(ctypes.Structure):
@@ -202,7 +203,8 @@ def fast():
             _fast = False
         else:
             at = [ctypes.cast(f, ctypes.c_void_p).value for f in
-                  (lib.fd_append_kv_norm, lib.fd_evict_kv, lib.fd_decode_paged_weights, lib.fd_decode_paged_diff)]
+                  (lib.fd_append_kv_norm, lib.fd_evict_kv, lib.fd_decode_paged_weights, lib.fd_decode_paged_diff,
+                   lib.fd_cross_paged, lib.fd_decode_paged_prefix)]
             _fd_torch.init(*at, FdError)
             _fast = _fd_torch
     return _fast

@@ -20,7 +20,7 @@ BINDING = os.path.join(HERE, "_fd_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["fd_api.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e4m3.cu", "decode_scores_f16.cu",
            "decode_scores_bf16.cu", "decode_scores_e4m3.cu", "decode_diff_f16.cu", "decode_diff_bf16.cu",
-           "decode_diff_e4m3.cu", "merge.cu", "append.cu",
+           "decode_diff_e4m3.cu", "decode_state_f16.cu", "decode_state_bf16.cu", "decode_state_e4m3.cu", "merge.cu", "append.cu",
            "append_norm.cu", "weights.cu", "evict.cu", "noalloc.cu", "rows.cu", "rows_api.cu"]
 
 

@@ -547,7 +547,8 @@ __device__ __noinline__ void build_dispatch_tables_coop(const DecodeParams &p, i
 // MODE kScores: every score (log2 units, -inf where hidden) also goes to
 // DecodeParams::scores, for the attention-weight totals (weights.cu).  MODE
 // kDiff: differential attention (two padded query rows a head, see
-// kQRowsPerHead; the pair's difference and norm in the epilogue).  In both the
+// kQRowsPerHead; the pair's difference and norm in the epilogue).  In both, and
+// in kState (a state that another pass over other tokens joins, by its lse), the
 // denominator sums the weights before they are rounded for P.V: their
 // results go by the lse itself (a total of weights, a difference of two
 // outputs), where a plain decode's output is a ratio in which the rounding of
@@ -1315,13 +1316,13 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 }
             }
             uint32_t pb[SUBT][NT][2];
-            // Low parts of the weights (P = hi + lo): bf16 V, and f16 products
-            // outside the plain decode.  There the denominator sums the weights
+            // Low parts of the weights (P = hi + lo): bf16 V, and the f16 products of
+            // weight totals and of maps.  There the denominator sums the weights
             // unrounded (see MODE), so the roundings of 11 bits alone would not
             // cancel: up to 2^-12 of sum p |v|, which a difference of similar
             // maps and its norm scale up and an fp32 output shows.
             uint32_t pl[SUBT][NT][2];
-            constexpr bool kPair = KV == KV_BF16 || MODE != kPlain;
+            constexpr bool kPair = KV == KV_BF16 || MODE == kScores || MODE == kDiff;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float mn0 = mrow[n][0], mn1 = mrow[n][1];

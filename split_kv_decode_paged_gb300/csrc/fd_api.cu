@@ -19,12 +19,14 @@ using LaunchDecode = cudaError_t(const fd_problem &, const KernelShape &, const 
 LaunchDecode launch_decode_f16, launch_decode_bf16, launch_decode_e4m3;
 LaunchDecode launch_decode_scores_f16, launch_decode_scores_bf16, launch_decode_scores_e4m3;  // scores out (weights.cu)
 LaunchDecode launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3;        // differential attention
+LaunchDecode launch_decode_state_f16, launch_decode_state_bf16, launch_decode_state_e4m3;     // states that others join
 // Resident CTAs per SM of the one-token instance of a shape with that much
 // dynamic shared memory, its epilogue scratch in a stage or not (needs a device).
 using DecodeOccupancy = cudaError_t(const fd_problem &, const KernelShape &, size_t, bool, int *);
 DecodeOccupancy decode_occupancy_f16, decode_occupancy_bf16, decode_occupancy_e4m3;
 DecodeOccupancy decode_occupancy_scores_f16, decode_occupancy_scores_bf16, decode_occupancy_scores_e4m3;
 DecodeOccupancy decode_occupancy_diff_f16, decode_occupancy_diff_bf16, decode_occupancy_diff_e4m3;
+DecodeOccupancy decode_occupancy_state_f16, decode_occupancy_state_bf16, decode_occupancy_state_e4m3;
 size_t decode_smem_f16(const fd_problem &, const KernelShape &, int, bool);
 size_t decode_smem_bf16(const fd_problem &, const KernelShape &, int, bool);
 size_t decode_smem_e4m3(const fd_problem &, const KernelShape &, int, bool);
@@ -80,8 +82,10 @@ constexpr DecodeInstances kInstances[] = {
     {launch_decode_scores_f16, launch_decode_scores_bf16, launch_decode_scores_e4m3, decode_occupancy_scores_f16,
      decode_occupancy_scores_bf16, decode_occupancy_scores_e4m3},
     {launch_decode_diff_f16, launch_decode_diff_bf16, launch_decode_diff_e4m3, decode_occupancy_diff_f16,
-     decode_occupancy_diff_bf16, decode_occupancy_diff_e4m3}};
-static_assert(kPlain == 0 && kScores == 1 && kDiff == 2, "kInstances goes by MODE");
+     decode_occupancy_diff_bf16, decode_occupancy_diff_e4m3},
+    {launch_decode_state_f16, launch_decode_state_bf16, launch_decode_state_e4m3, decode_occupancy_state_f16,
+     decode_occupancy_state_bf16, decode_occupancy_state_e4m3}};
+static_assert(kPlain == 0 && kScores == 1 && kDiff == 2 && kState == 3, "kInstances goes by MODE");
 
 }  // namespace
 
@@ -363,8 +367,9 @@ fd_status fd_status_from_device(int32_t w) {
 namespace {
 
 // fd_plan for the kernel instances of a mode (kDiff: problem has the padded heads).
+// fold_rows > 0: that many q sequences read every KV row whole.
 fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
-                    fd_plan_t *plan, int mode) {
+                    fd_plan_t *plan, int mode, int fold_rows = 0) {
     if (!plan || !seq_lens_host) return FD_ERR_INVALID_ARG;
     fd_status st = validate_problem(problem);
     if (st != FD_OK) return st;
@@ -378,11 +383,12 @@ fd_status plan_impl(const fd_problem *problem, const int32_t *seq_lens_host, con
         return FD_ERR_INVALID_ARG;
     const int q_len = std::max(1, opt.q_len);
     if (q_len > 1 && opt.shared_kv) return FD_ERR_UNSUPPORTED;
-    if ((long long)problem->B * q_len > kMaxBatch) return FD_ERR_UNSUPPORTED;
+    if (fold_rows > 0 && (q_len > 1 || opt.shared_kv)) return FD_ERR_UNSUPPORTED;
+    if ((long long)problem->B * std::max(q_len, fold_rows) > kMaxBatch) return FD_ERR_UNSUPPORTED;
     // shared_kv: every q sequence attends KV row 0 (one block-table row, one
     // seq_lens entry): the B*G q rows of a KV head are sliced into items.
     // q_len > 1: the q_len query tokens of a sequence fold onto its KV row.
-    const int fold = opt.shared_kv ? problem->B : q_len;
+    const int fold = fold_rows > 0 ? fold_rows : opt.shared_kv ? problem->B : q_len;
     const int kv_rows = opt.shared_kv ? 1 : problem->B;
     const double margin = (opt.split_margin_pct > 0 ? opt.split_margin_pct : kDefaultSplitMarginPct) / 100.0;
     const fd_problem &p = *problem;
@@ -805,6 +811,25 @@ fd_status decode_impl(const fd_plan_t *plan, const void *q, const void *k_pages,
 }
 
 }  // namespace
+
+fd_status fd::plan_state(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options,
+                         int fold, fd_plan_t *plan) {
+    try {
+        return plan_impl(problem, seq_lens_host, options, plan, kState, fold);
+    } catch (...) {  // no memory for the lengths
+        return FD_ERR_UNSUPPORTED;
+    }
+}
+
+fd_status fd::decode_state(const fd_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
+                           const float *k_scale, const float *v_scale, const int32_t *block_table,
+                           const int32_t *seq_lens, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           int32_t *status_dev, void *stream) {
+    DecodeMode mode;
+    mode.instances = kState;
+    return decode_impl(plan, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, nullptr, out, lse, workspace,
+                       workspace_bytes, status_dev, stream, mode);
+}
 
 extern "C" {
 

@@ -181,8 +181,10 @@ struct AppendParams {
 };
 
 // MODE of a decode kernel instance: the plain decode, the one that also writes
-// its scores (attention-weight totals), differential attention.
-constexpr int kPlain = 0, kScores = 1, kDiff = 2;
+// its scores (attention-weight totals), differential attention, the plain decode
+// whose results join other states or go by their lse (its denominators sum the
+// weights unrounded).
+constexpr int kPlain = 0, kScores = 1, kDiff = 2, kState = 3;
 
 // Kernel configuration chosen at plan time.
 struct KernelShape {
@@ -212,6 +214,14 @@ cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
 cudaError_t launch_rows(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream);
 // The merge of the rows that it left in partial states.
 cudaError_t launch_rows_merge(const RowsParams &p, cudaStream_t stream);
+
+// The decode kernel's kState instances over KV rows that `fold` query rows a head
+// read whole (fold 0: as the options say): fd_plan and fd_decode_paged for them.
+fd_status plan_state(const fd_problem *problem, const int32_t *seq_lens_host, const fd_plan_options *options, int fold,
+                     fd_plan_t *plan);
+fd_status decode_state(const fd_plan_t *plan, const void *q, const void *k_pages, const void *v_pages,
+                       const float *k_scale, const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                       void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *status_dev, void *stream);
 
 // Checks and encodings that the entry points share (fd_api.cu).
 struct DeviceInfo {

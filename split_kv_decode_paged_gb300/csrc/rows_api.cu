@@ -19,6 +19,7 @@ constexpr long long kMaxRows = 1LL << 28;    // query tokens * heads
 constexpr int kMaxGroup = 1 << 15;           // query heads of a KV head
 constexpr int kMaxRowSms = 1 << 16;
 constexpr uint64_t kRowsTimeoutNs = 2000000000ull;  // 2 s limit on any device-side wait
+constexpr int kFewRows = 16;  // query rows of a KV head up to which the decode kernel takes a cross-attention call
 constexpr int kPlanCross = 2, kPlanPrefix = 3;      // fd_cross_plan_t::reserved[0]
 
 bool on(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -232,6 +233,16 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
         plan.ws_counters - plan.ws_partial_md < 2 * rows * S * sizeof(float) || plan.workspace_bytes < plan.ws_counters ||
         plan.workspace_bytes - plan.ws_counters < 256 + (S ? rows * sizeof(int) : 0))
         return false;
+    if (plan.has_few) {
+        const fd_plan_t &f = plan.few;
+        if (kind != kPlanCross || f.kv_rows != plan.kv_rows || f.row_fold != plan.beams * plan.tokens ||
+            f.problem.Hq != p.Hq || f.problem.Hkv != p.Hkv || f.problem.D != p.D || f.problem.out_dtype != p.out_dtype ||
+            f.problem.q_dtype != p.q_dtype || f.problem.kv_dtype != p.kv_dtype || f.problem.page_size != p.page_size ||
+            f.problem.num_pages != p.num_pages || f.problem.max_blocks_per_seq != p.max_blocks_per_seq ||
+            plan.ws_few % 256 || plan.workspace_bytes < plan.ws_few || plan.workspace_bytes - plan.ws_few < f.workspace_bytes ||
+            plan.ws_few < plan.ws_counters || plan.ws_few - plan.ws_counters < 256 + (S ? rows * sizeof(int) : 0))
+            return false;
+    }
     if (plan.capacity_tokens < 1 || plan.capacity_tokens > (long long)p.page_size * p.max_blocks_per_seq) return false;
     return plan.timeout_us >= 0 && plan.debug_stall_us >= 0 && plan.debug_stall_us <= 1000000;
 }
@@ -267,6 +278,25 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host, 
     if (r != FD_OK) return r;
     plan->beams = opt.beams;
     plan->reserved[0] = kPlanCross;
+    // Few query rows: the decode kernel, whose 8 or 16 columns of queries waste
+    // less of an SM's time on them than tiles of 128 rows, and which issues its
+    // loads further ahead (kFewRows has both sides' times).
+    const long long few = (long long)opt.beams * opt.tokens * (problem->Hq / problem->Hkv);
+    if (few <= kFewRows && (long long)problem->B * opt.beams * opt.tokens <= kMaxBatch) {
+        fd_plan_options po = {};
+        po.fuse_merge = 1;
+        po.num_splits = opt.num_splits;
+        po.num_sms = opt.num_sms;
+        po.max_seq_len = opt.max_kv_len;
+        po.timeout_us = opt.timeout_us;
+        po.debug_stall_us = opt.debug_stall_us;
+        po.debug_stall_role = opt.debug_stall_us > 0 ? 1 : 0;
+        if (plan_state(problem, kv_lens_host, &po, opt.beams * opt.tokens, &plan->few) == FD_OK) {
+            plan->has_few = 1;
+            plan->ws_few = plan->workspace_bytes;
+            plan->workspace_bytes += up256(plan->few.workspace_bytes);
+        }
+    }
     return FD_OK;
 }
 
@@ -283,6 +313,10 @@ fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q
         return FD_ERR_INVALID_ARG;
     if (q_stride < (long long)p.Hq * p.D || q_stride % 8) return FD_ERR_INVALID_ARG;
     if (workspace_bytes < plan->workspace_bytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+    if (plan->has_few && !q_lens && q_stride == (long long)p.Hq * p.D)
+        return decode_state(&plan->few, q, k_pages, v_pages, k_scale, v_scale, block_table, kv_lens, out, lse,
+                            static_cast<uint8_t *>(workspace) + plan->ws_few, plan->few.workspace_bytes, status_dev,
+                            stream);
     RowsParams rp;
     std::memset(&rp, 0, sizeof(rp));
     rp.q = q;
@@ -320,11 +354,7 @@ fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host
     std::memset(plan, 0, sizeof(*plan));
     fd_problem po = p;
     po.out_dtype = FD_F32;  // a state that the other pass joins
-    fd_status r = FD_ERR_UNSUPPORTED;
-    try {
-        r = fd_plan(&po, seq_lens_host, &own, &plan->own);
-    } catch (...) {  // no memory for the lengths
-    }
+    fd_status r = plan_state(&po, seq_lens_host, &own, 0, &plan->own);
     if (r != FD_OK) return r;
     opt.num_sms = own.num_sms;
     opt.timeout_us = own.timeout_us;
@@ -382,9 +412,9 @@ fd_status fd_decode_paged_prefix(const fd_prefix_plan_t *plan, const void *q, co
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *own_out = reinterpret_cast<float *>(ws + plan->ws_own_out);
     float *own_lse = reinterpret_cast<float *>(ws + plan->ws_own_lse);
-    const fd_status st = fd_decode_paged(&plan->own, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
-                                         own_out, own_lse, ws + plan->ws_own, plan->own.workspace_bytes, status_dev,
-                                         stream);
+    const fd_status st = decode_state(&plan->own, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens,
+                                      own_out, own_lse, ws + plan->ws_own, plan->own.workspace_bytes, status_dev,
+                                      stream);
     if (st != FD_OK) return st;
     RowsParams rp;
     std::memset(&rp, 0, sizeof(rp));

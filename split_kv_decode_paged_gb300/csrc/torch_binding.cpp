@@ -1,6 +1,6 @@
 // torch_binding.cpp -- the short way from torch tensors to libfd for the calls
 // that a serving loop makes once a layer and step: append_kv_norm, evict_kv,
-// PagedDecoder.decode_weights and DiffDecoder.  A call's arguments are checked
+// PagedDecoder.decode_weights, DiffDecoder, CrossDecoder and PrefixDecoder.  A call's arguments are checked
 // and its outputs allocated here instead of in Python, which took 15 to 25 us
 // of host time a call around 4 us of launches.
 //
@@ -28,6 +28,8 @@ decltype(&fd_append_kv_norm) g_append = nullptr;
 decltype(&fd_evict_kv) g_evict = nullptr;
 decltype(&fd_decode_paged_weights) g_weights = nullptr;
 decltype(&fd_decode_paged_diff) g_diff = nullptr;
+decltype(&fd_cross_paged) g_cross = nullptr;
+decltype(&fd_decode_paged_prefix) g_prefix = nullptr;
 
 PyObject *g_error = nullptr;  // FdError
 
@@ -431,6 +433,74 @@ PyObject *diff(PyObject *const *a) {
     return tuple_of({out.object(), l});
 }
 
+// plan, q, k_pages, v_pages, block_table, kv_lens, q_lens, k_scale, v_scale,
+// out, lse, want_lse, workspace, status
+PyObject *cross(PyObject *const *a) {
+    Call c;
+    const void *at = PyLong_AsVoidPtr(a[0]);
+    if (!at) throw Other();
+    const fd_cross_plan_t &pl = *static_cast<const fd_cross_plan_t *>(at);
+    const fd_problem &p = pl.problem;
+    const bool flat = pl.tokens == 1 && c.tensor(a[1]).dim() == 3;
+    const int64_t s4[4] = {pl.seqs, pl.tokens, p.Hq, p.D}, s3[3] = {pl.seqs, p.Hq, p.D};
+    const at::IntArrayRef shape = flat ? at::IntArrayRef(s3, 3) : at::IntArrayRef(s4, 4);
+    long long stride = 0;
+    const void *q = c.rows(a[1], torch_type(p.q_dtype), shape, &stride);
+    const Pools po = pools(c, p, a[2], a[3], a[7], a[8]);
+    const int32_t *bt = c.data<const int32_t>(a[4], at::kInt, {pl.kv_rows, p.max_blocks_per_seq});
+    const int32_t *kl = c.data<const int32_t>(a[5], at::kInt, {pl.kv_rows});
+    const int32_t *ql = c.maybe<const int32_t>(a[6], at::kInt, {pl.seqs});
+    size_t ws_bytes = 0;
+    void *ws = c.bytes(a[12], &ws_bytes);
+    int32_t *status = c.status(a[13]);
+    void *stream = c.stream();
+    const bool want_lse = a[10] != Py_None || as_bool(a[11]);
+    const Output out = output(c, a[9], shape, torch_type(p.out_dtype));
+    Output lse;
+    if (want_lse) lse = output(c, a[10], shape.slice(0, shape.size() - 1), at::kFloat);
+    run([&] {
+        return g_cross(&pl, q, stride, ql, po.k, po.v, po.ks, po.vs, bt, kl, out.ptr, static_cast<float *>(lse.ptr), ws,
+                       ws_bytes, status, stream);
+    });
+    PyObject *l = want_lse ? lse.object() : Py_None;
+    if (!want_lse) Py_INCREF(Py_None);
+    return tuple_of({out.object(), l});
+}
+
+// plan, q, k_pages, v_pages, prefix_table, prefix_lens, members, offsets,
+// block_table, seq_lens, k_scale, v_scale, out, lse, want_lse, workspace, status
+PyObject *prefix(PyObject *const *a) {
+    Call c;
+    const void *at = PyLong_AsVoidPtr(a[0]);
+    if (!at) throw Other();
+    const fd_prefix_plan_t &pp = *static_cast<const fd_prefix_plan_t *>(at);
+    const fd_plan_t &pl = pp.own;
+    const fd_problem &p = pp.shared.problem;  // its block table is the prefixes'
+    const void *q = query(c, pl, a[1], p.Hq);
+    const Pools po = pools(c, p, a[2], a[3], a[10], a[11]);
+    const int32_t *pt = c.data<const int32_t>(a[4], at::kInt, {pp.prefixes, p.max_blocks_per_seq});
+    const int32_t *ln = c.data<const int32_t>(a[5], at::kInt, {pp.prefixes});
+    const int32_t *mb = c.data<const int32_t>(a[6], at::kInt, {pp.shared.seqs});
+    const int32_t *of = c.data<const int32_t>(a[7], at::kInt, {pp.prefixes + 1});
+    const int32_t *bt = c.data<const int32_t>(a[8], at::kInt, {pl.kv_rows, pl.problem.max_blocks_per_seq});
+    const int32_t *sl = c.data<const int32_t>(a[9], at::kInt, {pl.kv_rows});
+    size_t ws_bytes = 0;
+    void *ws = c.bytes(a[15], &ws_bytes);
+    int32_t *status = c.status(a[16]);
+    void *stream = c.stream();
+    const bool want_lse = a[13] != Py_None || as_bool(a[14]);
+    const Output out = output(c, a[12], Shape(pl, {p.Hq, p.D}), torch_type(p.out_dtype));
+    Output lse;
+    if (want_lse) lse = output(c, a[13], Shape(pl, {p.Hq}), at::kFloat);
+    run([&] {
+        return g_prefix(&pp, q, po.k, po.v, po.ks, po.vs, pt, ln, mb, of, bt, sl, out.ptr, static_cast<float *>(lse.ptr),
+                        ws, ws_bytes, status, stream);
+    });
+    PyObject *l = want_lse ? lse.object() : Py_None;
+    if (!want_lse) Py_INCREF(Py_None);
+    return tuple_of({out.object(), l});
+}
+
 PyObject *raise(fd_status status, const char *what) {
     PyObject *e = PyObject_CallFunction(g_error, "is", (int)status, what);
     if (e) {
@@ -441,7 +511,7 @@ PyObject *raise(fd_status status, const char *what) {
 }
 
 constexpr char kAppend[] = "fd_append_kv_norm", kEvict[] = "fd_evict_kv", kWeights[] = "fd_decode_paged_weights",
-               kDiff[] = "fd_decode_paged_diff";
+               kDiff[] = "fd_decode_paged_diff", kCross[] = "fd_cross_paged", kPrefix[] = "fd_decode_paged_prefix";
 
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N, const char *NAME>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -458,9 +528,9 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyObject *init(PyObject *, PyObject *args) {
-    unsigned long long f[4];
+    unsigned long long f[6];
     PyObject *error;
-    if (!PyArg_ParseTuple(args, "KKKKO", &f[0], &f[1], &f[2], &f[3], &error)) return nullptr;
+    if (!PyArg_ParseTuple(args, "KKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &error)) return nullptr;
     Py_INCREF(error);
     Py_XDECREF(g_error);
     g_error = error;
@@ -468,6 +538,8 @@ PyObject *init(PyObject *, PyObject *args) {
     g_evict = reinterpret_cast<decltype(g_evict)>(f[1]);
     g_weights = reinterpret_cast<decltype(g_weights)>(f[2]);
     g_diff = reinterpret_cast<decltype(g_diff)>(f[3]);
+    g_cross = reinterpret_cast<decltype(g_cross)>(f[4]);
+    g_prefix = reinterpret_cast<decltype(g_prefix)>(f[5]);
     Py_RETURN_NONE;
 }
 
@@ -478,6 +550,8 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, "addresses of libfd's entr
                          FD_FAST("evict_kv", evict, 13, kEvict),
                          FD_FAST("decode_weights", weights, 16, kWeights),
                          FD_FAST("decode_diff", diff, 17, kDiff),
+                         FD_FAST("cross", cross, 14, kCross),
+                         FD_FAST("decode_prefix", prefix, 17, kPrefix),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fd_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -6,6 +6,8 @@ All compute runs in libfd.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -69,6 +71,13 @@ class CrossDecoder(_Planned):
         """q's tokens may lie at a stride (a slice of a fused projection);
         q_lens int32 [B]: tokens of each sequence in this call (None: all T;
         rows of out and lse beyond are not written).  Returns (out, lse)."""
+        if stream is None and (fast := _lib.fast()):
+            done = fast.cross(ctypes.addressof(self.plan), q, k_pages, v_pages, block_table, kv_lens, q_lens, k_scale, v_scale,
+                              out, lse, want_lse, self.workspace, self.status)
+            if done is not None:
+                return done
+        if not isinstance(q, torch.Tensor):
+            raise ValueError("CrossDecoder: q must be a tensor")
         if out is None:
             out = _lib.empty_on(q.shape, q.dtype, self.device, stream)
         if lse is None and want_lse:
@@ -133,6 +142,14 @@ class PrefixDecoder(_Planned):
                  out=None, lse=None, want_lse=True, stream=None):
         """prefix_lens int32 [P], seq_lens int32 [B] (own tokens, after this
         step's were appended).  Returns (out, lse)."""
+        if stream is None and (fast := _lib.fast()):
+            done = fast.decode_prefix(ctypes.addressof(self.plan), q, k_pages, v_pages, prefix_table, prefix_lens, self.members,
+                                      self.offsets, block_table, seq_lens, k_scale, v_scale, out, lse, want_lse,
+                                      self.workspace, self.status)
+            if done is not None:
+                return done
+        if not isinstance(q, torch.Tensor):
+            raise ValueError("PrefixDecoder: q must be a tensor")
         if out is None:
             out = _lib.empty_on(q.shape, q.dtype, self.device, stream)
         if lse is None and want_lse:

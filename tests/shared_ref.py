@@ -16,8 +16,7 @@ in fp32 add at most n 2^-24 each, in numerator and denominator.  Together
     sum p |v| (r_p + 4 e_s + n 2^-23 + 2^-18) + n 2^-24 max |v|
 and then the output's own rounding.  The log-sum-exp: 2 e_s + n 2^-24 + 2^-18
 (1 + |lse|).  Decode behind prefixes joins a second pass over the own tokens,
-whose f16 weights are rounded in numerator and denominator: 2^-10 there in
-place of r_p, and 2^-11 more for its lse.
+whose weights are f16 but for bf16 pools (pairs of bf16): r_p at least 2^-11.
 """
 import torch
 
@@ -80,7 +79,7 @@ def attend_many(q, k, v, n_seen=None):
     return out.reshape(m, Hq, D), size.reshape(m, Hq, D), lse.reshape(m, Hq), err
 
 
-def check(out, lse, ref, n, r, dtype, lse_extra=0.0, what="", vmax=0.0):
+def check(out, lse, ref, n, r, dtype, what="", vmax=0.0):
     """out [m, Hq, D] and lse [m, Hq] against ref = attend_many's result; vmax:
     the largest |v| where weights are f16."""
     o, size, l, err = ref
@@ -93,7 +92,7 @@ def check(out, lse, ref, n, r, dtype, lse_extra=0.0, what="", vmax=0.0):
     empty = torch.isinf(l)
     assert bool((torch.isneginf(lse) == empty).all()), f"{what}: -inf rows of lse"
     loff = (lse.double() - l)[~empty].abs()
-    lb = 2 * err + n * 2.0 ** -24 + 2.0 ** -18 * (1 + l[~empty].abs()) + lse_extra
+    lb = 2 * err + n * 2.0 ** -24 + 2.0 ** -18 * (1 + l[~empty].abs())
     assert bool((loff <= lb).all()), f"{what}: lse off by {float((loff - lb).max())} beyond its bound"
 
 
@@ -165,7 +164,7 @@ class Prefix:
         out, lse = out.cpu().reshape(shape), None if lse is None else lse.cpu().reshape(shape[:-1])
         k, v = values(self.k, self.ks), values(self.v, self.vs)
         narrow = self.kv != torch.bfloat16  # the own pass works in f16
-        r = max(r_p(self.q_dtype, self.kv), 2.0 ** -10 if narrow else 0.0)
+        r = max(r_p(self.q_dtype, self.kv), 2.0 ** -11)
         for b, L in enumerate(self.lens):
             kk, vv = seq_tokens(k, self.table[b], L, self.ps), seq_tokens(v, self.table[b], L, self.ps)
             if self.of[b] >= 0:
@@ -175,5 +174,5 @@ class Prefix:
             seen = [kk.shape[0] - self.T + 1 + t for t in range(self.T)]
             ref = attend_many(self.q[b].double(), kk, vv, seen)
             check(out[b], None if lse is None else lse[b], ref, kk.shape[0], r, self.q_dtype,
-                  lse_extra=2.0 ** -11 if narrow else 0.0, what=f"{what} sequence {b}",
+                  what=f"{what} sequence {b}",
                   vmax=float(vv.abs().max()) if len(vv) and narrow else 0.0)

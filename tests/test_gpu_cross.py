@@ -14,7 +14,7 @@ KINDS = [(F16, F16), (BF16, BF16), (E4M3, BF16), (E4M3, F16)]
 IDS = ["f16", "bf16", "e4m3-bf16", "e4m3-f16"]
 
 
-def run(c, plan_lens=None, want_lse=True, fill=7.0, **opts):
+def run(c, plan_lens=None, want_lse=True, fill=7.0, both=True, **opts):
     d = c.device()
     q_lens = d.pop("q_lens")
     dec = fd.CrossDecoder.for_pools(d["q"], d["k_pages"], d["v_pages"], d["block_table"], plan_lens or c.kv_lens,
@@ -23,6 +23,11 @@ def run(c, plan_lens=None, want_lse=True, fill=7.0, **opts):
     lse = torch.full(d["q"].shape[:-1], fill, device="cuda") if want_lse else None
     dec(**d, q_lens=q_lens, out=out, lse=lse, want_lse=want_lse)
     dec.check()
+    if both and dec.plan.has_few and q_lens is None:
+        # the decode kernel took the call; given counts, the other kernel takes it
+        out2, lse2 = dec(**d, q_lens=torch.full((len(c.q),), c.T, dtype=torch.int32, device="cuda"))
+        dec.check()
+        c.verify(out2, lse2, what="the same, with counts")
     return out, lse, dec
 
 
@@ -126,13 +131,14 @@ def test_query_range_over_e4m3(fdlib, mult):
     c.verify(out, lse, what="query range")
 
 
-def test_nan_codes_stay_in_their_head(fdlib):
+@pytest.mark.parametrize("T", [3, 30])
+def test_nan_codes_stay_in_their_head(fdlib, T):
     """A live NaN code reaches every row of its KV head and none of the others."""
-    c = Cross(14, [200, 77], T=3, Hq=4, Hkv=2, D=64, kv=E4M3, ps=16)
+    c = Cross(14, [200, 77], T=T, Hq=4, Hkv=2, D=64, kv=E4M3, ps=16)
     ref, _, _ = run(c)
     c.v.view(torch.uint8)[int(c.table[0, 1]), 3, 1, 5] = 0x7f
     c.k.view(torch.uint8)[int(c.table[1, 0]), 2, 0, 9] = 0xff
-    out, lse, _ = run(c)
+    out, lse, _ = run(c, both=False)
     assert bool(torch.isnan(out[0, :, 2:, 5]).all()) and bool(torch.isnan(out[1, :, :2]).all())
     out[0, :, 2:, 5], ref[0, :, 2:, 5] = 0, 0
     out[1, :, :2], ref[1, :, :2] = 0, 0
@@ -159,10 +165,11 @@ def test_rising_maximum(fdlib):
     c.verify(out, lse, what="rising maximum")
 
 
-def test_device_errors_are_reported(fdlib):
+@pytest.mark.parametrize("T", [4, 40])
+def test_device_errors_are_reported(fdlib, T):
     """Lengths beyond the capacity, pages and query counts out of range: the
     status says so, the other sequences are right, nothing else is touched."""
-    c = Cross(10, [100, 60, 90], T=4, Hq=4, Hkv=2, D=64)
+    c = Cross(10, [100, 60, 90], T=T, Hq=4, Hkv=2, D=64)
     d = c.device()
     ql = d.pop("q_lens")
     assert ql is None
@@ -174,7 +181,7 @@ def test_device_errors_are_reported(fdlib):
         assert int(dec.status.item()) & bit  # a cut length may meet unused pages: their bit as well
         with pytest.raises(fd.FdError):
             dec.check()
-        ref, _ = dec(**d)
+        ref, _ = dec(**d, q_lens=torch.full_like(d["kv_lens"], T) if "q_lens" in kw else None)
         dec.check()
         for b in good:
             assert torch.equal(out[b], ref[b])
@@ -189,6 +196,6 @@ def test_device_errors_are_reported(fdlib):
     table = d["block_table"].clone()
     table[2, 1] = 1 << 20
     call(_lib.FD_DEV_BAD_PAGE, [0, 1], block_table=table)
-    counts = torch.tensor([4, 9, -1], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([T, T + 5, -1], dtype=torch.int32, device="cuda")
     out = call(_lib.FD_DEV_CAPACITY, [0], q_lens=counts)
     assert bool((out[1:] == 7.0).all())
