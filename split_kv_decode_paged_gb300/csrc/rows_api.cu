@@ -32,16 +32,17 @@ constexpr int kMaxRowSplits = 64;
 constexpr size_t kMaxPartialBytes = size_t(256) << 20;
 // Times of the cost model, in ns: what an item costs beside its tiles (query
 // rows, epilogue), what a split one costs more (its partial state), and the
-// second launch that merges.
-constexpr double kItemNs = 2500, kSplitNs = 1000, kMergeNs = 3000;
+// second launch that merges: its own time and the partial states it reads (bytes
+// a ns).
+constexpr double kItemNs = 2500, kSplitNs = 1000, kMergeNs = 3000, kMergeRate = 4000;
 
-// Time of one CTA for a tile of 128 tokens: the largest of its share of the
-// memory's rate, of the products of its row tiles and, for one row tile alone,
-// of the chain from scores through softmax to output.
+// Time of one CTA for a tile of 128 tokens: its share of the memory's rate, or
+// what one and two row tiles measured (E4M3 codes are converted first).
 double tile_ns(const fd_problem &p, int row_tiles) {
-    const double bytes = 2.0 * kTile * p.D * (p.kv_dtype == FD_E4M3 ? 1 : 2) / 44.0;
-    const double flops = row_tiles * 4.0 * kTile * kTile * p.D / 11000.0;
-    return std::max(std::max(bytes, flops), p.D == 128 ? 1200.0 : 900.0);
+    const bool fp8 = p.kv_dtype == FD_E4M3;
+    const double bytes = 2.0 * kTile * p.D * (fp8 ? 1 : 2) / 44.0;
+    const double busy = (row_tiles == 2 ? (p.D == 128 ? 1450.0 : 1350.0) : (p.D == 128 ? 1000.0 : 800.0)) * (fp8 ? 1.5 : 1.0);
+    return std::max(bytes, busy);
 }
 
 // Shared by both planners.  tokens_of(s): query tokens of segment s (segment
@@ -77,6 +78,11 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
         const long long S = ((long long)room + C - 1) / C;
         return S == 1 || (S <= kMaxRowSplits && rows * S * (p.D + 2) * sizeof(float) <= kMaxPartialBytes);
     };
+    // the kernel's order: longest rows first where it has few of them
+    std::vector<int> order(kv_rows + 1);
+    std::iota(order.begin(), order.end(), 0);
+    if (kv_rows < 32)
+        std::stable_sort(order.begin(), order.end() - 1, [&](int a, int b) { return kv_lens[a] > kv_lens[b]; });
     // items of all KV heads with chunks of C tokens, and their time on sms CTAs
     auto cost = [&](int C, long long *items_out) {
         std::vector<std::pair<double, long long>> items;  // time, how many of it
@@ -89,7 +95,7 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
             total += ns * n;
             count += n;
         };
-        for (int s = 0; s <= kv_rows; ++s) {
+        for (int s : order) {
             const long long r = (long long)tokens_of(s) * G;
             const int L = s < kv_rows ? kv_lens[s] : 0;
             const int ns = L == 0 ? 1 : (L + C - 1) / C;
@@ -106,10 +112,11 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
             }
         }
         if (items_out) *items_out = count;
+        const double merge = split ? kMergeNs + (double)rows * ((longest + C - 1) / C) * p.D * 4.0 / kMergeRate : 0.0;
         double longest_item = 0;
         for (const auto &it : items) longest_item = std::max(longest_item, it.first);
         if (count > 64LL * sms)  // plenty: the tail is about half an item
-            return total / sms + 0.5 * longest_item + (split ? kMergeNs : 0);
+            return total / sms + 0.5 * longest_item + merge;
         std::priority_queue<double, std::vector<double>, std::greater<double>> q;
         for (int i = 0; i < sms; ++i) q.push(0.0);
         double worst = 0;
@@ -120,7 +127,7 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
                 worst = std::max(worst, t);
                 q.push(t);
             }
-        return worst + (split ? kMergeNs : 0);
+        return worst + merge;
     };
     int best = chunk_of(std::max(1, std::min(opt.num_splits, kMaxRowSplits)));
     if (opt.num_splits == 0) {

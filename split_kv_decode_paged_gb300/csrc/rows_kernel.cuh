@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     __syncthreads();
     // Run of segments of each lane of the producer warp: [lane * per, ...).
     const int per = (nseg + 31) >> 5;
-    int run_items = 0, run_before = 0, run_off = 0, run_end = 0, run_len = 0, run_tokens = 0, total = 0;
+    int run_items = 0, run_before = 0, run_off = 0, run_end = 0, run_len = 0, run_tokens = 0, run_seg = 0, total = 0;
     if (warp == 9) {
         const int s0 = min(lane * per, nseg), s1 = min(s0 + per, nseg);
         for (int s = s0; s < s1; ++s) run_items += s_items[s];
@@ -342,6 +342,24 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         if (per == 1 && s1 > s0) {
             run_len = seg.kv_len(s0);
             run_tokens = seg.tokens(run_off, run_end);
+        }
+        if (per == 1) {
+            // longest KV rows first, so that the short ones fill the end
+            int rank = 0, src = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int len = __shfl_sync(0xffffffffu, run_len, i);
+                rank += len > run_len || (len == run_len && i < lane);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (__shfl_sync(0xffffffffu, rank, i) == lane) src = i;
+            run_seg = src;
+            run_items = __shfl_sync(0xffffffffu, run_items, src);
+            run_off = __shfl_sync(0xffffffffu, run_off, src);
+            run_end = __shfl_sync(0xffffffffu, run_end, src);
+            run_len = __shfl_sync(0xffffffffu, run_len, src);
+            run_tokens = __shfl_sync(0xffffffffu, run_tokens, src);
         }
         int incl = run_items;
 #pragma unroll
@@ -432,7 +450,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                     const int rows = __shfl_sync(0xffffffffu, ntokens, ln) * p.G;
                     const int mt = max(1, (rows + 2 * kTileRows - 1) / (2 * kTileRows));
                     int k = left - __shfl_sync(0xffffffffu, incl - n, ln);
-                    it.seg = s0 + ln;
+                    it.seg = per == 1 ? __shfl_sync(0xffffffffu, run_seg, ln) : s0 + ln;
                     it.first = __shfl_sync(0xffffffffu, first, ln);
                     it.row0 = (k % mt) * 2 * kTileRows;
                     k /= mt;
