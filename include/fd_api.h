@@ -604,8 +604,8 @@ typedef struct {
     size_t ws_partial_md;
     size_t ws_counters;
     size_t ws_few;
-    fd_plan_t few;        /* of the decode kernel, which takes calls of up to 16
-                             query rows a KV head (see fd_plan_cross)             */
+    fd_plan_t few;        /* of the decode kernel, which takes calls of few query
+                             rows a KV head (see fd_plan_cross)                   */
     int has_few;          /* whether there is one                                 */
     int reserved[3];      /* fd_plan_prefix marks its plans here                  */
 } fd_cross_plan_t;
@@ -617,9 +617,9 @@ typedef struct {
  *   kv_lens_host  HOST int32 [B]: the lengths the work is split for
  *   options       may be NULL (one token, one beam)
  * B * beams * T is at most 2^22, and times Hq at most 2^28; Hq / Hkv at most
- * 2^15.  Where a KV head has at most 16 query rows (beams * T * Hq / Hkv; and B *
- * beams * T at most 8192) the plan also holds one of the decode kernel, which
- * then takes the calls without q_lens and with q dense. */
+ * 2^15.  Where a KV head has at most 16 query rows (beams * T * Hq / Hkv; E4M3
+ * pools 32; and B * beams * T at most 8192) the plan also holds one of the decode
+ * kernel, which then takes the calls without q_lens and with q dense. */
 fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
                         const fd_cross_options *options, fd_cross_plan_t *plan);
 
@@ -634,16 +634,20 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
  *   block_table  device int32 [B, max_blocks_per_seq]
  *   kv_lens      device int32 [B].  0 gives out = 0 and lse = -inf (and so does a
  *                row of scores that are all -inf); a length below 0 or beyond the
- *                plan's capacity sets FD_DEV_CAPACITY and is cut to it
- *   out          device [B * beams, T, Hq, D] in q_dtype, 16-byte aligned, dense
+ *                plan's capacity (capacity_tokens; few.capacity_tokens where the
+ *                decode kernel takes the call) sets FD_DEV_CAPACITY and is cut to it
+ *   out          device [B * beams, T, Hq, D] in q_dtype, 16-byte aligned, dense;
+ *                memory that no other argument covers
  *   lse          device fp32 [B * beams, T, Hq] (natural log), or NULL
  *   workspace    device, 256-byte aligned, >= plan->workspace_bytes, zero-filled
  *                before its first use and after a call that reported an FD_DEV_*
  *                error; one per call in flight
  *   the pools, their scales, status_dev and stream as in fd_decode_paged.
  * K and V behind a row's length are not used, whatever they hold.  The weights
- * enter P.V rounded to the type of the product: q_dtype, and for an E4M3 pool
- * pairs of bf16 (f16 q) or bf16. */
+ * enter P.V rounded to the type of the product: q_dtype; over an E4M3 pool f16,
+ * but where V's scales differ by more than a factor of 8 within a chunk of a row
+ * bf16 (f16 q: pairs of bf16).  The decode kernel rounds them as fd_decode_paged
+ * does. */
 fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q_stride,
                          const int32_t *q_lens, const void *k_pages, const void *v_pages,
                          const float *k_scale, const float *v_scale, const int32_t *block_table,

@@ -205,7 +205,8 @@ def fast():
             at = [ctypes.cast(f, ctypes.c_void_p).value for f in
                   (lib.fd_append_kv_norm, lib.fd_evict_kv, lib.fd_decode_paged_weights, lib.fd_decode_paged_diff,
                    lib.fd_cross_paged, lib.fd_decode_paged_prefix)]
-            _fd_torch.init(*at, FdError)
+            _fd_torch.init(*at[:4], FdError)
+            _fd_torch.init_shared(*at[4:])
             _fast = _fd_torch
     return _fast
 

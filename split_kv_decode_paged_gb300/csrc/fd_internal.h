@@ -144,7 +144,6 @@ struct RowsParams {
     int S, chunk, cap;
     int boxr;                  // token rows per TMA box: gcd(page_size, tile)
     uint32_t g_magic;          // ceil(2^32 / G), 0: G = 1
-    int kv_once;               // K and V are read by one item only
     int q_bf16, kv_kind, D;
     float scale_log2;          // log2(e) / sqrt(D)
     uint64_t timeout_ns, stall_ns;

@@ -19,7 +19,13 @@ constexpr long long kMaxRows = 1LL << 28;    // query tokens * heads
 constexpr int kMaxGroup = 1 << 15;           // query heads of a KV head
 constexpr int kMaxRowSms = 1 << 16;
 constexpr uint64_t kRowsTimeoutNs = 2000000000ull;  // 2 s limit on any device-side wait
-constexpr int kFewRows = 16;  // query rows of a KV head up to which the decode kernel takes a cross-attention call
+// Query rows of a KV head up to which the decode kernel takes a cross-attention
+// call, decode and rows kernel in us.  16 bits (64 sequences, 512-8192 tokens, 4
+// heads a KV head): 4 rows 172, 203; 16 rows 178, 211; 24 rows 300, 214 (16 rows a
+// pass over K and V).  E4M3 (16 of 2048-16384 tokens, 8 heads), whose codes the
+// rows kernel converts for 128 rows whatever their number: 8 rows 58, 156; 32
+// rows 136, 156; 64 rows 263, 161.
+constexpr int kFewRows = 16, kFewRowsE4m3 = 32;
 constexpr int kPlanCross = 2, kPlanPrefix = 3;      // fd_cross_plan_t::reserved[0]
 
 bool on(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -208,7 +214,6 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     rp.row_splits = rp.counters + 64;
     rp.boxr = std::gcd(p.page_size, kTile);
     rp.g_magic = rp.G > 1 ? (uint32_t)(((1ull << 32) + rp.G - 1) / rp.G) : 0;
-    rp.kv_once = 0;
     CUtensorMap tmk, tmv;
     const bool ok = p.kv_dtype == FD_E4M3
                         ? encode_pool_map(&tmk, k_pages, p, rp.boxr, true) && encode_pool_map(&tmv, v_pages, p, rp.boxr, true)
@@ -232,6 +237,7 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
         return false;
     if (kind == kPlanCross && (plan.beams < 1 || (long long)plan.kv_rows * plan.beams != plan.seqs)) return false;
     if (plan.chunk_tokens < kTile || plan.chunk_tokens % kTile || plan.num_splits > kMaxRowSplits || plan.grid_ctas < 1 ||
+        plan.grid_ctas > kMaxRowSms ||
         plan.capacity_tokens > (long long)plan.num_splits * plan.chunk_tokens)
         return false;
     const size_t rows = (size_t)plan.seqs * plan.tokens * p.Hq, S = plan.num_splits > 1 ? (size_t)plan.num_splits : 0;
@@ -286,10 +292,9 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host, 
     plan->beams = opt.beams;
     plan->reserved[0] = kPlanCross;
     // Few query rows: the decode kernel, whose 8 or 16 columns of queries waste
-    // less of an SM's time on them than tiles of 128 rows, and which issues its
-    // loads further ahead (kFewRows has both sides' times).
+    // less of an SM's time on them than tiles of 128 rows.
     const long long few = (long long)opt.beams * opt.tokens * (problem->Hq / problem->Hkv);
-    if (few <= kFewRows && (long long)problem->B * opt.beams * opt.tokens <= kMaxBatch) {
+    if (few <= (problem->kv_dtype == FD_E4M3 ? kFewRowsE4m3 : kFewRows) && (long long)problem->B * opt.beams * opt.tokens <= kMaxBatch) {
         fd_plan_options po = {};
         po.fuse_merge = 1;
         po.num_splits = opt.num_splits;

@@ -528,9 +528,9 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyObject *init(PyObject *, PyObject *args) {
-    unsigned long long f[6];
+    unsigned long long f[4];
     PyObject *error;
-    if (!PyArg_ParseTuple(args, "KKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &error)) return nullptr;
+    if (!PyArg_ParseTuple(args, "KKKKO", &f[0], &f[1], &f[2], &f[3], &error)) return nullptr;
     Py_INCREF(error);
     Py_XDECREF(g_error);
     g_error = error;
@@ -538,14 +538,21 @@ PyObject *init(PyObject *, PyObject *args) {
     g_evict = reinterpret_cast<decltype(g_evict)>(f[1]);
     g_weights = reinterpret_cast<decltype(g_weights)>(f[2]);
     g_diff = reinterpret_cast<decltype(g_diff)>(f[3]);
-    g_cross = reinterpret_cast<decltype(g_cross)>(f[4]);
-    g_prefix = reinterpret_cast<decltype(g_prefix)>(f[5]);
+    Py_RETURN_NONE;
+}
+
+PyObject *init_shared(PyObject *, PyObject *args) {
+    unsigned long long f[2];
+    if (!PyArg_ParseTuple(args, "KK", &f[0], &f[1])) return nullptr;
+    g_cross = reinterpret_cast<decltype(g_cross)>(f[0]);
+    g_prefix = reinterpret_cast<decltype(g_prefix)>(f[1]);
     Py_RETURN_NONE;
 }
 
 #define FD_FAST(name, f, n, what) \
     {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n, what>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"init", init, METH_VARARGS, "addresses of libfd's entry points and the error class"},
+                         {"init_shared", init_shared, METH_VARARGS, "addresses of fd_cross_paged and fd_decode_paged_prefix"},
                          FD_FAST("append_kv_norm", append, 19, kAppend),
                          FD_FAST("evict_kv", evict, 13, kEvict),
                          FD_FAST("decode_weights", weights, 16, kWeights),

@@ -3,6 +3,7 @@ them: after the appends that fill the pages, in captured graphs, on other
 streams, one call behind the other, with many KV rows and groups, over pools
 past 2^31 elements, both ways of marshalling, and when a device-side wait runs
 out."""
+import ctypes
 import random
 
 import pytest
@@ -298,6 +299,42 @@ def test_both_ways_of_marshalling(fdlib, monkeypatch, T):
         cdec.check()
         pdec.check()
     assert all(torch.equal(x, y) for x, y in zip(*res))
+
+
+@pytest.mark.parametrize("status", ["FD_ERR_CUDA", "FD_ERR_INVALID_ARG"])
+def test_failed_and_refused_calls(fdlib, monkeypatch, status):
+    """A call whose launches failed raises and is not made again; a refused one
+    goes the Python way.  The entry points are stand-ins that launch nothing."""
+    c = Cross(18, [30], T=2, Hq=4, Hkv=2, D=64)
+    p = Prefix(19, [40], [0, 0], [9, 20], Hq=4, Hkv=2, D=64)
+    cd, pd = c.device(), p.device()
+    cdec, pdec = cross_decoder(c, cd), prefix_decoder(p, pd)
+    fast = _lib.fast()
+    assert fast
+    names = ("fd_cross_paged", "fd_decode_paged_prefix")
+    real = [ctypes.cast(getattr(fdlib, n), ctypes.c_void_p).value for n in names]
+    code, calls, again = getattr(_lib, status), [], []
+
+    @ctypes.CFUNCTYPE(ctypes.c_int)
+    def stub():
+        calls.append(code)
+        return code
+
+    fast.init_shared(*[ctypes.cast(stub, ctypes.c_void_p).value] * 2)
+    try:
+        for n in names:
+            monkeypatch.setattr(_lib, n, lambda *a, **kw: again.append(a))
+        for i, f in enumerate((lambda: cdec(**cd), lambda: pdec(**pd))):
+            if code == _lib.FD_ERR_CUDA:
+                with pytest.raises(fd.FdError) as e:
+                    f()
+                assert e.value.code == code and "fd_" in str(e.value) and not again
+            else:
+                f()
+                assert len(again) == i + 1
+            assert len(calls) == i + 1
+    finally:
+        fast.init_shared(*real)
 
 
 @pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
