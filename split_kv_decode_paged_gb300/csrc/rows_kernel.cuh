@@ -1038,10 +1038,11 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
                         tmem_wait_ld();
                         tmem_loaded<128>(s);
-                        // E4M3: a group's scale goes into its factor; one that is not
-                        // positive into the scores, before hidden ones are set to
-                        // -inf (the highest score would be the lowest product, or
-                        // -inf times 0).
+                        // E4M3: a group's scale goes into its factor; where a factor
+                        // is not positive (a scale that is not, or a product that
+                        // underflows) into the scores, before hidden ones are set
+                        // to -inf (the highest score would be the lowest product,
+                        // or -inf times 0).
                         [[maybe_unused]] float fs[8], vs[8];
                         if constexpr (FP8) {
                             const float4 *cs = reinterpret_cast<const float4 *>(c.scale[es]);
@@ -1052,7 +1053,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                             vs[4] = v1.x; vs[5] = v1.y; vs[6] = v1.z; vs[7] = v1.w;
                             bool odd = false;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) odd |= !(fs[k] > 0.f);
+                            for (int k = 0; k < 8; ++k) odd |= !(row_sc * fs[k] > 0.f);
                             if (odd) {
 #pragma unroll
                                 for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * fs[k >> 4]);
