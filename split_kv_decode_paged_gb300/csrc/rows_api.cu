@@ -225,6 +225,13 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     return FD_OK;
 }
 
+// Both describe the same heads, types and pools (they may have another block
+// table and output type).
+bool same_pools(const fd_problem &a, const fd_problem &b) {
+    return a.Hq == b.Hq && a.Hkv == b.Hkv && a.D == b.D && a.q_dtype == b.q_dtype && a.kv_dtype == b.kv_dtype &&
+           a.page_size == b.page_size && a.num_pages == b.num_pages;
+}
+
 // What a plan handed in must satisfy for its launch to stay in bounds.
 bool plan_ok(const fd_cross_plan_t &plan, int kind) {
     const fd_problem &p = plan.problem;
@@ -248,10 +255,9 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
         return false;
     if (plan.has_few) {
         const fd_plan_t &f = plan.few;
-        if (kind != kPlanCross || f.kv_rows != plan.kv_rows || f.row_fold != plan.beams * plan.tokens ||
-            f.problem.Hq != p.Hq || f.problem.Hkv != p.Hkv || f.problem.D != p.D || f.problem.out_dtype != p.out_dtype ||
-            f.problem.q_dtype != p.q_dtype || f.problem.kv_dtype != p.kv_dtype || f.problem.page_size != p.page_size ||
-            f.problem.num_pages != p.num_pages || f.problem.max_blocks_per_seq != p.max_blocks_per_seq ||
+        if (kind != kPlanCross || f.kv_rows != plan.kv_rows || f.row_fold != plan.beams * plan.tokens || f.q_len > 1 ||
+            !same_pools(f.problem, p) || f.problem.out_dtype != p.out_dtype ||
+            f.problem.max_blocks_per_seq != p.max_blocks_per_seq ||
             plan.ws_few % 256 || plan.workspace_bytes < plan.ws_few || plan.workspace_bytes - plan.ws_few < f.workspace_bytes ||
             plan.ws_few < plan.ws_counters || plan.ws_few - plan.ws_counters < 256 + (S ? rows * sizeof(int) : 0))
             return false;
@@ -404,8 +410,7 @@ fd_status fd_decode_paged_prefix(const fd_prefix_plan_t *plan, const void *q, co
     const fd_cross_plan_t &sh = plan->shared;
     const fd_problem &p = sh.problem;
     if (plan->prefixes != sh.kv_rows || plan->own.kv_rows != sh.seqs || std::max(1, plan->own.q_len) != sh.tokens ||
-        plan->own.problem.Hq != p.Hq || plan->own.problem.Hkv != p.Hkv || plan->own.problem.D != p.D ||
-        plan->own.problem.out_dtype != FD_F32)
+        plan->own.row_fold != sh.tokens || !same_pools(plan->own.problem, p) || plan->own.problem.out_dtype != FD_F32)
         return FD_ERR_INVALID_ARG;
     const size_t rows = (size_t)sh.seqs * sh.tokens * p.Hq;
     if (plan->ws_own_lse < plan->ws_own_out || plan->ws_own_lse - plan->ws_own_out < rows * p.D * 4 ||
