@@ -150,7 +150,8 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
             }
         }
     }
-    while (!fits(best)) best = (best + best / 2 + kTile - 1) / kTile * kTile;
+    while (!fits(best))
+        best = (int)std::min((best + best / 2LL + kTile - 1) / kTile * kTile, (room + kTile - 1LL) / kTile * kTile);
     long long items = 0;
     cost(best, &items);
     // other lengths or groups than the planned ones may make more items
@@ -243,7 +244,8 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
         (long long)plan.seqs * plan.tokens > kMaxTokens || (long long)plan.seqs * plan.tokens * p.Hq > kMaxRows)
         return false;
     if (kind == kPlanCross && (plan.beams < 1 || (long long)plan.kv_rows * plan.beams != plan.seqs)) return false;
-    if (plan.chunk_tokens < kTile || plan.chunk_tokens % kTile || plan.num_splits > kMaxRowSplits || plan.grid_ctas < 1 ||
+    // (chunks of at most 2^30 tokens: length + chunk - 1 stays within an int)
+    if (plan.chunk_tokens < kTile || plan.chunk_tokens > (1 << 30) || plan.chunk_tokens % kTile || plan.num_splits > kMaxRowSplits || plan.grid_ctas < 1 ||
         plan.grid_ctas > kMaxRowSms ||
         plan.capacity_tokens > (long long)plan.num_splits * plan.chunk_tokens)
         return false;
