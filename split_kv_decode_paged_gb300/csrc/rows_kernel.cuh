@@ -33,7 +33,9 @@
 // largest element below 2^15 (elements down to 2^-31 of it are exact), undone on
 // the scores.
 // Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
-// leaves the loop, which ends the others' waits the same way.
+// leaves the loop, which ends the others' waits the same way.  The limit is for
+// what does not come, not for how long an item is: the query warps, which wait
+// for the next item all through this one, start theirs anew while tiles are loaded.
 //
 // Bounds, measured on GB300 (one pass among others).  D = 128, 16 bits, two row
 // tiles: the products, 4 x 2048 queries over 8192 states of 32/8 heads 729 us =
@@ -118,6 +120,9 @@ struct RowsControl {
     float2 join[kTileRows];    // reference and denominator that tile 1's warps hand to tile 0's
     float raw_scale[Sh::RAW_STAGES + 1][16];  // of a stage's groups of 16 tokens: K's, then V's
     alignas(16) float scale[Sh::FP8 ? Sh::STAGES : 1][16];
+    // Last, as the items' place decides how they are read: between tmem and held
+    // this word cost D = 64 prompts 4% (32 x 448 over 1500 136 -> 142 us).
+    uint32_t beat;             // tiles loaded so far
 };
 
 // The segments of a call: query tokens and KV length of each, in the kernel's
@@ -225,6 +230,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, uint64
     return false;
 }
 
+// The query warps' waits, which may take as long as an item: false once the limit
+// has passed twice without a tile loaded in between.  (In every role's waits the
+// look at it cost 2% to 6%, over E4M3 pools 25%: it is code between their steps.
+// Theirs take a tile's time or two.)
+template <typename Control>
+__device__ __forceinline__ bool warp_wait_item(Control &c, uint64_t &bar, uint32_t parity, uint64_t limit) {
+    uint32_t seen = ~0u;
+    while (!warp_wait(bar, parity, limit)) {
+        uint32_t beat;
+        asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(beat) : "r"(smem_u32(&c.beat)) : "memory");
+        if (__all_sync(0xffffffffu, beat == seen)) return false;
+        seen = beat;
+    }
+    return true;
+}
+
 template <int KV, int D, bool QBF16>
 __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     fd_rows_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap tmk,
@@ -266,6 +287,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         mbar_init(smem_u32(&c.join_full), 4);
         mbar_init(smem_u32(&c.join_empty), 4);
         c.held[0] = c.held[1] = 0;
+        c.beat = 0;
         for (int i = 0; i < NST; ++i) {
             mbar_init(smem_u32(&c.kv_full[i]), FP8 ? 4 : 1);
             mbar_init(smem_u32(&c.kv_empty[i]), 1);
@@ -510,6 +532,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             int pg_cur = npg0, pg_nxt = npg1, batch = 0;
             if (it.ntok == 0) look_up((int)gridDim.x + __shfl_sync(0xffffffffu, next, 0));
             for (int k0 = 0; k0 < nbox && ok; k0 += BPT) {
+                if (lane == 0) atomicAdd(&c.beat, 1u);
                 if (k0 == ahead) look_up((int)gridDim.x + __shfl_sync(0xffffffffu, next, 0));
                 if (k0 >= (batch + 1) * 32) {
                     ++batch;
@@ -677,13 +700,13 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         uint32_t n_q[2] = {0, 0};         // tiles loaded
         while (true) {
             const int slot = n_item % kItemSlots;
-            if (!warp_wait(c.item_full[slot], (n_item / kItemSlots) & 1, limit)) {
+            if (!warp_wait_item(c, c.item_full[slot], (n_item / kItemSlots) & 1, limit)) {
                 rows_flag(p.status, FD_DEV_TIMEOUT);
                 break;
             }
             const RowsItem it = c.item[slot];
             if (it.seg < 0) break;
-            if (!warp_wait(c.rows_empty, (n_item & 1) ^ 1, limit)) {
+            if (!warp_wait_item(c, c.rows_empty, (n_item & 1) ^ 1, limit)) {
                 rows_flag(p.status, FD_DEV_TIMEOUT);
                 break;
             }
@@ -718,7 +741,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
             bool ok = warp_wait(QSCALE ? c.rows_read : c.rows_full, n_item & 1, limit);
             const int tiles = it.nrows > kTileRows ? 2 : 1;
             for (int i = 0; i < tiles && ok; ++i) {
-                ok = warp_wait(c.q_empty[i], (n_q[i] & 1) ^ 1, limit);
+                ok = warp_wait_item(c, c.q_empty[i], (n_q[i] & 1) ^ 1, limit);
                 if (ok && it.ntok > 0) {
                     constexpr int CH = D / 8;  // 16-byte pieces of a row
                     const int ch = t % CH;

@@ -1,0 +1,27 @@
+"""Limits of device-side waits (timeout_us) of cross attention and shared
+prefixes: a limit that ends a wait for something that does not come leaves a
+call alone whose parts only take longer than that."""
+import pytest
+import torch
+
+import split_kv_decode_paged_gb300 as fd
+from tests.shared_ref import Cross
+
+pytestmark = pytest.mark.gpu
+
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.mark.parametrize("kv", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_items_longer_than_the_limit(fdlib, kv):
+    """One chunk of 40000 tokens (313 tiles of at least 1.3 us) under a limit
+    of 100 us: the next item's query rows are waited for all the while."""
+    c = Cross(21, [40000, 300], T=140, Hq=1, Hkv=1, D=64, kv=kv, ps=128)
+    d = c.device()
+    dec = fd.CrossDecoder.for_pools(d["q"], d["k_pages"], d["v_pages"], d["block_table"], c.kv_lens, num_splits=1,
+                                    timeout_us=100)
+    assert dec.plan.num_splits == 1
+    for _ in range(3):
+        out, lse = dec(**d)
+        dec.check()
+    c.verify(out, lse, what="long items")
