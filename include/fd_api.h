@@ -680,7 +680,9 @@ typedef struct {
  *                      (see fd_decode_paged_prefix)
  *   options            of the own pass, may be NULL: q_len, num_sms, max_seq_len,
  *                      timeout_us, debug_stall_us and debug_stall_role apply (no
- *                      shared_kv); num_sms and timeout_us to both passes
+ *                      shared_kv); num_sms and timeout_us to both passes (that
+ *                      over prefixes of 16 bits begins while the own pass ends,
+ *                      and its waits may last 1 ms longer)
  *   prefix_options     may be NULL: num_splits, max_kv_len and debug_stall_us of
  *                      the pass over the prefixes (its other fields are not used) */
 fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host, int prefixes,

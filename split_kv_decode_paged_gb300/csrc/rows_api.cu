@@ -19,6 +19,11 @@ constexpr long long kMaxRows = 1LL << 28;    // query tokens * heads
 constexpr int kMaxGroup = 1 << 15;           // query heads of a KV head
 constexpr int kMaxRowSms = 1 << 16;
 constexpr uint64_t kRowsTimeoutNs = 2000000000ull;  // 2 s limit on any device-side wait
+// Added to it where the pass over prefixes starts while the own tokens' pass ends
+// (16-bit pools) and waits for that, without a limit, to join its state: what is
+// left of it, its last stages and merges, takes tens of us, and other warps' waits
+// last as long.
+constexpr uint64_t kOwnEndNs = 1000000ull;
 // Query rows of a KV head up to which the decode kernel takes a cross-attention
 // call, decode and rows kernel in us.  16 bits (64 sequences, 512-8192 tokens, 4
 // heads a KV head): 4 rows 172, 203; 16 rows 178, 211; 24 rows 300, 214 (16 rows a
@@ -206,6 +211,7 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     rp.kv_kind = p.kv_dtype == FD_F16 ? KV_F16 : (p.kv_dtype == FD_BF16 ? KV_BF16 : KV_E4M3);
     rp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.D));
     rp.timeout_ns = plan.timeout_us > 0 ? (uint64_t)plan.timeout_us * 1000ull : kRowsTimeoutNs;
+    if (rp.own_out && p.kv_dtype != FD_E4M3) rp.timeout_ns += kOwnEndNs;
     rp.stall_ns = (uint64_t)plan.debug_stall_us * 1000ull;
     const size_t rows = (size_t)plan.seqs * plan.tokens * p.Hq;
     rp.part_o = reinterpret_cast<float *>(workspace + plan.ws_partial_o);
