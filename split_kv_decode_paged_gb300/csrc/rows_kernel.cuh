@@ -35,7 +35,8 @@
 // Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
 // leaves the loop, which ends the others' waits the same way.  The limit is for
 // what does not come, not for how long an item is: the query warps, which wait
-// for the next item all through this one, start theirs anew while tiles are loaded.
+// for the next item all through this one, start theirs anew while tiles are loaded
+// and lists of counts read.
 //
 // Bounds, measured on GB300 (one pass among others).  D = 128, 16 bits, two row
 // tiles: the products, 4 x 2048 queries over 8192 states of 32/8 heads 729 us =
@@ -48,6 +49,7 @@
 // tensor memory; two of them, so that one's softmax hides the other's products.
 #pragma once
 
+#include <limits.h>
 #include <math.h>
 
 #include <type_traits>
@@ -103,6 +105,7 @@ struct RowsShape {
     static constexpr int RING = CONTROL + 2 * TILE, RAW_RING = RING + STAGES * TILE;
     static constexpr int SMEM = RAW_RING + RAW_STAGES * RAW;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
+    static_assert(3 * (kMaxBatch + 2) * 4 <= SMEM - CONTROL, "room for the segments' counts");
 };
 
 template <typename Sh>
@@ -122,7 +125,7 @@ struct RowsControl {
     alignas(16) float scale[Sh::FP8 ? Sh::STAGES : 1][16];
     // Last, as the items' place decides how they are read: between tmem and held
     // this word cost D = 64 prompts 4% (32 x 448 over 1500 136 -> 142 us).
-    uint32_t beat;             // tiles loaded so far
+    uint32_t beat;             // tiles loaded and counts read on so far
 };
 
 // The segments of a call: query tokens and KV length of each, in the kernel's
@@ -132,21 +135,81 @@ struct Segments {
     __device__ int count() const { return p.kv_rows + (p.offsets ? 1 : 0); }
     // offsets[s] before it is made to rise
     __device__ int raw_offset(int s) const { return s > p.kv_rows ? p.seqs : (s == 0 ? 0 : __ldcg(p.offsets + s)); }
-    __device__ int q_len(int b) const {
-        if (!p.q_lens) return p.T;
+    __device__ int q_len(int b, bool &bad) const {
         const int n = __ldcg(p.q_lens + b);
-        return n < 0 || n > p.T ? 0 : n;
+        const bool out = n < 0 || n > p.T;
+        bad |= out;
+        return out ? 0 : n;
     }
     __device__ int kv_len(int s) const {
         if (s >= p.kv_rows) return 0;
         return min(max(__ldcg(p.kv_lens + s), 0), p.cap);
     }
-    // query tokens of sequences [first, end) of the member order
-    __device__ int tokens(int first, int end) const {
+    // query tokens of sequences [first, end) of the member order, by one thread
+    __device__ int tokens(int first, int end, bool &bad) const {
         if (!p.q_lens) return (end - first) * p.T;
         int n = 0;
-        for (int b = first; b < end; ++b) n += q_len(b);
+#pragma unroll 8
+        for (int b = first; b < end; ++b) n += q_len(b, bad);
         return n;
+    }
+    // by a whole warp
+    __device__ int warp_tokens(int first, int end, bool &bad, int lane) const {
+        int n = 0;
+#pragma unroll 8
+        for (int b = first + lane; b < end; b += 32) n += q_len(b, bad);
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+    // Whether a warp on every segment takes fewer rounds of loads than a thread on
+    // every one, eight loads a round, the threads' scattered ones twice as long: 8
+    // KV rows of 64 sequences with counts 14.5 us a call by warps, 17 by threads.
+    __device__ bool by_warp(int segments, int warps, int threads) const {
+        return p.q_lens && (segments + warps - 1) / warps * ((p.beams + 255) >> 8) <
+                               2 * ((segments + threads - 1) / threads) * ((p.beams + 7) >> 3);
+    }
+    // The q tokens (sequence * T + token) of a segment's query tokens n[0 .. 3]
+    // (-1: none) of every lane, whose sequences are [first, end), by a whole warp:
+    // the sums of 256 sequences at a time, running sums where one of n may be among
+    // them.
+    __device__ void find(int first, int end, const int (&n)[4], int (&q)[4], int lane, uint32_t *beat) const {
+        int high = max(max(n[0], n[1]), max(n[2], n[3])), low = INT_MAX;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) low = min(low, n[k] < 0 ? INT_MAX : n[k]);
+        low = __reduce_min_sync(0xffffffffu, low);
+        high = __reduce_max_sync(0xffffffffu, high);
+        int base = 0;      // tokens of the sequences before
+        bool bad = false;  // said at the start
+        for (int b0 = first; b0 < end && base <= high; b0 += 8 * 32) {
+            if (lane == 0) atomicAdd(beat, 1u);
+            const int sum = end - first > 32 ? warp_tokens(b0, min(b0 + 8 * 32, end), bad, lane) : INT_MAX - base;
+            if (base + sum <= low) {
+                base += sum;
+                continue;
+            }
+#pragma unroll 1
+            for (int b1 = b0; b1 < min(b0 + 8 * 32, end) && base <= high; b1 += 32) {
+                int incl = b1 + lane < end ? q_len(b1 + lane, bad) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += t;
+                }
+                const int total = __shfl_sync(0xffffffffu, incl, 31);
+                if (base + total > low) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int left = n[k] - base;
+                        int at = 0;  // the lane's sequence: the first whose running sum is above left
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            if (__shfl_sync(0xffffffffu, incl, at + o - 1) <= left) at += o;
+                        const int before = __shfl_sync(0xffffffffu, incl, max(at - 1, 0));
+                        if (left >= 0 && left < total) q[k] = (b1 + at) * p.T + left - (at ? before : 0);
+                    }
+                }
+                base += total;
+            }
+        }
     }
     // items of a segment with that many query tokens
     __device__ int items(int tokens, int len) const {
@@ -323,8 +386,8 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     // use yet): the producer warp keeps their sums over 32 runs of segments.
     const Segments seg{p};
     const int nseg = seg.count();
-    int *scratch = reinterpret_cast<int *>(smem + Sh::CONTROL);  // offsets that rise, then items: nseg + 1 each
-    int *s_off = scratch, *s_items = scratch + nseg + 1;
+    int *scratch = reinterpret_cast<int *>(smem + Sh::CONTROL);  // offsets that rise, items, query tokens: nseg + 1 each
+    int *s_off = scratch, *s_items = scratch + nseg + 1, *s_tokens = scratch + 2 * (nseg + 1);
     if (p.offsets) {
         // offsets made to rise within [0, seqs]: a running maximum, by one warp
         if (warp == 0) {
@@ -351,18 +414,25 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         for (int s = threadIdx.x; s <= nseg; s += Sh::THREADS) s_off[s] = s * p.beams;
     }
     __syncthreads();
+    const bool by_warp = seg.by_warp(nseg, Sh::THREADS / 32, Sh::THREADS);
+    if (by_warp) {
+        bool bad = false;
+        for (int s = warp; s < nseg; s += Sh::THREADS / 32) {
+            const int n = seg.warp_tokens(s_off[s], s_off[s + 1], bad, lane);
+            if (lane == 0) s_tokens[s] = n;
+        }
+        if (bad) rows_flag(p.status, FD_DEV_CAPACITY);
+        __syncthreads();
+    }
     for (int s = threadIdx.x; s < nseg; s += Sh::THREADS) {
-        const int first = s_off[s], end = s_off[s + 1];
-        s_items[s] = seg.items(seg.tokens(first, end), seg.kv_len(s));
+        bool bad = false;
+        if (!by_warp) s_tokens[s] = seg.tokens(s_off[s], s_off[s + 1], bad);
+        s_items[s] = seg.items(s_tokens[s], seg.kv_len(s));
         if (s < p.kv_rows) {
             const int L = __ldcg(p.kv_lens + s);
-            if (L < 0 || L > p.cap) rows_flag(p.status, FD_DEV_CAPACITY);
+            bad |= L < 0 || L > p.cap;
         }
-        if (p.q_lens)
-            for (int b = first; b < end; ++b) {
-                const int n = __ldcg(p.q_lens + b);
-                if (n < 0 || n > p.T) rows_flag(p.status, FD_DEV_CAPACITY);
-            }
+        if (bad) rows_flag(p.status, FD_DEV_CAPACITY);
     }
     __syncthreads();
     // Run of segments of each lane of the producer warp: [lane * per, ...).
@@ -375,7 +445,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
         run_end = s_off[s1];
         if (per == 1 && s1 > s0) {
             run_len = seg.kv_len(s0);
-            run_tokens = seg.tokens(run_off, run_end);
+            run_tokens = s_tokens[s0];
         }
         if (per == 1) {
             // longest KV rows first, so that the short ones fill the end
@@ -464,7 +534,19 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                         end = first + p.beams;
                     }
                     const int len = per == 1 ? run_len : (s < s_end ? seg.kv_len(s) : 0);
-                    const int ntokens = per == 1 ? run_tokens : (s < s_end ? seg.tokens(first, end) : 0);
+                    int ntokens = run_tokens;
+                    [[maybe_unused]] bool bad = false;  // said at the start
+                    if (per > 1 && seg.by_warp(min(32, s_end - s0), 1, 32)) {
+                        const int f0 = __shfl_sync(0xffffffffu, first, 0);
+                        for (int x = 0; x < 32 && s0 + x < s_end; ++x) {
+                            if (lane == 0) atomicAdd(&c.beat, 1u);
+                            const int t = seg.warp_tokens(f0 + x * p.beams, f0 + (x + 1) * p.beams, bad, lane);
+                            if (lane == x) ntokens = t;
+                        }
+                        if (s >= s_end) ntokens = 0;
+                    } else if (per > 1) {
+                        ntokens = s < s_end ? seg.tokens(first, end, bad) : 0;
+                    }
                     const int n = per == 1 ? run_items : (s < s_end ? seg.items(ntokens, len) : 0);
                     int incl = n;
 #pragma unroll
@@ -711,29 +793,34 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 break;
             }
             int *tok = c.tok;
+            if (p.q_lens && p.beams > 1) {
+                int n[4], q4[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int r = t + 64 * u;
-                int q = -1;
-                if (r < it.nrows) {
-                    int n = it.n0 + small_div(it.g0 + r, p.g_magic);  // token of the segment
-                    if (p.q_lens) {
-                        int b = it.first;
-                        for (int len = seg.q_len(b); n >= len && b + 1 < p.seqs; len = seg.q_len(b)) {
-                            n -= len;
-                            ++b;
-                        }
-                        q = b * p.T + n;
-                    } else {
-                        const int k = p.T == 1 ? n : n / p.T, i = it.first + k;
+                for (int u = 0; u < 4; ++u) {
+                    const int r = t + 64 * u;
+                    n[u] = r < it.nrows ? it.n0 + small_div(it.g0 + r, p.g_magic) : -1;  // token of the segment
+                    q4[u] = -1;
+                }
+                seg.find(it.first, it.first + p.beams, n, q4, lane, &c.beat);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) tok[t + 64 * u] = q4[u];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = t + 64 * u;
+                    int q = -1;
+                    if (r < it.nrows) {
+                        const int n = it.n0 + small_div(it.g0 + r, p.g_magic);
+                        // place of its sequence in the segment (counts of queries: it has one)
+                        const int k = p.q_lens ? 0 : p.T == 1 ? n : n / p.T, i = it.first + k;
                         const int b = p.members ? __ldcg(p.members + i) : i;
                         if (b >= 0 && b < p.seqs)
                             q = b * p.T + (n - k * p.T);
                         else
                             rows_flag(p.status, FD_DEV_BAD_PAGE);
                     }
+                    tok[r] = q;
                 }
-                tok[r] = q;
             }
             // what the loaders need of each other's rows; the softmax warps get them
             // now, or with the rows' factors
