@@ -1316,13 +1316,18 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
                 }
             }
             uint32_t pb[SUBT][NT][2];
-            // Low parts of the weights (P = hi + lo): bf16 V, and the f16 products of
-            // weight totals and of maps.  There the denominator sums the weights
+            // Low parts of the weights (P = hi + lo): bf16 V, and the f16 products
+            // outside the plain decode.  There the denominator sums the weights
             // unrounded (see MODE), so the roundings of 11 bits alone would not
             // cancel: up to 2^-12 of sum p |v|, which a difference of similar
-            // maps and its norm scale up and an fp32 output shows.
+            // maps and its norm scale up and an fp32 output shows.  Not over E4M3
+            // pools where the result is a state (kState): there 11 bits are what
+            // the plain decode has, of values of 4 bits, and pairs take 174 to 182
+            // registers at D = 128, more than two CTAs an SM have (256 sequences of
+            // 16-2048 own tokens behind twelve prefixes 199 -> 217 us).  f16: no
+            // cost (48 x 4 drafts 66.8 us, 24 x 5 beams 29.8 either way).
             uint32_t pl[SUBT][NT][2];
-            constexpr bool kPair = KV == KV_BF16 || MODE == kScores || MODE == kDiff;
+            constexpr bool kPair = KV == KV_BF16 || (MODE != kPlain && !(MODE == kState && FP8));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float mn0 = mrow[n][0], mn1 = mrow[n][1];
