@@ -646,8 +646,7 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
  * K and V behind a row's length are not used, whatever they hold.  The weights
  * enter P.V rounded to the type of the product: q_dtype; over an E4M3 pool f16,
  * but where V's scales differ by more than a factor of 8 within a chunk of a row
- * bf16 (f16 q: pairs of bf16).  The decode kernel rounds them as fd_decode_paged
- * does. */
+ * pairs of bf16 (16 bits). */
 fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q_stride,
                          const int32_t *q_lens, const void *k_pages, const void *v_pages,
                          const float *k_scale, const float *v_scale, const int32_t *block_table,

@@ -28,8 +28,8 @@
 // one rounding, relative to a power of two R at or above the chunk's largest
 // scale (O is multiplied by it at the end).  Where a chunk's scales differ by more
 // than kScaleRange, small ones times R^-1 would leave f16's normal range: V and
-// the weights are bf16 there (with f16 queries the weights are pairs of bf16,
-// two products).  A bf16 query row enters times a power of two that brings its
+// the weights are bf16 there, the weights as pairs (two products), so that what
+// other pages' scales are does not cost bits.  A bf16 query row enters times a power of two that brings its
 // largest element below 2^15 (elements down to 2^-31 of it are exact), undone on
 // the scores.
 // Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     using Sh = RowsShape<KV, D>;
     constexpr bool FP8 = Sh::FP8;
     constexpr bool B16 = KV == KV_BF16;    // products in bf16 (else f16)
-    constexpr bool PAIR = FP8 && !QBF16;   // bf16 weights of an E4M3 chunk of wide scales as pairs
+    constexpr bool PAIR = FP8;             // bf16 weights (E4M3: chunks of wide scales) as pairs
     constexpr bool QSCALE = FP8 && QBF16;  // query rows scaled into f16
     static_assert(FP8 || QBF16 == (KV == KV_BF16), "16-bit pools have q's type");
     constexpr int HALVES = Sh::HALVES, NST = Sh::STAGES;
@@ -1240,7 +1240,7 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                                 if constexpr (FP8) {
                                     unpair(mul2(pair(x0, x1), pair(vs[k >> 4], vs[k >> 4])), x0, x1);
                                 }
-                                if (B16 || (!PAIR && to_bf16)) {
+                                if (to_bf16 && !PAIR) {
                                     s[k >> 1] = pack_bf16x2(x0, x1);
                                 } else if (to_bf16) {
                                     const uint32_t w = pack_bf16x2(x0, x1);
