@@ -581,6 +581,10 @@ typedef struct {
     int timeout_us;     /* limit of every device-side wait, as in fd_plan_options */
     int debug_stall_us; /* TEST HOOK, 0 = off: the loads of every CTA start this
                            late, so that the waits for them run out; <= 1 s       */
+    int weight_parts;   /* bf16 pools: the parts of a softmax weight in P.V, 1 (8
+                           bits) or 2 (hi + lo, 16 bits, as in fd_decode_paged; one
+                           product more).  0 = 1 for cross attention, 2 for
+                           prefixes                                               */
 } fd_cross_options;
 
 /* A plan: plain data in host memory, reusable for any number of calls while
@@ -594,7 +598,7 @@ typedef struct {
     int num_splits;       /* partial-state slots per query row                    */
     int chunk_tokens;     /* tokens per split                                     */
     int capacity_tokens;
-    int tile_rows;        /* query rows of one work item, at most                 */
+    int weight_parts;     /* 1 or 2 (see fd_cross_options)                        */
     int grid_ctas;
     int num_sms;
     int timeout_us;
@@ -644,9 +648,12 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
  *                error; one per call in flight
  *   the pools, their scales, status_dev and stream as in fd_decode_paged.
  * K and V behind a row's length are not used, whatever they hold.  The weights
- * enter P.V rounded to the type of the product: q_dtype; over an E4M3 pool f16,
- * but where V's scales differ by more than a factor of 8 within a chunk of a row
- * pairs of bf16 (16 bits). */
+ * enter P.V rounded to the type of the product: bf16 pools weight_parts bf16 (8 or
+ * 16 bits), f16 pools f16 (11 bits), E4M3 pools f16, but where V's scales differ by
+ * more than a factor of 8 within a chunk of a row pairs of bf16 (16 bits).  The
+ * decode kernel, which takes calls of few query rows (see fd_plan_cross), has pairs
+ * over 16-bit pools whatever weight_parts says: with 1, and over f16 pools, a call
+ * is more exact there than the same one with q_lens, a token stride or more rows. */
 fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q_stride,
                          const int32_t *q_lens, const void *k_pages, const void *v_pages,
                          const float *k_scale, const float *v_scale, const int32_t *block_table,
@@ -682,8 +689,9 @@ typedef struct {
  *                      shared_kv); num_sms and timeout_us to both passes (that
  *                      over prefixes of 16 bits begins while the own pass ends,
  *                      and its waits may last 1 ms longer)
- *   prefix_options     may be NULL: num_splits, max_kv_len and debug_stall_us of
- *                      the pass over the prefixes (its other fields are not used) */
+ *   prefix_options     may be NULL: num_splits, max_kv_len, debug_stall_us and
+ *                      weight_parts of the pass over the prefixes (its other fields
+ *                      are not used) */
 fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host, int prefixes,
                          int prefix_max_blocks, const int32_t *prefix_lens_host,
                          const int32_t *offsets_host, const fd_plan_options *options,

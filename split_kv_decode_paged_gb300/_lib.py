@@ -94,13 +94,13 @@ class FdNormAppend(ctypes.Structure):
 
 class FdCrossOptions(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("tokens", "beams", "num_splits", "num_sms", "max_kv_len", "timeout_us",
-                                            "debug_stall_us")]
+                                            "debug_stall_us", "weight_parts")]
 
 
 class FdCrossPlan(ctypes.Structure):
     _fields_ = ([("problem", FdProblem)] +
                 [(n, ctypes.c_int) for n in ("kv_rows", "seqs", "tokens", "beams", "num_splits", "chunk_tokens",
-                                             "capacity_tokens", "tile_rows", "grid_ctas", "num_sms", "timeout_us",
+                                             "capacity_tokens", "weight_parts", "grid_ctas", "num_sms", "timeout_us",
                                              "debug_stall_us")] +
                 [(n, ctypes.c_size_t) for n in ("workspace_bytes", "ws_partial_o", "ws_partial_md", "ws_counters",
                                                 "ws_few")] +
@@ -783,14 +783,16 @@ def _host_i32(entry, name, x, n):
 
 
 def fd_plan_cross(problem: FdProblem, kv_lens_host, tokens=1, beams=1, num_splits=0, num_sms=0, max_kv_len=0,
-                  timeout_us=0, debug_stall_us=0) -> FdCrossPlan:
+                  timeout_us=0, debug_stall_us=0, weight_parts=0) -> FdCrossPlan:
     """Plan cross attention of problem.B KV rows times beams sequences of
-    tokens query tokens each; kv_lens_host are the rows' lengths."""
+    tokens query tokens each; kv_lens_host are the rows' lengths.  weight_parts:
+    bf16 parts of a softmax weight over bf16 pools (0: one)."""
     a = _Args("fd_plan_cross")
     lens = _host_i32("fd_plan_cross", "kv_lens_host", kv_lens_host, problem.B)
     opts = FdCrossOptions(*(a.whole(n, v) for n, v in (
         ("tokens", tokens), ("beams", beams), ("num_splits", num_splits), ("num_sms", num_sms),
-        ("max_kv_len", max_kv_len), ("timeout_us", timeout_us), ("debug_stall_us", debug_stall_us))))
+        ("max_kv_len", max_kv_len), ("timeout_us", timeout_us), ("debug_stall_us", debug_stall_us),
+        ("weight_parts", weight_parts))))
     plan = FdCrossPlan()
     rc = load().fd_plan_cross(ctypes.byref(problem), lens.data_ptr(), ctypes.byref(opts), ctypes.byref(plan))
     if rc != FD_OK:
@@ -823,11 +825,12 @@ def fd_cross_paged(plan: FdCrossPlan, q, k_pages, v_pages, k_scale, v_scale, blo
 
 
 def fd_plan_prefix(problem: FdProblem, seq_lens_host, prefix_max_blocks, prefix_lens_host, offsets_host, num_splits=0,
-                   max_prefix_len=0, prefix_stall_us=0, **own) -> FdPrefixPlan:
+                   max_prefix_len=0, prefix_stall_us=0, weight_parts=0, **own) -> FdPrefixPlan:
     """Plan decode behind shared prefixes: problem and seq_lens_host as
     fd_plan for the sequences' own tokens, own its options (q_len, num_sms,
     max_seq_len, timeout_us, ...); prefix_lens_host [P], offsets_host [P + 1]
-    as fd_decode_paged_prefix's; num_splits and max_prefix_len (capacity) of
+    as fd_decode_paged_prefix's; num_splits, max_prefix_len (capacity) and
+    weight_parts (bf16 parts of a softmax weight over bf16 pools, 0: two) of
     the prefixes."""
     a = _Args("fd_plan_prefix")
     names = [n for n, _ in FdPlanOptions._fields_]
@@ -839,7 +842,8 @@ def fd_plan_prefix(problem: FdProblem, seq_lens_host, prefix_max_blocks, prefix_
     plens = _host_i32("fd_plan_prefix", "prefix_lens_host", prefix_lens_host, P)
     offs = _host_i32("fd_plan_prefix", "offsets_host", offsets_host, P + 1)
     po = FdCrossOptions(num_splits=a.whole("num_splits", num_splits), max_kv_len=a.whole("max_prefix_len", max_prefix_len),
-                        debug_stall_us=a.whole("prefix_stall_us", prefix_stall_us))
+                        debug_stall_us=a.whole("prefix_stall_us", prefix_stall_us),
+                        weight_parts=a.whole("weight_parts", weight_parts))
     plan = FdPrefixPlan()
     rc = load().fd_plan_prefix(ctypes.byref(problem), lens.data_ptr(), P, a.whole("prefix_max_blocks", prefix_max_blocks),
                                plens.data_ptr(), offs.data_ptr(), ctypes.byref(opts), ctypes.byref(po), ctypes.byref(plan))

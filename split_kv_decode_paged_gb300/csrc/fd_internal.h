@@ -145,6 +145,7 @@ struct RowsParams {
     int boxr;                  // token rows per TMA box: gcd(page_size, tile)
     uint32_t g_magic;          // ceil(2^32 / G), 0: G = 1
     int q_bf16, kv_kind, D;
+    int weight_parts;          // bf16 pools: bf16 parts of a weight
     float scale_log2;          // log2(e) / sqrt(D)
     uint64_t timeout_ns, stall_ns;
 };

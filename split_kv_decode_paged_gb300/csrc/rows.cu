@@ -104,25 +104,27 @@ cudaError_t launch_after(Kernel kern, unsigned grid, unsigned threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int KV, int D, bool QBF16>
+template <int KV, int D, bool QBF16, int PARTS>
 cudaError_t launch_rows_t(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream) {
     using Sh = RowsShape<KV, D>;
-    auto kern = fd_rows_kernel<KV, D, QBF16>;
+    auto kern = fd_rows_kernel<KV, D, QBF16, PARTS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     if (e != cudaSuccess) return e;
     return launch_after(kern, (unsigned)grid, Sh::THREADS, Sh::SMEM, stream, p, tmk, tmv);
 }
 
-template <int KV, bool QBF16>
+template <int KV, bool QBF16, int PARTS = 1>
 cudaError_t launch_rows_d(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream) {
-    return p.D == 128 ? launch_rows_t<KV, 128, QBF16>(p, tmk, tmv, grid, stream)
-                      : launch_rows_t<KV, 64, QBF16>(p, tmk, tmv, grid, stream);
+    return p.D == 128 ? launch_rows_t<KV, 128, QBF16, PARTS>(p, tmk, tmv, grid, stream)
+                      : launch_rows_t<KV, 64, QBF16, PARTS>(p, tmk, tmv, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const RowsParams &p, const CUtensorMap &tmk, const CUtensorMap &tmv, int grid, cudaStream_t stream) {
-    if (p.kv_kind == KV_BF16) return launch_rows_d<KV_BF16, true>(p, tmk, tmv, grid, stream);
+    if (p.kv_kind == KV_BF16)
+        return p.weight_parts == 2 ? launch_rows_d<KV_BF16, true, 2>(p, tmk, tmv, grid, stream)
+                                   : launch_rows_d<KV_BF16, true, 1>(p, tmk, tmv, grid, stream);
     if (p.kv_kind == KV_F16) return launch_rows_d<KV_F16, false>(p, tmk, tmv, grid, stream);
     return p.q_bf16 ? launch_rows_d<KV_E4M3, true>(p, tmk, tmv, grid, stream)
                     : launch_rows_d<KV_E4M3, false>(p, tmk, tmv, grid, stream);

@@ -49,10 +49,12 @@ constexpr double kItemNs = 2500, kSplitNs = 1000, kMergeNs = 3000, kMergeRate = 
 
 // Time of one CTA for a tile of 128 tokens: its share of the memory's rate, or
 // what one and two row tiles measured (E4M3 codes are converted first).
-double tile_ns(const fd_problem &p, int row_tiles) {
+double tile_ns(const fd_problem &p, int row_tiles, int weight_parts) {
     const bool fp8 = p.kv_dtype == FD_E4M3;
+    // (two parts a weight, 4 x 2048 over 8192: 1.42 times at D = 128, 1.39 at D = 64)
+    const double parts = p.kv_dtype == FD_BF16 && weight_parts == 2 ? 1.4 : 1.0;
     const double bytes = 2.0 * kTile * p.D * (fp8 ? 1 : 2) / 44.0;
-    const double busy = (row_tiles == 2 ? (p.D == 128 ? 1450.0 : 1350.0) : (p.D == 128 ? 1000.0 : 800.0)) * (fp8 ? 1.5 : 1.0);
+    const double busy = (row_tiles == 2 ? (p.D == 128 ? 1450.0 : 1350.0) : (p.D == 128 ? 1000.0 : 800.0)) * (fp8 ? 1.5 : parts);
     return std::max(bytes, busy);
 }
 
@@ -62,7 +64,7 @@ template <typename TokensOf>
 fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int max_blocks, const int32_t *kv_lens,
                     const fd_cross_options &opt, TokensOf tokens_of, fd_cross_plan_t *plan) {
     if (opt.num_splits < 0 || opt.num_sms < 0 || opt.num_sms > kMaxRowSms || opt.max_kv_len < 0 || opt.timeout_us < 0 ||
-        opt.debug_stall_us < 0 || opt.debug_stall_us > 1000000)
+        opt.debug_stall_us < 0 || opt.debug_stall_us > 1000000 || opt.weight_parts < 1 || opt.weight_parts > 2)
         return FD_ERR_INVALID_ARG;
     if (p.out_dtype != p.q_dtype) return FD_ERR_UNSUPPORTED;
     if (p.Hq / p.Hkv > kMaxGroup) return FD_ERR_UNSUPPORTED;
@@ -118,8 +120,8 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
             for (int part = 0; part < 2; ++part) {
                 const double tiles = (part ? last : C) / (double)kTile;
                 const long long n = part ? 1 : ns - 1;
-                add(std::ceil(tiles) * tile_ns(p, 2) + more, n * whole);
-                if (rest) add(std::ceil(tiles) * tile_ns(p, rest > kTile ? 2 : 1) + more, n * p.Hkv);
+                add(std::ceil(tiles) * tile_ns(p, 2, opt.weight_parts) + more, n * whole);
+                if (rest) add(std::ceil(tiles) * tile_ns(p, rest > kTile ? 2 : 1, opt.weight_parts) + more, n * p.Hkv);
             }
         }
         if (items_out) *items_out = count;
@@ -170,7 +172,7 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
     plan->num_splits = (room + best - 1) / best;
     plan->chunk_tokens = best;
     plan->capacity_tokens = room;
-    plan->tile_rows = kItemRows;
+    plan->weight_parts = opt.weight_parts;
     plan->grid_ctas = (int)std::min<long long>(items, sms);
     plan->num_sms = sms;
     plan->timeout_us = opt.timeout_us;
@@ -208,6 +210,7 @@ fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pag
     rp.chunk = plan.chunk_tokens;
     rp.cap = plan.capacity_tokens;
     rp.q_bf16 = p.q_dtype == FD_BF16;
+    rp.weight_parts = plan.weight_parts;
     rp.kv_kind = p.kv_dtype == FD_F16 ? KV_F16 : (p.kv_dtype == FD_BF16 ? KV_BF16 : KV_E4M3);
     rp.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)p.D));
     rp.timeout_ns = plan.timeout_us > 0 ? (uint64_t)plan.timeout_us * 1000ull : kRowsTimeoutNs;
@@ -271,7 +274,8 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
             return false;
     }
     if (plan.capacity_tokens < 1 || plan.capacity_tokens > (long long)p.page_size * p.max_blocks_per_seq) return false;
-    return plan.timeout_us >= 0 && plan.debug_stall_us >= 0 && plan.debug_stall_us <= 1000000;
+    return plan.timeout_us >= 0 && plan.debug_stall_us >= 0 && plan.debug_stall_us <= 1000000 && plan.weight_parts >= 1 &&
+           plan.weight_parts <= 2;
 }
 
 bool pools_ok(const fd_problem &p, const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale) {
@@ -292,6 +296,9 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host, 
     fd_cross_options opt = {};
     if (options) opt = *options;
     if (opt.tokens < 0 || opt.beams < 0) return FD_ERR_INVALID_ARG;
+    // One bf16 part: a prompt's time is its products' (4 x 2048 queries over 8192
+    // states 740 us, with two 1032).
+    if (opt.weight_parts == 0) opt.weight_parts = 1;
     opt.tokens = std::max(1, opt.tokens);
     opt.beams = std::max(1, opt.beams);
     if (opt.beams > kMaxBeams || opt.tokens > kMaxTokens) return FD_ERR_UNSUPPORTED;
@@ -382,6 +389,9 @@ fd_status fd_plan_prefix(const fd_problem *problem, const int32_t *seq_lens_host
     po.out_dtype = FD_F32;  // a state that the other pass joins
     fd_status r = plan_state(&po, seq_lens_host, &own, 0, &plan->own);
     if (r != FD_OK) return r;
+    // Two bf16 parts, as in the decode of whole sequences (64 behind 8170 tokens 69 us,
+    // with one 66; 512 behind 32768 406 and 338).
+    if (opt.weight_parts == 0) opt.weight_parts = 2;
     opt.num_sms = own.num_sms;
     opt.timeout_us = own.timeout_us;
     const int T = std::max(1, own.q_len);

@@ -309,14 +309,17 @@ __device__ __forceinline__ bool warp_wait_item(Control &c, uint64_t &bar, uint32
     return true;
 }
 
-template <int KV, int D, bool QBF16>
+// PARTS: bf16 pools, bf16 parts of a weight.  One, as wide as the output, rounds a
+// weight to 8 bits; two (16 bits) cost a third product of the size of the first two.
+template <int KV, int D, bool QBF16, int PARTS>
 __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
     fd_rows_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv) {
     using Sh = RowsShape<KV, D>;
     constexpr bool FP8 = Sh::FP8;
     constexpr bool B16 = KV == KV_BF16;    // products in bf16 (else f16)
-    constexpr bool PAIR = FP8;             // bf16 weights (E4M3: chunks of wide scales) as pairs
+    constexpr bool PAIR = FP8 || PARTS == 2;  // bf16 weights (E4M3: chunks of wide scales) as pairs
+    static_assert(PARTS == 1 || B16, "parts of bf16 weights");
     constexpr bool QSCALE = FP8 && QBF16;  // query rows scaled into f16
     static_assert(FP8 || QBF16 == (KV == KV_BF16), "16-bit pools have q's type");
     constexpr int HALVES = Sh::HALVES, NST = Sh::STAGES;
@@ -946,7 +949,11 @@ __global__ void __launch_bounds__(RowsShape<KV, D>::THREADS, 1)
                 } else {
                     for (int k = 0; k < steps; ++k) mma_ts(d, a0 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, k > 0 || more);
                 }
-                if (PAIR && idesc_pv == idesc_bf16)  // the weights' low parts
+                if (PARTS == 2 && steps == kTileTokens / 16) {
+#pragma unroll
+                    for (int k = 0; k < kTileTokens / 16; ++k)
+                        mma_ts(d, a0 + 64 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, true);
+                } else if (PAIR && idesc_pv == idesc_bf16)  // the weights' low parts
                     for (int k = 0; k < steps; ++k) mma_ts(d, a0 + 64 + k * 8, b0 + k * (2 * Sh::GROUP >> 4), idesc_pv, true);
                 mma_commit(smem_u32(&c.pv_done[i]));
             }
