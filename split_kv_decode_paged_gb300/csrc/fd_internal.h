@@ -129,7 +129,6 @@ struct RowsParams {
     const int32_t *offsets;    // [kv_rows + 1], or null (beams sequences a KV row)
     const int32_t *block_table, *kv_lens;  // [kv_rows, max_blocks], [kv_rows]
     const float *k_scale, *v_scale;        // [num_pages, Hkv] or null
-    const void *k_pages, *v_pages;
     void *out;                 // [seqs, T, Hq, D]
     float *lse;                // [seqs, T, Hq] or null
     const float *own_out;      // [seqs, T, Hq, D] and [seqs, T, Hq]: a state over other

@@ -193,8 +193,6 @@ fd_status plan_rows(const fd_problem &p, int kv_rows, int seqs, int tokens, int 
 fd_status run_rows(const fd_cross_plan_t &plan, RowsParams rp, const void *k_pages, const void *v_pages,
                    uint8_t *workspace, void *stream) {
     const fd_problem &p = plan.problem;
-    rp.k_pages = k_pages;
-    rp.v_pages = v_pages;
     rp.kv_rows = plan.kv_rows;
     rp.seqs = plan.seqs;
     rp.T = plan.tokens;
