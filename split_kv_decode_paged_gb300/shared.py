@@ -20,6 +20,9 @@ class _Planned:
         self.device = torch.device(device)
         self.workspace = torch.zeros(max(256, int(self.plan.workspace_bytes)), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        if self.device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            # finish the fills before a call on another stream runs
+            torch.cuda.current_stream(self.device).synchronize()
 
     def check(self):
         """Synchronise the decoder's device and raise FdError if the device
@@ -43,7 +46,9 @@ class CrossDecoder(_Planned):
     not overlap on the GPU).
 
     problem.B counts KV rows (one per encoded input); beams sequences in a row
-    read each of them, tokens query tokens each."""
+    read each of them, tokens query tokens each.  Over bf16 pools the softmax
+    weights of many query rows have one bf16 part; weight_parts=2 gives them the
+    two of PagedDecoder."""
 
     def __init__(self, problem, kv_lens_host, tokens=1, beams=1, device="cuda", **plan_opts):
         self.problem = problem
@@ -93,7 +98,8 @@ class PrefixDecoder(_Planned):
     sequence's own tokens as in PagedDecoder, and the two are joined.
 
     prefix_of: for each sequence the index of its prefix, or -1 for none, in
-    any order.  regroup() changes it without a new plan."""
+    any order.  regroup() changes it without a new plan.  weight_parts=1 rounds
+    the softmax weights of bf16 prefixes to one bf16, which is faster."""
 
     def __init__(self, problem, seq_lens_host, prefix_max_blocks, prefix_lens_host, prefix_of, device="cuda",
                  **plan_opts):
