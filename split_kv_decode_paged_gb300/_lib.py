@@ -773,7 +773,7 @@ def fd_decode_paged_diff(plan: FdPlan, q, k_pages, v_pages, k_scale, v_scale, bl
 
 def _host_i32(entry, name, x, n):
     """Host int32 entries x (a tensor or sequence of n whole numbers)."""
-    t = torch.as_tensor(x)
+    t = torch.as_tensor(x, dtype=torch.int32) if isinstance(x, (list, tuple)) and not x else torch.as_tensor(x)
     if t.dim() != 1 or t.numel() != n or t.dtype.is_floating_point or t.dtype == torch.bool or t.dtype.is_complex:
         raise ValueError(f"{entry}: {name} must be {n} whole numbers")
     t = t.cpu().to(torch.int64)

@@ -129,7 +129,7 @@ class PrefixDecoder(_Planned):
     def _grouped(self, prefix_of):
         """(members, offsets) of fd_decode_paged_prefix, on the host."""
         of = _lib._host_i32("PrefixDecoder", "prefix_of", prefix_of, self.problem.B)
-        if int(of.min()) < -1 or int(of.max()) >= self.prefixes:
+        if of.numel() and (int(of.min()) < -1 or int(of.max()) >= self.prefixes):
             raise ValueError(f"PrefixDecoder: prefix_of must be -1 to {self.prefixes - 1}")
         key = torch.where(of < 0, self.prefixes, of)
         counts = torch.bincount(key, minlength=self.prefixes + 1)[:self.prefixes]

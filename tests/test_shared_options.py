@@ -6,7 +6,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
+import split_kv_decode_paged_gb300 as fd
 from split_kv_decode_paged_gb300 import _lib
 from tests.test_shared_args import INVALID, _raw_cross, code, problem
 
@@ -58,3 +60,15 @@ def test_layouts(tmp_path):
         cname, field, at = line.split()
         py = structs[cname]
         assert int(at) == (ctypes.sizeof(py) if field == "size" else getattr(py, field).offset), (cname, field)
+
+
+def test_empty_batches():
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16)
+    pages = torch.zeros(64, 16, 2, 128, dtype=torch.bfloat16)
+    table, ptable = torch.zeros(0, 8, dtype=torch.int32), torch.zeros(1, 8, dtype=torch.int32)
+    for lens in ([], torch.zeros(0, dtype=torch.int32)):
+        for make in (lambda: fd.CrossDecoder.for_pools(q, pages, pages, table, lens, num_sms=152),
+                     lambda: fd.PrefixDecoder.for_pools(q, pages, pages, ptable, [30], lens, table, lens, num_sms=152)):
+            with pytest.raises(fd.FdError) as e:
+                make()
+            assert e.value.code == INVALID
