@@ -29,7 +29,10 @@ constexpr uint64_t kOwnEndNs = 1000000ull;
 // heads a KV head): 4 rows 172, 203; 16 rows 178, 211; 24 rows 300, 214 (16 rows a
 // pass over K and V).  E4M3 (16 of 2048-16384 tokens, 8 heads), whose codes the
 // rows kernel converts for 128 rows whatever their number: 8 rows 58, 156; 32
-// rows 136, 156; 64 rows 263, 161.
+// rows 136, 156; 64 rows 263, 161.  2 to 64 sequences of 512 or 4096 tokens, D = 64
+// and 128: the decode kernel is the faster one up to both limits but for 32 E4M3
+// rows of 64 x 4096 tokens (143, 126; D = 64 99, 91) and 16 of 16 bits at D = 64 (64,
+// 63).
 constexpr int kFewRows = 16, kFewRowsE4m3 = 32;
 constexpr int kPlanCross = 2, kPlanPrefix = 3;      // fd_cross_plan_t::reserved[0]
 

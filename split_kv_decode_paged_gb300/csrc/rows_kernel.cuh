@@ -29,9 +29,9 @@
 // scale (O is multiplied by it at the end).  Where a chunk's scales differ by more
 // than kScaleRange, small ones times R^-1 would leave f16's normal range: V and
 // the weights are bf16 there, the weights as pairs (two products), so that what
-// other pages' scales are does not cost bits.  A bf16 query row enters times a power of two that brings its
-// largest element below 2^15 (elements down to 2^-31 of it are exact), undone on
-// the scores.
+// other pages' scales are does not cost bits.  A bf16 query row enters times a
+// power of two that brings its largest element below 2^15 (elements down to 2^-31
+// of it are exact), undone on the scores.
 // Every wait is bounded; one that runs out sets FD_DEV_TIMEOUT and its warp
 // leaves the loop, which ends the others' waits the same way.  The limit is for
 // what does not come, not for how long an item is: the query warps, which wait
@@ -39,12 +39,14 @@
 // and lists of counts read.
 //
 // Bounds, measured on GB300 (one pass among others).  D = 128, 16 bits, two row
-// tiles: the products, 4 x 2048 queries over 8192 states of 32/8 heads 729 us =
-// 1.51 PFLOP/s, 79% of a large library product's rate.  D = 64: the softmax, whose
-// work is the same for half of the products' (32 x 448 over 1500, 16 heads 136 us,
-// 0.65 PFLOP/s).  E4M3: the conversion, 1370 cycles for a tile of K or V.  Few
-// rows over long KV rows: memory (64 x 4 rows a KV head over 512-8192 states 201
-// us, 84% of the copy rate; the decode kernel, which takes such calls, 168).
+// tiles: the products, 4 x 2048 queries over 8192 states of 32/8 heads 735 us =
+// 1.50 PFLOP/s, 79% of a large library product's rate (two parts a weight 1032).
+// D = 64: the softmax, whose work is the same for half of the products' (32 x 448
+// over 1500, 16 heads 138 us, 0.64 PFLOP/s).  E4M3: the conversion, 1370 cycles for
+// a tile of K or V, of some 3850 for a pair of them; the softmax warps of these
+// instances spill 210 to 260 bytes at their 184 registers.  Few rows over long KV
+// rows: memory (64 x 4 rows a KV head over 512-8192 states 201 us, 84% of the copy
+// rate; the decode kernel, which takes such calls, 168).
 // Tiles of 128 rows and tokens: the largest whose scores and outputs, twice, fill
 // tensor memory; two of them, so that one's softmax hides the other's products.
 #pragma once
