@@ -649,11 +649,12 @@ fd_status fd_plan_cross(const fd_problem *problem, const int32_t *kv_lens_host,
  *   the pools, their scales, status_dev and stream as in fd_decode_paged.
  * K and V behind a row's length are not used, whatever they hold.  The weights
  * enter P.V rounded to the type of the product: bf16 pools weight_parts bf16 (8 or
- * 16 bits), f16 pools f16 (11 bits), E4M3 pools f16, but where V's scales differ by
- * more than a factor of 8 within a chunk of a row pairs of bf16 (16 bits).  The
- * decode kernel, which takes calls of few query rows (see fd_plan_cross), has pairs
- * over 16-bit pools whatever weight_parts says: with 1, and over f16 pools, a call
- * is more exact there than the same one with q_lens, a token stride or more rows. */
+ * 16 bits), f16 pools f16 (11 bits; those below 2^-24 of a row's largest may be 0),
+ * E4M3 pools f16 as well, but where V's scales differ by more than a factor of 8
+ * within a chunk of a row pairs of bf16 (16 bits).  The decode kernel, which takes
+ * calls of few query rows (see fd_plan_cross), has pairs over 16-bit pools whatever
+ * weight_parts says: with 1, and over f16 pools, a call is more exact there than
+ * the same one with q_lens, a token stride or more rows. */
 fd_status fd_cross_paged(const fd_cross_plan_t *plan, const void *q, long long q_stride,
                          const int32_t *q_lens, const void *k_pages, const void *v_pages,
                          const float *k_scale, const float *v_scale, const int32_t *block_table,

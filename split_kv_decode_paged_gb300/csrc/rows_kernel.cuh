@@ -42,7 +42,7 @@
 // tiles: the products, 4 x 2048 queries over 8192 states of 32/8 heads 735 us =
 // 1.50 PFLOP/s, 79% of a large library product's rate (two parts a weight 1032).
 // D = 64: the softmax, whose work is the same for half of the products' (32 x 448
-// over 1500, 16 heads 138 us, 0.64 PFLOP/s).  E4M3: the conversion, 1370 cycles for
+// over 1500, 16 heads 135 us, 0.65 PFLOP/s).  E4M3: the conversion, 1370 cycles for
 // a tile of K or V, of some 3850 for a pair of them; the softmax warps of these
 // instances spill 210 to 260 bytes at their 184 registers.  Few rows over long KV
 // rows: memory (64 x 4 rows a KV head over 512-8192 states 201 us, 84% of the copy
@@ -151,28 +151,29 @@ struct Segments {
     __device__ int tokens(int first, int end, bool &bad) const {
         if (!p.q_lens) return (end - first) * p.T;
         int n = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int b = first; b < end; ++b) n += q_len(b, bad);
         return n;
     }
     // by a whole warp
     __device__ int warp_tokens(int first, int end, bool &bad, int lane) const {
         int n = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int b = first + lane; b < end; b += 32) n += q_len(b, bad);
         return __reduce_add_sync(0xffffffffu, n);
     }
     // Whether a warp on every segment takes fewer rounds of loads than a thread on
-    // every one, eight loads a round, the threads' scattered ones twice as long: 8
-    // KV rows of 64 sequences with counts 14.5 us a call by warps, 17 by threads.
+    // every one, four loads a round, the threads' scattered ones twice as long: 8
+    // KV rows of 64 sequences with counts 16.6 us a call by warps, 19.4 by threads.
     __device__ bool by_warp(int segments, int warps, int threads) const {
-        return p.q_lens && (segments + warps - 1) / warps * ((p.beams + 255) >> 8) <
-                               2 * ((segments + threads - 1) / threads) * ((p.beams + 7) >> 3);
+        return p.q_lens && (segments + warps - 1) / warps * ((p.beams + 127) >> 7) <
+                               2 * ((segments + threads - 1) / threads) * ((p.beams + 3) >> 2);
     }
     // The q tokens (sequence * T + token) of a segment's query tokens n[0 .. 3]
     // (-1: none) of every lane, whose sequences are [first, end), by a whole warp:
     // the sums of 256 sequences at a time, running sums where one of n may be among
-    // them.
+    // them.  Its loops stay loops: unrolled, this code, which few calls reach, cost
+    // others 2% by its size alone (32 x 448 over 1500, D = 64, 134.4 -> 137.9 us).
     __device__ void find(int first, int end, const int (&n)[4], int (&q)[4], int lane, uint32_t *beat) const {
         int high = max(max(n[0], n[1]), max(n[2], n[3])), low = INT_MAX;
 #pragma unroll
@@ -191,7 +192,7 @@ struct Segments {
 #pragma unroll 1
             for (int b1 = b0; b1 < min(b0 + 8 * 32, end) && base <= high; b1 += 32) {
                 int incl = b1 + lane < end ? q_len(b1 + lane, bad) : 0;
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const int t = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += t;
@@ -202,7 +203,7 @@ struct Segments {
                     for (int k = 0; k < 4; ++k) {
                         const int left = n[k] - base;
                         int at = 0;  // the lane's sequence: the first whose running sum is above left
-#pragma unroll
+#pragma unroll 1
                         for (int o = 16; o > 0; o >>= 1)
                             if (__shfl_sync(0xffffffffu, incl, at + o - 1) <= left) at += o;
                         const int before = __shfl_sync(0xffffffffu, incl, max(at - 1, 0));
