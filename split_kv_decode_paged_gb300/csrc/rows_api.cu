@@ -255,7 +255,8 @@ bool plan_ok(const fd_cross_plan_t &plan, int kind) {
         return false;
     if (kind == kPlanCross && (plan.beams < 1 || (long long)plan.kv_rows * plan.beams != plan.seqs)) return false;
     // (chunks of at most 2^30 tokens: length + chunk - 1 stays within an int)
-    if (plan.chunk_tokens < kTile || plan.chunk_tokens > (1 << 30) || plan.chunk_tokens % kTile || plan.num_splits > kMaxRowSplits || plan.grid_ctas < 1 ||
+    if (plan.chunk_tokens < kTile || plan.chunk_tokens > (1 << 30) || plan.chunk_tokens % kTile ||
+        plan.num_splits > kMaxRowSplits || plan.grid_ctas < 1 ||
         plan.grid_ctas > kMaxRowSms ||
         plan.capacity_tokens > (long long)plan.num_splits * plan.chunk_tokens)
         return false;
